@@ -268,6 +268,80 @@ int moe_forward_fp8(const moe_config* cfg, int64_t T, const void* x, const void*
                     const void* ws_up, const void* ws_down, void* y, int32_t* topk_ids_out,
                     float* topk_weights_out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Grouped matrix products: the products an expert layer is made of, by themselves, with their gradients
+ * (for training such a layer) and in 8-bit integers (for serving it).  The grouped GEMM of [QA] Q8.3
+ * over the dispatch order of [DEEP] §10.2 Step 6; the pages give no sizes limits, gradients or 8-bit
+ * integer format for it, so these are stated here.
+ *
+ * A row space [0, max_rows) is cut into n_groups groups: group g is rows
+ * [group_offsets[g], group_offsets[g+1]) (int32, device, non-decreasing, from 0 to at most max_rows;
+ * NULL: one group of all max_rows rows, n_groups = 1).  Group g multiplies with its weight W[g] of
+ * W [n_groups, N, K] (nn.Linear [out, in] layout).  Groups may be empty or hold every row.  Rows at or
+ * beyond group_offsets[n_groups] are not computed.
+ *   dtype      MOE_BF16 or MOE_F32: the element type of x, dy and W.  Sums are held in fp32 (bf16 products
+ *              on v_mfma bf16, fp32 products in full fp32), each output rounded once.
+ *   *_dtype    MOE_BF16 or MOE_F32: the element type of the output
+ *   x_rows     rows x has; row_index NULL: x_rows >= max_rows and row r reads x[r]
+ *   row_index  [max_rows] int32 or NULL: row r reads x[row_index[r]], each in [0, x_rows) (others are
+ *              moved inside: they read no memory outside x, their results are unspecified)
+ * Sizes: any N, K from 1 to 2^20, any max_rows, 1 <= n_groups <= 4096; one group's weight and, with a
+ * row_index, all of x below 4 GiB (else MOE_ERR_UNSUPPORTED).  Matrices need only start on a boundary of
+ * their element size; those that start on 16 bytes and whose rows are multiples of 16 bytes run on the
+ * fast kernels.
+ * Infinities and NaN follow the sums they are part of: a value in one row (or group) never reaches the
+ * results of another.  Results are the same from call to call, bit for bit (no atomics).
+ * Workspace: moe_matmul_workspace_size() of the same sizes (it may be 0: then workspace may be NULL).
+ * Otherwise the conventions above (device pointers, streams, errors, no allocation) hold. */
+typedef enum {
+  MOE_MATMUL_FORWARD = 0, /* moe_grouped_matmul    */
+  MOE_MATMUL_DX = 1,      /* moe_grouped_matmul_dx */
+  MOE_MATMUL_DW = 2,      /* moe_grouped_matmul_dw */
+  MOE_MATMUL_I8 = 3       /* moe_matmul_i8 (dtype ignored) */
+} moe_matmul_op;
+size_t moe_matmul_workspace_size(int32_t op, int32_t dtype, int32_t n_groups, int64_t max_rows, int32_t N,
+                                 int32_t K);
+
+/* y[r, n] = sum_k x[row_index ? row_index[r] : r, k] * W[g(r), n, k]
+ *   x [x_rows, K], w [n_groups, N, K], y [max_rows, N] of y_dtype out */
+int moe_grouped_matmul(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
+                       int64_t max_rows, const void* x, int64_t x_rows, const int32_t* row_index, const void* w,
+                       void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient for the rows: dx[r, k] = sum_n dy[r, n] * W[g(r), n, k]
+ *   dy [max_rows, N], w [n_groups, N, K], dx [max_rows, K] of dx_dtype out
+ * Where the rows were gathered, a token's gradient is the sum over its rows: moe_combine with weights 1. */
+int moe_grouped_matmul_dx(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
+                          int64_t max_rows, const void* dy, const void* w, void* dx, int32_t dx_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient for the weights: dW[g, n, k] = sum over the rows r of group g of
+ * dy[r, n] * x[row_index ? row_index[r] : r, k]; an empty group's dW[g] is 0 (also with max_rows = 0).
+ *   dy [max_rows, N], x [x_rows, K], dw [n_groups, N, K] of dw_dtype out */
+int moe_grouped_matmul_dw(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
+                          int64_t max_rows, const void* dy, const void* x, int64_t x_rows,
+                          const int32_t* row_index, void* dw, int32_t dw_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Rows in 8-bit integers, one scale per row: with a_r = max_c |v[r, c]|,
+ *     scales[r] = a_r / 127,  codes[r, c] = rint(127 v[r, c] / a_r)  (ties to even; a_r = 0: codes 0)
+ * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up side by side, and
+ * v = SiLU(gate) * up in fp32.  A row with an infinity or NaN in v gets the scale NaN and codes 0.
+ *   x of x_dtype (MOE_BF16 or MOE_F32); codes [rows, cols] int8 out; scales [rows] fp32 out
+ * 1 <= cols <= 2^20.  No workspace. */
+int moe_quantize_rows(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, int8_t* codes,
+                      float* scales, void* stream);
+
+/* The grouped product of 8-bit integers with scales for each row and each output channel:
+ *     y[r, n] = x_scales[i] * w_scales[g(r), n] * sum_k x_codes[i, k] * w_codes[g(r), n, k],
+ *     i = row_index ? row_index[r] : r, the sum exact in int32 (K <= 131071)
+ *   x_codes [x_rows, K] int8, x_scales [x_rows] fp32, w_codes [n_groups, N, K] int8,
+ *   w_scales [n_groups, N] fp32, y [max_rows, N] of y_dtype out */
+int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets, int64_t max_rows,
+                  const int8_t* x_codes, const float* x_scales, int64_t x_rows, const int32_t* row_index,
+                  const int8_t* w_codes, const float* w_scales, void* y, int32_t y_dtype, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
 /* Message of the last failed call on this thread ("" if none); valid until the next call. */
 const char* moe_last_error(void);
 

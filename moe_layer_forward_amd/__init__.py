@@ -23,9 +23,13 @@ MOE_F32, MOE_BF16 = 0, 1
 (MOE_OP_ROUTE, MOE_OP_PERMUTE, MOE_OP_GROUPED_SWIGLU, MOE_OP_COMBINE, MOE_OP_FORWARD,
  MOE_OP_FORWARD_ROUTED, MOE_OP_FORWARD_Q4, MOE_OP_FORWARD_FP8) = range(8)
 
+MOE_MATMUL_FORWARD, MOE_MATMUL_DX, MOE_MATMUL_DW, MOE_MATMUL_I8 = range(4)
+
 EXPORTED = ("moe_workspace_size", "moe_route", "moe_permute", "moe_grouped_swiglu", "moe_combine", "moe_forward",
-            "moe_forward_noalloc", "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8", "moe_last_error",
-            "moe_profile_events", "moe_profile_count", "moe_profile_kernel")
+            "moe_forward_noalloc", "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8",
+            "moe_matmul_workspace_size", "moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
+            "moe_quantize_rows", "moe_matmul_i8", "moe_last_error", "moe_profile_events",
+            "moe_profile_count", "moe_profile_kernel")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20  # the fixed scratch of moe_forward_noalloc (include/moe.h)
 
 
@@ -80,6 +84,16 @@ def load_library():
         lib.moe_forward_routed.argtypes = [cfgp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         lib.moe_forward_q4.argtypes = [cfgp, i64] + [vp] * 17 + [sz, vp]
         lib.moe_forward_fp8.argtypes = [cfgp, i64] + [vp] * 17 + [sz, vp]
+        lib.moe_matmul_workspace_size.argtypes = [i32, i32, i32, i64, i32, i32]
+        lib.moe_matmul_workspace_size.restype = sz
+        lib.moe_grouped_matmul.argtypes = [i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i32, vp, sz, vp]
+        lib.moe_grouped_matmul_dx.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, vp, i32, vp, sz, vp]
+        lib.moe_grouped_matmul_dw.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, i32, vp, sz, vp]
+        lib.moe_quantize_rows.argtypes = [i32, i64, i32, i32, vp, vp, vp, vp]
+        lib.moe_matmul_i8.argtypes = [i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, i32, vp, sz, vp]
+        for name in ("moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw", "moe_quantize_rows",
+                     "moe_matmul_i8"):
+            getattr(lib, name).restype = ctypes.c_int
         for name in ("moe_route", "moe_permute", "moe_grouped_swiglu", "moe_combine", "moe_forward",
                      "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8"):
             getattr(lib, name).restype = ctypes.c_int
@@ -326,6 +340,195 @@ def moe_forward_fp8(cfg, x, w_router, f8, ws_gate=None, ws_up=None, ws_down=None
     uint8 OCP E4M3 [E, N, K], scales float32 [E, N/128, K/128]; layouts as in include/moe.h)."""
     return _forward_quant("moe_forward_fp8", MOE_OP_FORWARD_FP8, (1, 4), cfg, x, w_router, f8, ws_gate, ws_up,
                           ws_down, score_bias, logit_offset, return_routing, workspace, out)
+
+
+# --------------------------------------------------------------------------- grouped matrix products
+def _matmul_dtype(t, what):
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_F32
+    raise ValueError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _want(t, what, shape, dtype=None):
+    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be {tuple(shape)}{f' {dtype}' if dtype is not None else ''}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+
+
+def _groups(group_offsets, row_index, G):
+    """Check the int32 vectors of a grouped product (group_offsets None: one group)."""
+    import torch
+
+    if group_offsets is None:
+        if G != 1:
+            raise ValueError(f"group_offsets is required for {G} groups")
+    else:
+        _want(group_offsets, "group_offsets", (G + 1,), torch.int32)
+    if row_index is not None and (row_index.dim() != 1 or row_index.dtype != torch.int32):
+        raise ValueError(f"row_index must be a vector of int32, got {tuple(row_index.shape)} {row_index.dtype}")
+
+
+def _out(out, shape, dtype, default, dev):
+    """The output tensor and its moe dtype: out as given (dtype then names its type, if given), or a new one."""
+    import torch
+
+    if out is None:
+        want = default if dtype is None else dtype
+        if want not in (MOE_F32, MOE_BF16):
+            raise ValueError(f"the output dtype must be MOE_F32 or MOE_BF16, got {want}")
+        return torch.empty(shape, dtype=torch.bfloat16 if want == MOE_BF16 else torch.float32, device=dev), want
+    got = _matmul_dtype(out, "out")
+    if dtype is not None and dtype != got:
+        raise ValueError("out has another type than the output dtype asked for")
+    _want(out, "out", shape)
+    return out, got
+
+
+def _one_device(*tensors):
+    """The tensors' device and its current stream; every tensor must be there."""
+    dev, stream = _dev(*tensors)
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"moe: tensors on {t.device} and {dev}")
+    return dev, stream
+
+
+def moe_matmul_workspace_size(op: int, dtype: int, n_groups: int, max_rows: int, N: int, K: int) -> int:
+    n = load_library().moe_matmul_workspace_size(op, dtype, n_groups, max_rows, N, K)
+    if n == 0 and moe_last_error():
+        raise MoeError(MOE_ERR_INVALID_ARG, moe_last_error())
+    return int(n)
+
+
+def _matmul_ws(workspace, op, dtype, G, rows, N, K, dev):
+    """(tensor or None, bytes): the caller's workspace, or a new one of the size the call needs."""
+    import torch
+
+    if workspace is not None:
+        return workspace, workspace.numel() * workspace.element_size()
+    n = moe_matmul_workspace_size(op, dtype, G, rows, N, K)
+    return (torch.empty(n, dtype=torch.uint8, device=dev), n) if n else (None, 0)
+
+
+def _launch(dev, call):
+    """call() with dev current (a stream belongs to its device)."""
+    import torch
+
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(call())
+    else:
+        with torch.cuda.device(dev):
+            _check(call())
+
+
+def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, workspace=None, out=None):
+    """Product of ragged row groups with their group's weight: y[r] = W[g(r)] x[row_index[r] or r].
+
+    x [x_rows, K] and w [G, N, K] of one type (bfloat16 or float32), group_offsets [G + 1] int32 (None:
+    one group of all rows), row_index [rows] int32 or None (then the rows are x's).  Returns y [rows, N] of
+    x's type, or of y_dtype (MOE_BF16, MOE_F32).  Rows past group_offsets[G] are not written."""
+    dt = _matmul_dtype(x, "x")
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [rows, K] and w [G, N, K]")
+    G, N, K = w.shape
+    _want(w, "w", (G, N, x.shape[1]), x.dtype)
+    _groups(group_offsets, row_index, G)
+    rows = x.shape[0] if row_index is None else row_index.shape[0]
+    dev, stream = _one_device(x, w, group_offsets, row_index, workspace, out)
+    y, ydt = _out(out, (rows, N), y_dtype, dt, dev)
+    ws, nb = _matmul_ws(workspace, MOE_MATMUL_FORWARD, dt, G, rows, N, K, dev)
+    _launch(dev, lambda: load_library().moe_grouped_matmul(dt, G, N, K, _ptr(group_offsets), rows, _ptr(x), x.shape[0],
+                                                           _ptr(row_index), _ptr(w), _ptr(y), ydt, _ptr(ws), nb,
+                                                           stream))
+    return y
+
+
+def moe_grouped_matmul_dx(dy, w, group_offsets, dx_dtype=None, workspace=None, out=None):
+    """Gradient of moe_grouped_matmul for its rows: dx[r] = W[g(r)]^T dy[r], dy [rows, N] -> dx [rows, K]
+    (one row per row of dy; where the forward gathered rows, sum them per token with moe_combine, weights 1)."""
+    dt = _matmul_dtype(dy, "dy")
+    if dy.dim() != 2 or w.dim() != 3:
+        raise ValueError("dy must be [rows, N] and w [G, N, K]")
+    G, N, K = w.shape
+    _want(w, "w", (G, dy.shape[1], K), dy.dtype)
+    _groups(group_offsets, None, G)
+    rows = dy.shape[0]
+    dev, stream = _one_device(dy, w, group_offsets, workspace, out)
+    dx, odt = _out(out, (rows, K), dx_dtype, dt, dev)
+    ws, nb = _matmul_ws(workspace, MOE_MATMUL_DX, dt, G, rows, N, K, dev)
+    _launch(dev, lambda: load_library().moe_grouped_matmul_dx(dt, G, N, K, _ptr(group_offsets), rows, _ptr(dy), _ptr(w),
+                                                              _ptr(dx), odt, _ptr(ws), nb, stream))
+    return dx
+
+
+def moe_grouped_matmul_dw(dy, x, group_offsets, row_index=None, dw_dtype=None, workspace=None, out=None):
+    """Gradient of moe_grouped_matmul for its weights: dW[g] = sum over group g's rows of dy[r]^T x[row], with
+    dy [rows, N] and x [x_rows, K] -> dW [G, N, K] (zeros for an empty group)."""
+    dt = _matmul_dtype(dy, "dy")
+    if dy.dim() != 2 or x.dim() != 2 or x.dtype != dy.dtype:
+        raise ValueError("dy must be [rows, N] and x [x_rows, K] of one type")
+    G = 1 if group_offsets is None else group_offsets.shape[0] - 1
+    _groups(group_offsets, row_index, G)
+    (rows, N), (x_rows, K) = dy.shape, x.shape
+    if (x_rows if row_index is None else row_index.shape[0]) != rows:
+        raise ValueError(f"dy has {rows} rows, x (or row_index) {x_rows if row_index is None else row_index.shape[0]}")
+    dev, stream = _one_device(dy, x, group_offsets, row_index, workspace, out)
+    dw, odt = _out(out, (G, N, K), dw_dtype, dt, dev)
+    ws, nb = _matmul_ws(workspace, MOE_MATMUL_DW, dt, G, rows, N, K, dev)
+    _launch(dev, lambda: load_library().moe_grouped_matmul_dw(dt, G, N, K, _ptr(group_offsets), rows, _ptr(dy), _ptr(x),
+                                                              x_rows, _ptr(row_index), _ptr(dw), odt, _ptr(ws), nb,
+                                                              stream))
+    return dw
+
+
+def moe_quantize_rows(x, swiglu=False, codes=None, scales=None):
+    """Rows in 8-bit integers with one scale per row: returns (codes int8 [rows, cols], scales float32 [rows]),
+    x ~ codes * scales[:, None].  swiglu: x is [rows, 2 cols], gate | up, and SiLU(gate) * up is quantized."""
+    import torch
+
+    dt = _matmul_dtype(x, "x")
+    if x.dim() != 2 or (swiglu and x.shape[1] % 2):
+        raise ValueError("x must be [rows, cols] (swiglu: [rows, 2 cols])")
+    rows, cols = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
+    dev, stream = _one_device(x, codes, scales)
+    codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    scales = scales if scales is not None else torch.empty(rows, dtype=torch.float32, device=dev)
+    _want(codes, "codes", (rows, cols), torch.int8)
+    _want(scales, "scales", (rows,), torch.float32)
+    _launch(dev, lambda: load_library().moe_quantize_rows(dt, rows, cols, int(bool(swiglu)), _ptr(x), _ptr(codes),
+                                                          _ptr(scales), stream))
+    return codes, scales
+
+
+def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_index=None, y_dtype=MOE_BF16,
+                  workspace=None, out=None):
+    """Grouped product of 8-bit integers with scales for each row and output channel:
+    y[r, n] = x_scales[i] w_scales[g, n] sum_k x_codes[i, k] w_codes[g, n, k], i = row_index[r] or r.
+
+    x_codes [x_rows, K] int8, x_scales [x_rows] float32 (moe_quantize_rows), w_codes [G, N, K] int8,
+    w_scales [G, N] float32; group_offsets None: one group.  Returns y [rows, N] of y_dtype."""
+    import torch
+
+    if x_codes.dim() != 2 or w_codes.dim() != 3:
+        raise ValueError("x_codes must be [rows, K] and w_codes [G, N, K]")
+    G, N, K = w_codes.shape
+    _want(x_codes, "x_codes", (x_codes.shape[0], K), torch.int8)
+    _want(w_codes, "w_codes", (G, N, K), torch.int8)
+    _want(x_scales, "x_scales", (x_codes.shape[0],), torch.float32)
+    _want(w_scales, "w_scales", (G, N), torch.float32)
+    _groups(group_offsets, row_index, G)
+    rows = x_codes.shape[0] if row_index is None else row_index.shape[0]
+    dev, stream = _one_device(x_codes, x_scales, w_codes, w_scales, group_offsets, row_index, workspace, out)
+    y, ydt = _out(out, (rows, N), y_dtype if out is None else None, MOE_BF16, dev)
+    ws, nb = _matmul_ws(workspace, MOE_MATMUL_I8, MOE_F32, G, rows, N, K, dev)
+    _launch(dev, lambda: load_library().moe_matmul_i8(G, N, K, _ptr(group_offsets), rows, _ptr(x_codes), _ptr(x_scales),
+                                                      x_codes.shape[0], _ptr(row_index), _ptr(w_codes), _ptr(w_scales),
+                                                      _ptr(y), ydt, _ptr(ws), nb, stream))
+    return y
 
 
 def moe_profile_events(events_array, n_events: int):

@@ -1,0 +1,219 @@
+// Building blocks of the grouped matrix products (gmm_any.hip, gmm_tile.hip): element types, LDS
+// stages and fragments, and the mapping of row tiles to groups.
+//
+// The products, over groups of rows [off[g], off[g+1]) and weights W [G, N, K]:
+//   NT  y[r, n]     = sum_k x[idx(r), k] W[g(r), n, k]     contraction K: contiguous in x and in W
+//   NN  dx[r, k]    = sum_n dy[r, n] W[g(r), n, k]         contraction N: contiguous in dy, a row index of W
+//   TN  dW[g, n, k] = sum_{r in g} dy[r, n] x[idx(r), k]   contraction r: a row index of both
+//
+// In every form the output tile is P rows x Q columns: the P operand gives the output's rows (x or dy
+// rows; for TN the columns of dy), the Q operand its columns, which are contiguous in memory (W rows;
+// for NN and TN the columns of W and of x).  One step of the contraction is 128 bytes of each operand
+// row whatever the type: 64 bf16, 128 int8 or 32 fp32 values, so that one LDS stage, one 16-byte
+// fragment read and one swizzle serve the three types:
+//   * bf16: v_mfma_f32_16x16x32_bf16, lane l holds k = 8 (l / 16) .. + 7 of row l % 16
+//   * int8: v_mfma_i32_16x16x64_i8, lane l holds k = 16 (l / 16) .. + 15 of row l % 16, exact int32 sums
+//   * fp32: four v_mfma_f32_16x16x4_f32 (full fp32 products), the t-th taking element t of each lane's
+//     four: k = 4 (l / 16) + t.  Both operands use the same order, so the sum is over the same k.
+// The Q fragment is the MFMA's first operand, so lane l, element e of a 16 x 16 accumulator block is
+// output row l % 16, column 4 (l / 16) + e: four consecutive columns per lane.
+#pragma once
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace moe {
+
+typedef uint32_t gmm_u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t gmm_i32x4 __attribute__((ext_vector_type(4)));
+
+struct GmmBf16 {
+  typedef f32x4 Acc;
+  static constexpr int kBytes = 2;
+  __device__ static __forceinline__ Acc mfma(gmm_u32x4 q, gmm_u32x4 p, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, q), __builtin_bit_cast(bf16x8, p), c, 0,
+                                                   0, 0);
+  }
+};
+
+struct GmmI8 {
+  typedef gmm_i32x4 Acc;
+  static constexpr int kBytes = 1;
+  __device__ static __forceinline__ Acc mfma(gmm_u32x4 q, gmm_u32x4 p, Acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(gmm_i32x4, q), __builtin_bit_cast(gmm_i32x4, p), c,
+                                                 0, 0, 0);
+  }
+};
+
+struct GmmF32 {
+  typedef f32x4 Acc;
+  static constexpr int kBytes = 4;
+  __device__ static __forceinline__ Acc mfma(gmm_u32x4 q, gmm_u32x4 p, Acc c) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(q[t]), __uint_as_float(p[t]), c, 0, 0, 0);
+    return c;
+  }
+};
+
+constexpr int kGmmStepBytes = 128;  // bytes of an operand row per contraction step
+
+// LDS stage of an operand whose rows run along the contraction: OUTER rows of 128 bytes, 16-byte chunk c
+// of row r at c ^ ((r >> 1) & 7), so that the 16 rows of one fragment read fall in 16 bank groups.
+template <class T, int OUTER>
+struct GmmAlong {
+  static constexpr bool kAlong = true;
+  static constexpr int kChunks = 8;  // 16-byte chunks per row
+  static constexpr int kRows = OUTER;
+  static constexpr int kStageBytes = OUTER * kGmmStepBytes;
+  __device__ static __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+  __device__ static __forceinline__ int pos(int r, int c) { return r * kGmmStepBytes + ((c ^ swz(r)) << 4); }
+  // Per-lane byte offsets of a fragment read inside a 16-row block (block b at b * 2048).
+  struct Lane {
+    int off[2];
+  };
+  __device__ static __forceinline__ Lane lane() {
+    const int l = threadIdx.x & 63, x = l & 15, g = l >> 4;
+    return Lane{{pos(x, g), pos(x, 4 + g)}};
+  }
+  // Fragment of the 16-row block b for contraction half kk of the step.
+  __device__ static __forceinline__ gmm_u32x4 frag(const char* st, const Lane& ln, int b, int kk) {
+    return *reinterpret_cast<const gmm_u32x4*>(st + b * 16 * kGmmStepBytes + ln.off[kk]);
+  }
+};
+
+// LDS stage of an operand whose rows run across the contraction: one row per contraction index (64 bf16
+// or 32 fp32 of them), OUTER columns wide.
+//   bf16: a fragment is two ds_read_b64_tr_b16.  Each transposes a 4 x 16 block per 16 lanes: lane i
+//     names 4 columns (i % 4) of row i / 4 and receives column i of the 4 rows.  The 16 columns of a
+//     block are one 32-byte unit; unit u of row r sits at u ^ s(r), s = (r & 3) | (r >> 1 & 4), so that
+//     the 8 rows x 32 bytes that 32 lanes read fall in all 64 banks.
+//   fp32: a fragment is four 4-byte reads (element t from row 4 (l / 16) + t); the 16 columns are one
+//     64-byte unit, at u ^ (r >> 2 & 3), so that the four rows of one read fall in all 64 banks.
+template <class T, int OUTER>
+struct GmmAcross {
+  static constexpr bool kAlong = false;
+  static constexpr int kRows = kGmmStepBytes / T::kBytes;
+  static constexpr int kRowBytes = OUTER * T::kBytes;
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kStageBytes = kRows * kRowBytes;
+  static constexpr int kUnit = 16 * T::kBytes;  // bytes of 16 columns
+  static_assert(T::kBytes == 2 || T::kBytes == 4, "types");
+  __device__ static __forceinline__ int swz(int r) {
+    return T::kBytes == 2 ? (r & 3) | ((r >> 1) & 4) : (r >> 2) & 3;
+  }
+  // chunk that belongs at chunk position p of row r, and (the same involution) the position of chunk c
+  __device__ static __forceinline__ int chunk_at(int r, int p) {
+    constexpr int kSub = kUnit / 16;
+    return ((p / kSub) ^ swz(r)) * kSub + p % kSub;
+  }
+  __device__ static __forceinline__ int pos(int r, int c) { return r * kRowBytes + (chunk_at(r, c) << 4); }
+  struct Lane {
+    int row;  // byte offset of the lane's first row, plus its place inside a unit
+    int s;    // its swizzle
+  };
+  __device__ static __forceinline__ Lane lane() {
+    const int l = threadIdx.x & 63, i = l & 15, g = l >> 4;
+    if constexpr (T::kBytes == 2) {
+      const int r = 8 * g + (i >> 2);
+      return Lane{r * kRowBytes + (i & 3) * 8, swz(r)};
+    } else {
+      return Lane{4 * g * kRowBytes + i * 4, swz(4 * g)};
+    }
+  }
+  __device__ static __forceinline__ gmm_u32x4 frag(const char* st, const Lane& ln, int b, int kk) {
+    const char* p = st + ln.row + ((b ^ ln.s) * kUnit) + kk * (kRows / 2) * kRowBytes;
+    if constexpr (T::kBytes == 2) {
+#if defined(__HIP_DEVICE_COMPILE__)
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      typedef __attribute__((address_space(3))) s16x4* Ptr;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(p)));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(p + 4 * kRowBytes)));
+      return gmm_u32x4{lo[0], lo[1], hi[0], hi[1]};
+#else
+      return gmm_u32x4{};
+#endif
+    } else {
+      gmm_u32x4 v;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) v[t] = *reinterpret_cast<const uint32_t*>(p + t * kRowBytes);
+      return v;
+    }
+  }
+};
+
+template <GmmForm F, class T, int OUTER>
+using GmmP = std::conditional_t<F == GmmForm::kTN, GmmAcross<T, OUTER>, GmmAlong<T, OUTER>>;
+template <GmmForm F, class T, int OUTER>
+using GmmQ = std::conditional_t<F == GmmForm::kNT, GmmAlong<T, OUTER>, GmmAcross<T, OUTER>>;
+
+// Rows [beg, end) of group g, kept inside [0, max_rows] whatever the offsets hold (null: one group of
+// all rows).
+__device__ __forceinline__ void gmm_group_rows(const int32_t* off, int64_t max_rows, int g, int64_t& beg,
+                                               int64_t& end) {
+  beg = off ? off[g] : 0;
+  end = off ? off[g + 1] : max_rows;
+  beg = beg < 0 ? 0 : beg > max_rows ? max_rows : beg;
+  end = end < beg ? beg : end > max_rows ? max_rows : end;
+}
+
+// The t-th row tile of bm rows, counting every group's tiles in group order: its group and rows.  Every
+// wave of the work-group finds it by itself: lane l sums the tile counts of ceil(G / 64) consecutive
+// groups, a scan over the lanes finds the lane, and the wave walks that lane's groups.  No plan launch
+// and no workspace; G = 384 costs six loads per lane.  False past the last tile.
+__device__ __forceinline__ bool gmm_find_tile(const int32_t* off, int G, int64_t max_rows, int bm, int64_t t, int& g,
+                                              int64_t& beg, int64_t& end) {
+  if (!off || G == 1) {
+    g = 0;
+    gmm_group_rows(off, max_rows, 0, beg, end);
+    beg += t * bm;
+    if (beg >= end) return false;
+    end = beg + bm < end ? beg + bm : end;
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  const int per = (G + 63) / 64;
+  int n = 0;
+  for (int j = 0; j < per; ++j) {
+    const int gg = lane * per + j;
+    if (gg < G) {
+      int64_t b, e;
+      gmm_group_rows(off, max_rows, gg, b, e);
+      n += (int)((e - b + bm - 1) / bm);
+    }
+  }
+  int incl = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += v;
+  }
+  const uint64_t past = __ballot((int64_t)incl > t);
+  if (!past) return false;
+  const int owner = __ffsll((unsigned long long)past) - 1;
+  int64_t rel = t - __shfl(incl - n, owner, 64);
+  for (int j = 0; j < per; ++j) {
+    const int gg = owner * per + j;
+    if (gg >= G) return false;
+    int64_t b, e;
+    gmm_group_rows(off, max_rows, gg, b, e);
+    const int64_t tiles = (e - b + bm - 1) / bm;
+    if (rel < tiles) {
+      g = __builtin_amdgcn_readfirstlane(gg);
+      beg = b + rel * bm;
+      end = beg + bm < e ? beg + bm : e;
+      return true;
+    }
+    rel -= tiles;
+  }
+  return false;
+}
+
+// Most row tiles of bm rows that G groups over max_rows rows can have.
+inline int64_t gmm_max_tiles(int64_t max_rows, int G, int bm) {
+  const int64_t full = max_rows / bm + G;
+  return full < max_rows ? full : max_rows;
+}
+
+}  // namespace moe

@@ -530,6 +530,53 @@ int forward_quant(const char* name, const moe_config* cfg, int64_t T, const void
   return device_status(e, "combine");
 }
 
+// ----------------------------------------------------------------------------- grouped matrix products
+constexpr int32_t kMaxMatmulSide = 1 << 20;
+constexpr int32_t kMaxI8Depth = 131071;  // 128 * 128 * K < 2^31
+
+// Checks that the product calls share.  need_x / need_w: the operands the form reads.
+int check_matmul(const char* fn, const moe::GmmArgs& a, int32_t out_dtype) {
+  using moe::GmmForm;
+  using moe::GmmType;
+  const int64_t e = a.type == GmmType::kI8 ? 1 : a.type == GmmType::kBf16 ? 2 : 4;
+  if (a.G < 1 || a.G > kMaxGroups) return fail(MOE_ERR_INVALID_ARG, "%s: n_groups must be in [1, %d]", fn, kMaxGroups);
+  if (a.N < 1 || a.K < 1) return fail(MOE_ERR_INVALID_ARG, "%s: N and K must be positive (N=%d K=%d)", fn, a.N, a.K);
+  if (a.max_rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative max_rows", fn);
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: output dtype %d", fn, out_dtype);
+  if (a.max_rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: max_rows exceeds 2^31-1", fn);
+  if (a.N > kMaxMatmulSide || a.K > kMaxMatmulSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: N and K must be at most %d", fn, kMaxMatmulSide);
+  if (a.type == GmmType::kI8 && a.K > kMaxI8Depth)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: K must be at most %d for exact int32 sums", fn, kMaxI8Depth);
+  if ((int64_t)a.N * a.K * e >= (int64_t(1) << 32))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weight must stay below 4 GiB", fn);
+  if (!a.group_offsets && a.G != 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: group_offsets may be NULL for one group only", fn);
+  if (a.form != GmmForm::kNN) {
+    if (a.x_rows < 0 || (a.row_index ? a.x_rows == 0 && a.max_rows > 0 : a.x_rows < a.max_rows))
+      return fail(MOE_ERR_INVALID_ARG, "%s: x has too few rows (%lld)", fn, (long long)a.x_rows);
+    if (a.x_rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: x_rows exceeds 2^31-1", fn);
+    if (a.row_index && a.x_rows * a.K * e >= (int64_t(1) << 32))
+      return fail(MOE_ERR_UNSUPPORTED, "%s: a gathered x must stay below 4 GiB", fn);
+  }
+  if (!moe::gmm_grid_ok(a)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many output tiles for one launch", fn);
+  return MOE_OK;
+}
+
+int matmul_type(const char* fn, int32_t dtype, moe::GmmType* t) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: dtype %d", fn, dtype);
+  *t = dtype == MOE_BF16 ? moe::GmmType::kBf16 : moe::GmmType::kF32;
+  return MOE_OK;
+}
+
+int run_matmul(const char* fn, const char* kernel, const moe::GmmArgs& a, void* workspace, size_t workspace_bytes,
+               void* stream) {
+  const int st = check_ws(workspace, workspace_bytes, moe::gmm_workspace(a));
+  if (st) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return device_status(timed(kernel, s, [&] { return moe::launch_gmm(a, workspace, s); }), fn);
+}
+
 // ----------------------------------------------------------------------------- no-allocation forward
 // Scratch of moe_forward_noalloc: a file-scope device array that every GPU the library runs on holds
 // (its own copy, at its own address) until the process ends.  In host code `scratch` names a host
@@ -854,6 +901,173 @@ int moe_forward_fp8(const moe_config* cfg, int64_t T, const void* x, const void*
   const moe::QWeights qw{moe::QFormat::kFp8, gate_codes, gate_scales, up_codes, up_scales, down_codes, down_scales};
   return forward_quant("moe_forward_fp8", cfg, T, x, w_router, score_bias, logit_offset, qw, ws_gate, ws_up, ws_down,
                        y, topk_ids_out, topk_weights_out, workspace, workspace_bytes, stream);
+}
+
+size_t moe_matmul_workspace_size(int32_t op, int32_t dtype, int32_t n_groups, int64_t max_rows, int32_t N,
+                                 int32_t K) {
+  const char* fn = "moe_matmul_workspace_size";
+  moe::GmmArgs a{};
+  if (op < MOE_MATMUL_FORWARD || op > MOE_MATMUL_I8) {
+    fail(MOE_ERR_INVALID_ARG, "%s: unknown op %d", fn, op);
+    return 0;
+  }
+  a.form = op == MOE_MATMUL_DX ? moe::GmmForm::kNN : op == MOE_MATMUL_DW ? moe::GmmForm::kTN : moe::GmmForm::kNT;
+  a.type = moe::GmmType::kI8;
+  if (op != MOE_MATMUL_I8 && matmul_type(fn, dtype, &a.type)) return 0;
+  a.G = n_groups;
+  a.N = N;
+  a.K = K;
+  a.max_rows = a.x_rows = max_rows;
+  static const int32_t some_offsets[1] = {0};  // any grouping: never read here
+  a.group_offsets = some_offsets;
+  if (check_matmul(fn, a, MOE_F32)) return 0;
+  ok();
+  return moe::gmm_workspace(a);
+}
+
+int moe_grouped_matmul(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
+                       int64_t max_rows, const void* x, int64_t x_rows, const int32_t* row_index, const void* w,
+                       void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  prof_reset();
+  const char* fn = "moe_grouped_matmul";
+  moe::GmmArgs a{};
+  int st = matmul_type(fn, dtype, &a.type);
+  if (st) return st;
+  a.form = moe::GmmForm::kNT;
+  a.G = n_groups;
+  a.N = N;
+  a.K = K;
+  a.group_offsets = group_offsets;
+  a.max_rows = max_rows;
+  a.x = x;
+  a.x_rows = x_rows;
+  a.row_index = row_index;
+  a.w = w;
+  a.out = y;
+  a.out_bf16 = y_dtype == MOE_BF16;
+  if ((st = check_matmul(fn, a, y_dtype))) return st;
+  if (max_rows == 0) return ok();
+  if (!x || !w || !y) return fail(MOE_ERR_INVALID_ARG, "%s: x, w and y are required", fn);
+  if ((st = check_aligned(fn, {{group_offsets, 4, "group_offsets"}, {row_index, 4, "row_index"},
+                               {x, elem_bytes(dtype), "x"}, {w, elem_bytes(dtype), "w"},
+                               {y, elem_bytes(y_dtype), "y"}})))
+    return st;
+  return run_matmul(fn, "grouped_matmul", a, workspace, workspace_bytes, stream);
+}
+
+int moe_grouped_matmul_dx(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
+                          int64_t max_rows, const void* dy, const void* w, void* dx, int32_t dx_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  prof_reset();
+  const char* fn = "moe_grouped_matmul_dx";
+  moe::GmmArgs a{};
+  int st = matmul_type(fn, dtype, &a.type);
+  if (st) return st;
+  a.form = moe::GmmForm::kNN;
+  a.G = n_groups;
+  a.N = N;
+  a.K = K;
+  a.group_offsets = group_offsets;
+  a.max_rows = max_rows;
+  a.dy = dy;
+  a.w = w;
+  a.out = dx;
+  a.out_bf16 = dx_dtype == MOE_BF16;
+  if ((st = check_matmul(fn, a, dx_dtype))) return st;
+  if (max_rows == 0) return ok();
+  if (!dy || !w || !dx) return fail(MOE_ERR_INVALID_ARG, "%s: dy, w and dx are required", fn);
+  if ((st = check_aligned(fn, {{group_offsets, 4, "group_offsets"}, {dy, elem_bytes(dtype), "dy"},
+                               {w, elem_bytes(dtype), "w"}, {dx, elem_bytes(dx_dtype), "dx"}})))
+    return st;
+  return run_matmul(fn, "grouped_matmul_dx", a, workspace, workspace_bytes, stream);
+}
+
+int moe_grouped_matmul_dw(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
+                          int64_t max_rows, const void* dy, const void* x, int64_t x_rows,
+                          const int32_t* row_index, void* dw, int32_t dw_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  prof_reset();
+  const char* fn = "moe_grouped_matmul_dw";
+  moe::GmmArgs a{};
+  int st = matmul_type(fn, dtype, &a.type);
+  if (st) return st;
+  a.form = moe::GmmForm::kTN;
+  a.G = n_groups;
+  a.N = N;
+  a.K = K;
+  a.group_offsets = group_offsets;
+  a.max_rows = max_rows;
+  a.x = x;
+  a.x_rows = x_rows;
+  a.row_index = row_index;
+  a.dy = dy;
+  a.out = dw;
+  a.out_bf16 = dw_dtype == MOE_BF16;
+  if ((st = check_matmul(fn, a, dw_dtype))) return st;
+  if (!dw || (max_rows > 0 && (!dy || !x)))  // no rows: dw is still written, with zeros
+    return fail(MOE_ERR_INVALID_ARG, "%s: dy, x and dw are required", fn);
+  if ((st = check_aligned(fn, {{group_offsets, 4, "group_offsets"}, {row_index, 4, "row_index"},
+                               {dy, elem_bytes(dtype), "dy"}, {x, elem_bytes(dtype), "x"},
+                               {dw, elem_bytes(dw_dtype), "dw"}})))
+    return st;
+  return run_matmul(fn, "grouped_matmul_dw", a, workspace, workspace_bytes, stream);
+}
+
+int moe_quantize_rows(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, int8_t* codes,
+                      float* scales, void* stream) {
+  prof_reset();
+  const char* fn = "moe_quantize_rows";
+  moe::GmmType t;
+  int st = matmul_type(fn, x_dtype, &t);
+  if (st) return st;
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative rows", fn);
+  if (cols < 1) return fail(MOE_ERR_INVALID_ARG, "%s: cols must be positive", fn);
+  if (swiglu != 0 && swiglu != 1) return fail(MOE_ERR_INVALID_ARG, "%s: swiglu must be 0 or 1", fn);
+  if (cols > kMaxMatmulSide) return fail(MOE_ERR_UNSUPPORTED, "%s: cols must be at most %d", fn, kMaxMatmulSide);
+  if (rows > (1 << 23)) return fail(MOE_ERR_UNSUPPORTED, "%s: rows must be at most 2^23", fn);
+  if (rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "%s: x, codes and scales are required", fn);
+  if ((st = check_aligned(fn, {{x, elem_bytes(x_dtype), "x"}, {scales, 4, "scales"}}))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return device_status(timed("quantize_rows", s, [&] {
+                         return moe::launch_quantize_rows(x, x_dtype == MOE_BF16, rows, cols, swiglu == 1, codes,
+                                                          scales, s);
+                       }),
+                       fn);
+}
+
+int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets, int64_t max_rows,
+                  const int8_t* x_codes, const float* x_scales, int64_t x_rows, const int32_t* row_index,
+                  const int8_t* w_codes, const float* w_scales, void* y, int32_t y_dtype, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  prof_reset();
+  const char* fn = "moe_matmul_i8";
+  moe::GmmArgs a{};
+  a.form = moe::GmmForm::kNT;
+  a.type = moe::GmmType::kI8;
+  a.G = n_groups;
+  a.N = N;
+  a.K = K;
+  a.group_offsets = group_offsets;
+  a.max_rows = max_rows;
+  a.x = x_codes;
+  a.x_rows = x_rows;
+  a.row_index = row_index;
+  a.w = w_codes;
+  a.x_scales = x_scales;
+  a.w_scales = w_scales;
+  a.out = y;
+  a.out_bf16 = y_dtype == MOE_BF16;
+  int st = check_matmul(fn, a, y_dtype);
+  if (st) return st;
+  if (max_rows == 0) return ok();
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !y)
+    return fail(MOE_ERR_INVALID_ARG, "%s: codes, scales and y are required", fn);
+  if ((st = check_aligned(fn, {{group_offsets, 4, "group_offsets"}, {row_index, 4, "row_index"},
+                               {x_scales, 4, "x_scales"}, {w_scales, 4, "w_scales"},
+                               {y, elem_bytes(y_dtype), "y"}})))
+    return st;
+  return run_matmul(fn, "matmul_i8", a, workspace, workspace_bytes, stream);
 }
 
 const char* moe_last_error(void) { return g_last_error.c_str(); }
