@@ -34,7 +34,8 @@ HIP_FLAGS = [
 
 MOE_SOURCES = ["moe_api.cpp", "route.hip", "permute.hip", "gemm_stream.hip", "gemm_tile.hip", "gemm_tile_q4.hip",
                "gemm_skinny.hip",
-               "gemm_quant.hip", "gemm_simple.hip", "combine.hip", "gmm_any.hip", "quantize.hip"]
+               "gemm_quant.hip", "gemm_simple.hip", "combine.hip", "gmm_launch.cpp", "gmm_any.hip",
+               "gmm_tile_nt.hip", "gmm_tile_nn.hip", "gmm_tile_tn.hip", "gmm_tile_i8.hip", "quantize.hip"]
 
 
 def _run(cmd, verbose):

@@ -221,12 +221,6 @@ int64_t gmm_any_grid(const GmmArgs& a) {
   return p_tiles * q_tiles;
 }
 
-bool gmm_grid_ok(const GmmArgs& a) { return gmm_any_grid(a) * kAnyThreads < (int64_t(1) << 32); }
-
-size_t gmm_workspace(const GmmArgs&) { return 0; }
-
-hipError_t launch_gmm(const GmmArgs& a, void*, hipStream_t s) { return launch_gmm_any(a, s); }
-
 hipError_t launch_gmm_any(const GmmArgs& a, hipStream_t s) {
   switch (a.form) {
     case GmmForm::kNT:

@@ -122,7 +122,10 @@ struct GmmAcross {
     }
   }
   __device__ static __forceinline__ gmm_u32x4 frag(const char* st, const Lane& ln, int b, int kk) {
-    const char* p = st + ln.row + ((b ^ ln.s) * kUnit) + kk * (kRows / 2) * kRowBytes;
+    return read_at(st + ln.row + ((b ^ ln.s) * kUnit) + kk * (kRows / 2) * kRowBytes);
+  }
+  // fragment whose first row (of this lane) is at p
+  __device__ static __forceinline__ gmm_u32x4 read_at(const char* p) {
     if constexpr (T::kBytes == 2) {
 #if defined(__HIP_DEVICE_COMPILE__)
       typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -170,6 +173,8 @@ __device__ __forceinline__ bool gmm_find_tile(const int32_t* off, int G, int64_t
     beg += t * bm;
     if (beg >= end) return false;
     end = beg + bm < end ? beg + bm : end;
+    beg = __builtin_amdgcn_readfirstlane((int)beg);  // rows fit 31 bits
+    end = __builtin_amdgcn_readfirstlane((int)end);
     return true;
   }
   const int lane = threadIdx.x & 63;
@@ -201,8 +206,8 @@ __device__ __forceinline__ bool gmm_find_tile(const int32_t* off, int G, int64_t
     const int64_t tiles = (e - b + bm - 1) / bm;
     if (rel < tiles) {
       g = __builtin_amdgcn_readfirstlane(gg);
-      beg = b + rel * bm;
-      end = beg + bm < e ? beg + bm : e;
+      beg = __builtin_amdgcn_readfirstlane((int)(b + rel * bm));  // rows fit 31 bits
+      end = __builtin_amdgcn_readfirstlane((int)(b + (rel + 1) * bm < e ? b + (rel + 1) * bm : e));
       return true;
     }
     rel -= tiles;

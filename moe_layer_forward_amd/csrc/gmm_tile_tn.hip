@@ -1,0 +1,15 @@
+// Tile kernel of the grouped products, bf16 gradient for the weights (gmm_tile.h).
+#include "gmm_tile.h"
+
+namespace moe {
+hipError_t launch_gmm_tile_tn(const GmmArgs& a, hipStream_t s) {
+  const int p_tiles = (a.N + kGmmTile - 1) / kGmmTile, slabs = (a.K + kGmmTile - 1) / kGmmTile;
+  const int64_t tiles = (int64_t)a.G * p_tiles;
+  const dim3 grid((unsigned)gmm_item_grid(tiles, slabs)), block(kGmmThreads);
+  if (a.row_index)
+    gmm_weights_kernel<GmmBf16, true><<<grid, block, 0, s>>>(a, tiles, slabs, p_tiles);
+  else
+    gmm_weights_kernel<GmmBf16, false><<<grid, block, 0, s>>>(a, tiles, slabs, p_tiles);
+  return hipGetLastError();
+}
+}  // namespace moe

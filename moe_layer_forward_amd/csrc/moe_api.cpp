@@ -548,7 +548,9 @@ int check_matmul(const char* fn, const moe::GmmArgs& a, int32_t out_dtype) {
     return fail(MOE_ERR_UNSUPPORTED, "%s: N and K must be at most %d", fn, kMaxMatmulSide);
   if (a.type == GmmType::kI8 && a.K > kMaxI8Depth)
     return fail(MOE_ERR_UNSUPPORTED, "%s: K must be at most %d for exact int32 sums", fn, kMaxI8Depth);
-  if ((int64_t)a.N * a.K * e >= (int64_t(1) << 32))
+  // 32-bit offsets in the kernels' descriptors, with room for one past every end
+  constexpr int64_t kSpan = (int64_t(1) << 32) - 256;
+  if ((int64_t)a.N * a.K * e > kSpan)
     return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weight must stay below 4 GiB", fn);
   if (!a.group_offsets && a.G != 1)
     return fail(MOE_ERR_INVALID_ARG, "%s: group_offsets may be NULL for one group only", fn);
