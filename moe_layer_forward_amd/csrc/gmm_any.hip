@@ -1,12 +1,14 @@
-// Grouped matrix products for any sizes, alignment and type: the plain kernel that every call can take.
+// Grouped matrix products for any sizes, alignment and type: the kernel of the fp32 products and of rows
+// that are not whole 16-byte pieces.
 //
-// Tile 128 x 128, 4 waves in 2 x 2, each 64 x 64 outputs (16 accumulator blocks).  Both operands are
-// read into registers one step ahead, 16 bytes a lane at whatever alignment the rows have (odd row
-// lengths), with the ends of rows filled with zeros element by element, and stored into one of two
-// LDS stages while the other is multiplied.  Contraction indices past the end are zero in both
-// operands, so no neighbouring row's values, finite or not, enter a sum.
-// Bound: the loads (a 16-byte load of an odd row touches two segments) and their trip through
-// registers; see launch_gmm for when the tile kernel takes a call instead.
+// Tile 128 x 128, 4 waves in 2 x 2; a wave owns every other 16-row block of the P rows and 64 Q columns (4 x 4
+// accumulator blocks), and skips the blocks that its group has no rows for.  Both operands are read
+// into registers one step ahead, 16 bytes a lane at whatever alignment the rows have, with the ends of
+// rows filled with zeros element by element, and stored into one of two LDS stages while the other is
+// multiplied.  Contraction indices past the end are zero in both operands, so no neighbouring row's
+// values, finite or not, enter a sum.  Outputs leave through LDS as 16-byte pieces of rows.
+// Two work-groups share a CU (64 KiB of LDS each).  Bound: fp32 by v_mfma_f32_16x16x4_f32 (256 FLOP a
+// clock and CU); odd rows by the loads and their trip through registers.
 #include "gmm_core.h"
 
 namespace moe {
@@ -14,6 +16,7 @@ namespace {
 
 constexpr int kAnyTile = 128;
 constexpr int kAnyThreads = 256;
+constexpr int kAnyStage = kAnyTile * kGmmStepBytes;  // 16 KiB
 
 // nv of the n elements at p (n = 16 bytes of them), zeros after them.
 template <class T>
@@ -42,39 +45,63 @@ __device__ __forceinline__ gmm_u32x4 load_chunk(const char* p, int nv) {
 // L = GmmAcross: chunk q is columns of contraction row q / kChunks.
 template <class T, class L>
 struct AnyOperand {
-  const char* base;         // element [0, 0] of the operand matrix of this tile's group
-  int64_t ld;               // bytes between rows
-  int64_t first;            // first row (Along) or first column (Across) of the tile
-  int64_t outer;            // rows (Along) or columns (Across) that exist
-  int64_t depth;            // length of the contraction
-  const int32_t* index;     // row gather (rows of the tile, or contraction rows), or null
-  int64_t index_rows;       // rows the gathered matrix has
+  static constexpr int kN = 16 / T::kBytes;
+  const char* ptr[4];       // Along: the chunk's row, at its chunk of step 0.  Across (not gathered): likewise
+  int n;                    // Along: elements of the row from the chunk of step 0 on.  Across: of the columns
+  int have;                 // Along: bit j: the row of chunk j exists
+  int64_t ld;               // Across: bytes between contraction rows
+  int depth;                // Across: contraction rows
+  const char* base;         // gathered Across: the matrix at the chunk's column
+  const int32_t* index;
+  int32_t index_last;
 
-  __device__ __forceinline__ int64_t row_of(int64_t r) const {
-    if (!index) return r;
-    const int64_t i = index[r];
-    return i < 0 ? 0 : i >= index_rows ? index_rows - 1 : i;
-  }
-
-  __device__ __forceinline__ void load(int64_t kt, gmm_u32x4 (&v)[4]) const {
-    constexpr int kN = 16 / T::kBytes;
+  // Along: rows [0, rows) of the tile, row r at base + row_of(r) * ld
+  template <class RowOf>
+  __device__ __forceinline__ void init_along(const char* b, int64_t ld_, int depth_, int rows, RowOf row_of) {
+    const int c = (threadIdx.x % L::kChunks) * kN;  // 256 threads: the same chunk of each of the four rows
+    n = depth_ - c;
+    have = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int q = threadIdx.x + kAnyThreads * j;
-      const int r = q / L::kChunks, c = q % L::kChunks;
-      int64_t row, col, nv;
-      if constexpr (L::kAlong) {
-        row = first + r;
-        col = kt * (kGmmStepBytes / T::kBytes) + c * kN;
-        nv = row < outer ? depth - col : 0;
-      } else {
-        row = kt * L::kRows + r;
-        col = first + c * kN;
-        nv = row < depth ? outer - col : 0;
-      }
-      const int n = nv <= 0 ? 0 : nv >= kN ? kN : (int)nv;
+      const int r = (threadIdx.x + kAnyThreads * j) / L::kChunks;
+      ptr[j] = b + (r < rows ? row_of(r) : 0) * ld_ + c * T::kBytes;
+      have |= (r < rows) << j;
+    }
+  }
+  // Across: columns [col0, cols) of contraction rows [0, depth)
+  __device__ __forceinline__ void init_across(const char* b, int64_t ld_, int depth_, int64_t col0, int64_t cols,
+                                              const int32_t* index_, int64_t index_rows) {
+    const int c = (threadIdx.x % L::kChunks) * kN;
+    const int64_t left = cols - col0 - c;
+    n = left > kN ? kN : (int)left;
+    ld = ld_;
+    depth = depth_;
+    index = index_;
+    index_last = (int32_t)index_rows - 1;
+    base = b + (col0 + c) * T::kBytes;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ptr[j] = base + (int64_t)((threadIdx.x + kAnyThreads * j) / L::kChunks) * ld;
+  }
+
+  __device__ __forceinline__ void load(int kt, gmm_u32x4 (&v)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       v[j] = gmm_u32x4{0, 0, 0, 0};
-      if (n > 0) v[j] = load_chunk<T>(base + row_of(row) * ld + col * T::kBytes, n);
+      if constexpr (L::kAlong) {
+        const int nv = (have >> j) & 1 ? n - kt * (kGmmStepBytes / T::kBytes) : 0;
+        if (nv > 0) v[j] = load_chunk<T>(ptr[j] + (int64_t)kt * kGmmStepBytes, nv);
+      } else {
+        const int r = kt * L::kRows + (threadIdx.x + kAnyThreads * j) / L::kChunks;
+        if (r < depth && n > 0) {
+          const char* p = ptr[j] + (int64_t)kt * L::kRows * ld;
+          if (index) {
+            int32_t i = index[r];
+            i = i < 0 ? 0 : i > index_last ? index_last : i;
+            p = base + (int64_t)i * ld;
+          }
+          v[j] = load_chunk<T>(p, n);
+        }
+      }
     }
   }
   __device__ static __forceinline__ void store(char* stage, const gmm_u32x4 (&v)[4]) {
@@ -86,25 +113,20 @@ struct AnyOperand {
   }
 };
 
-template <class T>
-__device__ __forceinline__ void store_out(const GmmArgs& a, void* out, int64_t row, int64_t col, int64_t ld, float v) {
-  if (a.out_bf16)
-    static_cast<uint16_t*>(out)[row * ld + col] = f32_to_bf16(v);
-  else
-    static_cast<float*>(out)[row * ld + col] = v;
-}
-
 template <GmmForm F, class T>
-__global__ __launch_bounds__(kAnyThreads) void gmm_any_kernel(GmmArgs a) {
+__global__ __launch_bounds__(kAnyThreads, 2) void gmm_any_kernel(GmmArgs a) {
   using LP = GmmP<F, T, kAnyTile>;
   using LQ = GmmQ<F, T, kAnyTile>;
-  __shared__ __align__(16) char p_lds[2][LP::kStageBytes], q_lds[2][LQ::kStageBytes];
+  static_assert(LP::kStageBytes == kAnyStage && LQ::kStageBytes == kAnyStage, "stages");
+  __shared__ __align__(16) char lds[4 * kAnyStage];  // P stages 0, 1, Q stages 0, 1; then the output tile
 
-  // which tile: NT / NN a row tile of a group x a column slab, TN a (group, n tile, k tile)
+  // which tile: NT / NN a row tile of a group x a column slab, TN a (group, n tile, k tile); which range
   const int64_t q_len = F == GmmForm::kNT ? a.N : a.K;
-  const int64_t q_tiles = (q_len + kAnyTile - 1) / kAnyTile;
-  const int64_t t = blockIdx.x / q_tiles;
-  const int64_t q0 = (blockIdx.x % q_tiles) * kAnyTile;
+  const int q_tiles = (int)((q_len + kAnyTile - 1) / kAnyTile);
+  const int sp = (int)(blockIdx.x % (unsigned)a.split);
+  const int64_t item = blockIdx.x / (unsigned)a.split;
+  const int64_t t = item / q_tiles;
+  const int64_t q0 = (item % q_tiles) * kAnyTile;
   int g;
   int64_t beg, end, p0 = 0;
   if constexpr (F == GmmForm::kTN) {
@@ -114,33 +136,46 @@ __global__ __launch_bounds__(kAnyThreads) void gmm_any_kernel(GmmArgs a) {
     gmm_group_rows(a.group_offsets, a.max_rows, g, beg, end);
   } else {
     if (!gmm_find_tile(a.group_offsets, a.G, a.max_rows, kAnyTile, t, g, beg, end)) return;
+    beg = gmm_uniform((int)beg);
+    end = gmm_uniform((int)end);
   }
+  // output rows of this tile (TN: columns of dy, rows of dW[g])
+  const int rows = (int)(F == GmmForm::kTN ? (a.N - p0 < kAnyTile ? a.N - p0 : kAnyTile) : end - beg);
+  const int cols = (int)(q_len - q0 < kAnyTile ? q_len - q0 : kAnyTile);
+  const int64_t ldn = (int64_t)a.N * T::kBytes, ldk = (int64_t)a.K * T::kBytes;
   const char* w = static_cast<const char*>(a.w);
-  if (F != GmmForm::kTN) w += (int64_t)g * a.N * a.K * T::kBytes;
+  if (F != GmmForm::kTN) w += (int64_t)g * a.N * ldk;
+  const auto x_row = [&](int r) -> int64_t {
+    if (!a.row_index) return beg + r;
+    const int64_t i = a.row_index[beg + r];
+    return i < 0 ? 0 : i >= a.x_rows ? a.x_rows - 1 : i;
+  };
 
   AnyOperand<T, LP> p;
   AnyOperand<T, LQ> q;
-  int64_t depth;
+  int depth;
   if constexpr (F == GmmForm::kNT) {
     depth = a.K;
-    p = {static_cast<const char*>(a.x), (int64_t)a.K * T::kBytes, beg, end, depth, a.row_index, a.x_rows};
-    q = {w, (int64_t)a.K * T::kBytes, q0, a.N, depth, nullptr, 0};
+    p.init_along(static_cast<const char*>(a.x), ldk, depth, rows, x_row);
+    q.init_along(w + q0 * ldk, ldk, depth, cols, [](int r) -> int64_t { return r; });
   } else if constexpr (F == GmmForm::kNN) {
     depth = a.N;
-    p = {static_cast<const char*>(a.dy), (int64_t)a.N * T::kBytes, beg, end, depth, nullptr, 0};
-    q = {w, (int64_t)a.K * T::kBytes, q0, a.K, depth, nullptr, 0};
+    p.init_along(static_cast<const char*>(a.dy) + beg * ldn, ldn, depth, rows, [](int r) -> int64_t { return r; });
+    q.init_across(w, ldk, depth, q0, a.K, nullptr, 0);
   } else {
-    depth = end - beg;
-    const int64_t ldn = (int64_t)a.N * T::kBytes, ldk = (int64_t)a.K * T::kBytes;
-    p = {static_cast<const char*>(a.dy) + beg * ldn, ldn, p0, a.N, depth, nullptr, 0};
-    q = {static_cast<const char*>(a.x) + (a.row_index ? 0 : beg * ldk), ldk, q0, a.K, depth,
-         a.row_index ? a.row_index + beg : nullptr, a.x_rows};
+    depth = (int)(end - beg);
+    p.init_across(static_cast<const char*>(a.dy) + beg * ldn, ldn, depth, p0, a.N, nullptr, 0);
+    q.init_across(static_cast<const char*>(a.x) + (a.row_index ? 0 : beg * ldk), ldk, depth, q0, a.K,
+                  a.row_index ? a.row_index + beg : nullptr, a.x_rows);
   }
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int pw = (wave >> 1) * 4, qw = (wave & 1) * 4;  // first 16-block of the wave's rows and columns
-  const auto lp = LP::lane();
-  const auto lq = LQ::lane();
+  const int lane = threadIdx.x & 63, wave = gmm_uniform(threadIdx.x >> 6);
+  const int wr = wave >> 1, wc = wave & 1;
+  const int blocks = gmm_uniform((rows + 15) / 16);
+  GmmFrags<LP, 2> fp;
+  fp.init(wr);
+  GmmFrags<LQ, 1> fq;
+  fq.init(4 * wc);
   typename T::Acc acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -148,67 +183,195 @@ __global__ __launch_bounds__(kAnyThreads) void gmm_any_kernel(GmmArgs a) {
     for (int s = 0; s < 4; ++s) acc[i][s] = typename T::Acc{0, 0, 0, 0};
 
   constexpr int kStep = kGmmStepBytes / T::kBytes;
-  const int64_t nk = (depth + kStep - 1) / kStep;
+  int first, nk;
+  gmm_range(gmm_uniform((depth + kStep - 1) / kStep), a.split, sp, first, nk);
   gmm_u32x4 pv[4], qv[4];
   if (nk > 0) {
-    p.load(0, pv);
-    q.load(0, qv);
-    p.store(p_lds[0], pv);
-    q.store(q_lds[0], qv);
+    p.load(first, pv);
+    q.load(first, qv);
+    p.store(lds, pv);
+    q.store(lds + 2 * kAnyStage, qv);
   }
   __syncthreads();
-  for (int64_t kt = 0; kt < nk; ++kt) {
+  for (int kt = 0; kt < nk; ++kt) {
     const int cur = kt & 1;
+    const char *ps = lds + cur * kAnyStage, *qs = lds + (2 + cur) * kAnyStage;
     if (kt + 1 < nk) {
-      p.load(kt + 1, pv);
-      q.load(kt + 1, qv);
+      p.load(first + kt + 1, pv);
+      q.load(first + kt + 1, qv);
     }
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       gmm_u32x4 qf[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) qf[s] = LQ::frag(q_lds[cur], lq, qw + s, kk);
+      for (int s = 0; s < 4; ++s) qf[s] = fq.read(qs, s, kk);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const gmm_u32x4 pf = LP::frag(p_lds[cur], lp, pw + i, kk);
+        if (wr + 2 * i < blocks) {
+          const gmm_u32x4 pf = fp.read(ps, i, kk);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) acc[i][s] = T::mfma(qf[s], pf, acc[i][s]);
+          for (int s = 0; s < 4; ++s) acc[i][s] = T::mfma(qf[s], pf, acc[i][s]);
+        }
       }
     }
     if (kt + 1 < nk) {
-      p.store(p_lds[cur ^ 1], pv);
-      q.store(q_lds[cur ^ 1], qv);
+      p.store(lds + (cur ^ 1) * kAnyStage, pv);
+      q.store(lds + (2 + (cur ^ 1)) * kAnyStage, qv);
     }
     __syncthreads();
   }
 
-  // TN: rows are columns of dy, written into dW[g]; otherwise rows [beg, end)
-  const int64_t row0 = F == GmmForm::kTN ? p0 : beg, row_end = F == GmmForm::kTN ? (int64_t)a.N : end;
-  char* out = static_cast<char*>(a.out);
-  if (F == GmmForm::kTN) out += (int64_t)g * a.N * a.K * (a.out_bf16 ? 2 : 4);
+  // The output tile through LDS, as fp32 (int32 partial sums as they are): row r of 512 bytes, its 16-byte
+  // piece c at c ^ (r & 15); the last barrier above freed the stages.
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + 16 * (pw + i) + (lane & 15);
-    if (row >= row_end) continue;
-    float sx = 1.f;
-    if constexpr (std::is_same_v<T, GmmI8>) sx = a.x_scales[p.row_of(row)];
+    const int r = 16 * (wr + 2 * i) + (lane & 15);
+    if (wr + 2 * i < blocks) {
+      float sx = 1.f;
+      if constexpr (std::is_same_v<T, GmmI8>)
+        if (a.split == 1) sx = a.x_scales[x_row(r < rows ? r : rows - 1)];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int64_t col = q0 + 16 * (qw + s) + 4 * (lane >> 4);
+      for (int s = 0; s < 4; ++s) {
+        const int col = 16 * (4 * wc + s) + 4 * (lane >> 4);
+        f32x4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (col + e >= q_len) continue;
-        float v = (float)acc[i][s][e];
-        if constexpr (std::is_same_v<T, GmmI8>) v = v * sx * a.w_scales[(int64_t)g * a.N + col + e];
-        store_out<T>(a, out, row, col + e, q_len, v);
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (std::is_same_v<T, GmmI8>) {
+            const int c = col + e < cols ? col + e : cols - 1;
+            v[e] = a.split == 1 ? (float)acc[i][s][e] * sx * a.w_scales[(int64_t)g * a.N + q0 + c]
+                                : __int_as_float(acc[i][s][e]);
+          } else {
+            v[e] = acc[i][s][e];
+          }
+        }
+        *reinterpret_cast<f32x4*>(lds + r * 512 + (((col >> 2) ^ (r & 15)) << 4)) = v;
       }
+    }
+  }
+  __syncthreads();
+  const int64_t out_row = F == GmmForm::kTN ? (int64_t)g * a.N + p0 : beg;
+  const int64_t out_rows = F == GmmForm::kTN ? (int64_t)a.G * a.N : a.max_rows;
+  const bool bf16 = a.split == 1 && a.out_bf16;
+  char* out = a.split == 1 ? static_cast<char*>(a.out) : reinterpret_cast<char*>(a.part + sp * out_rows * q_len);
+  out += (out_row * q_len + q0) * (bf16 ? 2 : 4);
+  // 8 columns a thread, at the alignment that the row has
+  for (int ch = threadIdx.x; ch < rows * 16; ch += kAnyThreads) {
+    const int r = ch >> 4, c = (ch & 15) * 8;
+    if (c >= cols) continue;
+    f32x4 v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[h] = *reinterpret_cast<const f32x4*>(lds + r * 512 + (((c / 4 + h) ^ (r & 15)) << 4));
+    const int n = cols - c;
+    if (bf16) {
+      uint16_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = f32_to_bf16(v[e >> 2][e & 3]);
+      char* o = out + ((int64_t)r * q_len + c) * 2;
+      if (n >= 8) {
+        __builtin_memcpy(o, h, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < n) reinterpret_cast<uint16_t*>(o)[e] = h[e];
+      }
+    } else {
+      char* o = out + ((int64_t)r * q_len + c) * 4;
+      if (n >= 8) {
+        __builtin_memcpy(o, v, 32);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < n) reinterpret_cast<float*>(o)[e] = v[e >> 2][e & 3];
+      }
+    }
+  }
+}
+
+// out = the sum over the ranges of part, in range order; one work-group per 1024 columns of a row.
+template <GmmForm F, bool kI8>
+__global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
+  const int64_t q_len = F == GmmForm::kNT ? a.N : a.K;
+  const int64_t out_rows = F == GmmForm::kTN ? (int64_t)a.G * a.N : a.max_rows;
+  const int per_row = (int)((q_len + 1023) / 1024);
+  const int64_t row = blockIdx.x / per_row;
+  const int64_t col = (int64_t)(blockIdx.x % per_row) * 1024 + threadIdx.x * 4;
+  if (F != GmmForm::kTN && a.group_offsets) {  // rows past the last group have no sums
+    int64_t beg, end;
+    gmm_group_rows(a.group_offsets, a.max_rows, a.G - 1, beg, end);
+    if (row >= end) return;
+  }
+  const int n = q_len - col < 4 ? (int)(q_len - col) : 4;
+  if (n <= 0) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  int isum[4] = {0, 0, 0, 0};
+  const float* p = a.part + row * q_len + col;
+  for (int s = 0; s < a.split; ++s, p += out_rows * q_len) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (n == 4) {
+      __builtin_memcpy(v, p, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) v[e] = p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (kI8)
+        isum[e] += __float_as_int(v[e]);
+      else
+        sum[e] += v[e];
+    }
+  }
+  if constexpr (kI8) {
+    int64_t i = row;
+    if (a.row_index) {
+      i = a.row_index[row];
+      i = i < 0 ? 0 : i >= a.x_rows ? a.x_rows - 1 : i;
+    }
+    int g = 0;  // the row's group: the first whose end is past it
+    if (a.group_offsets) {
+      int hi = a.G - 1;
+      while (g < hi) {
+        const int mid = (g + hi) / 2;
+        if (a.group_offsets[mid + 1] > row)
+          hi = mid;
+        else
+          g = mid + 1;
+      }
+    }
+    const float sx = a.x_scales[i];
+    const float* sw = a.w_scales + (int64_t)g * a.N + col;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = (float)isum[e] * sx * (e < n ? sw[e] : 0.f);
+  }
+  if (a.out_bf16) {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + row * q_len + col;
+    uint16_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = f32_to_bf16(sum[e]);
+    if (n == 4) {
+      __builtin_memcpy(o, h, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) o[e] = h[e];
+    }
+  } else {
+    float* o = static_cast<float*>(a.out) + row * q_len + col;
+    if (n == 4) {
+      __builtin_memcpy(o, sum, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) o[e] = sum[e];
     }
   }
 }
 
 template <GmmForm F, class T>
 hipError_t launch_any(const GmmArgs& a, hipStream_t s) {
-  gmm_any_kernel<F, T><<<dim3((unsigned)gmm_any_grid(a)), dim3(kAnyThreads), 0, s>>>(a);
+  gmm_any_kernel<F, T><<<dim3((unsigned)(gmm_any_grid(a) * a.split)), dim3(kAnyThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -234,6 +397,21 @@ hipError_t launch_gmm_any(const GmmArgs& a, hipStream_t s) {
       return a.type == GmmType::kBf16 ? launch_any<GmmForm::kTN, GmmBf16>(a, s)
                                       : launch_any<GmmForm::kTN, GmmF32>(a, s);
   }
+}
+
+hipError_t launch_gmm_join(const GmmArgs& a, hipStream_t s) {
+  const int64_t q_len = a.form == GmmForm::kNT ? a.N : a.K;
+  const int64_t rows = a.form == GmmForm::kTN ? (int64_t)a.G * a.N : a.max_rows;
+  const dim3 grid((unsigned)(rows * ((q_len + 1023) / 1024))), block(256);
+  if (a.type == GmmType::kI8)
+    gmm_join_kernel<GmmForm::kNT, true><<<grid, block, 0, s>>>(a);
+  else if (a.form == GmmForm::kNT)
+    gmm_join_kernel<GmmForm::kNT, false><<<grid, block, 0, s>>>(a);
+  else if (a.form == GmmForm::kNN)
+    gmm_join_kernel<GmmForm::kNN, false><<<grid, block, 0, s>>>(a);
+  else
+    gmm_join_kernel<GmmForm::kTN, false><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace moe

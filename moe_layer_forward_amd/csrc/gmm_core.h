@@ -124,7 +124,7 @@ struct GmmAcross {
   __device__ static __forceinline__ gmm_u32x4 frag(const char* st, const Lane& ln, int b, int kk) {
     return read_at(st + ln.row + ((b ^ ln.s) * kUnit) + kk * (kRows / 2) * kRowBytes);
   }
-  // fragment whose first row (of this lane) is at p
+  // the fragment whose first row (of this lane) is at p
   __device__ static __forceinline__ gmm_u32x4 read_at(const char* p) {
     if constexpr (T::kBytes == 2) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -150,6 +150,37 @@ template <GmmForm F, class T, int OUTER>
 using GmmP = std::conditional_t<F == GmmForm::kTN, GmmAcross<T, OUTER>, GmmAlong<T, OUTER>>;
 template <GmmForm F, class T, int OUTER>
 using GmmQ = std::conditional_t<F == GmmForm::kNT, GmmAlong<T, OUTER>, GmmAcross<T, OUTER>>;
+
+// A wave's fragment reads: block i of its blocks is 16-row block b0 + kStride i of the stage.
+template <class L, int kStride>
+struct GmmFrags {
+  uint32_t off[L::kAlong ? 2 : 4];
+  __device__ __forceinline__ void init(int b0) {
+    const auto ln = L::lane();
+    if constexpr (L::kAlong) {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) off[kk] = (uint32_t)(b0 * 16 * kGmmStepBytes + ln.off[kk]);
+    } else {  // (b0 + kStride m) below 8 per group of 8 units, so the swizzle stays inside it
+#pragma unroll
+      for (int m = 0; m < 4; ++m) off[m] = (uint32_t)(ln.row + ((b0 + kStride * m) ^ ln.s) * L::kUnit);
+    }
+  }
+  __device__ __forceinline__ gmm_u32x4 read(const char* st, int i, int kk) const {
+    if constexpr (L::kAlong)
+      return *reinterpret_cast<const gmm_u32x4*>(st + off[kk] + i * kStride * 16 * kGmmStepBytes);
+    else
+      return L::read_at(st + off[i & 3] + (i >> 2) * 4 * kStride * L::kUnit + kk * (L::kRows / 2) * L::kRowBytes);
+  }
+};
+
+// A value that every lane has, in scalar registers (the compiler cannot tell behind the lanes' search for the
+// tile; a descriptor in vector registers costs a loop over the lanes per load).
+__device__ __forceinline__ int gmm_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* gmm_uniform(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = (uint32_t)gmm_uniform((int)v), hi = (uint32_t)gmm_uniform((int)(v >> 32));
+  return reinterpret_cast<const char*>(lo | hi << 32);
+}
 
 // Rows [beg, end) of group g, kept inside [0, max_rows] whatever the offsets hold (null: one group of
 // all rows).
@@ -213,6 +244,12 @@ __device__ __forceinline__ bool gmm_find_tile(const int32_t* off, int G, int64_t
     rel -= tiles;
   }
   return false;
+}
+
+// Share sp of nk contraction steps cut into `split` nearly equal ranges.
+__device__ __forceinline__ void gmm_range(int nk, int split, int sp, int& first, int& n) {
+  first = (int)((int64_t)nk * sp / split);
+  n = (int)((int64_t)nk * (sp + 1) / split) - first;
 }
 
 // Most row tiles of bm rows that G groups over max_rows rows can have.

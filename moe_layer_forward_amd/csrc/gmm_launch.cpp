@@ -1,33 +1,74 @@
-// Which kernel a grouped product runs on.
+// Which kernel a grouped product runs on, and into how many ranges its contraction is cut.
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace moe {
 namespace {
 
+constexpr int64_t kCus = 256;
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// The tile kernels move 16-byte pieces: operand rows start on 16 bytes and are multiples of 16 bytes long.
-bool tile_ok(const GmmArgs& a) {
+int elem_bytes(const GmmArgs& a) { return a.type == GmmType::kI8 ? 1 : a.type == GmmType::kBf16 ? 2 : 4; }
+
+// The tile kernels move 16-byte pieces: operand rows are multiples of 16 bytes long ...
+bool tile_sizes(const GmmArgs& a) {
   if (a.type == GmmType::kF32) return false;
-  const int e = a.type == GmmType::kI8 ? 1 : 2;
-  if ((int64_t)a.K * e % 16) return false;
-  if (a.form != GmmForm::kNT && (int64_t)a.N * e % 16) return false;
-  return (a.form == GmmForm::kNN || aligned16(a.x)) && (a.form == GmmForm::kNT || aligned16(a.dy)) &&
+  const int e = elem_bytes(a);
+  return (int64_t)a.K * e % 16 == 0 && (a.form == GmmForm::kNT || (int64_t)a.N * e % 16 == 0);
+}
+// ... and start on 16 bytes.
+bool tile_ok(const GmmArgs& a) {
+  return tile_sizes(a) && (a.form == GmmForm::kNN || aligned16(a.x)) && (a.form == GmmForm::kNT || aligned16(a.dy)) &&
          (a.form == GmmForm::kTN || aligned16(a.w));
 }
+
+int64_t out_elems(const GmmArgs& a) {
+  return a.form == GmmForm::kTN ? (int64_t)a.G * a.N * a.K : a.max_rows * (a.form == GmmForm::kNT ? a.N : a.K);
+}
+
+// Ranges of the contraction for `items` output tiles (an upper bound) of at most `steps` steps, when `slots`
+// work-groups run at once: enough to fill the chip, each range at least kMinSteps steps.
+int split_of(int64_t items, int64_t steps, int64_t slots) {
+  constexpr int64_t kMinSteps = 6, kMaxSplit = 16;
+  if (items <= 0 || items > slots / 2) return 1;
+  return (int)std::max<int64_t>(1, std::min({slots / items, steps / kMinSteps, kMaxSplit}));
+}
+
+int64_t max_steps(const GmmArgs& a) {
+  const int64_t depth = a.form == GmmForm::kNT ? a.K : a.form == GmmForm::kNN ? a.N : a.max_rows;
+  return (depth * elem_bytes(a) + 127) / 128;
+}
+
+int any_split(const GmmArgs& a) { return split_of(gmm_any_grid(a), max_steps(a), 2 * kCus); }
+int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a), max_steps(a), kCus); }
 
 }  // namespace
 
 // Work-groups of 512 threads or fewer, a dealt grid at most twice the tiles.
 bool gmm_grid_ok(const GmmArgs& a) { return 2 * 512 * gmm_any_grid(a) < (int64_t(1) << 32); }
 
-size_t gmm_workspace(const GmmArgs&) { return 0; }
+size_t gmm_workspace(const GmmArgs& a) {
+  const int split = std::max(any_split(a), tile_sizes(a) ? tile_split(a) : 1);
+  return split > 1 ? (size_t)split * out_elems(a) * sizeof(float) : 0;
+}
 
-hipError_t launch_gmm(const GmmArgs& a, void*, hipStream_t s) {
-  if (!tile_ok(a)) return launch_gmm_any(a, s);
-  if (a.form == GmmForm::kNN) return launch_gmm_tile_nn(a, s);
-  if (a.form == GmmForm::kTN) return launch_gmm_tile_tn(a, s);
-  return a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, s) : launch_gmm_tile_nt(a, s);
+hipError_t launch_gmm(const GmmArgs& args, void* workspace, hipStream_t s) {
+  GmmArgs a = args;
+  const bool tile = tile_ok(a);
+  a.split = tile ? tile_split(a) : any_split(a);
+  a.part = static_cast<float*>(workspace);
+  hipError_t e;
+  if (!tile)
+    e = launch_gmm_any(a, s);
+  else if (a.form == GmmForm::kNN)
+    e = launch_gmm_tile_nn(a, s);
+  else if (a.form == GmmForm::kTN)
+    e = launch_gmm_tile_tn(a, s);
+  else
+    e = a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, s) : launch_gmm_tile_nt(a, s);
+  return e == hipSuccess && a.split > 1 ? launch_gmm_join(a, s) : e;
 }
 
 }  // namespace moe

@@ -32,15 +32,6 @@ constexpr int kGmmSuper = 4;        // row tiles that run side by side on one XC
 typedef __amdgpu_buffer_rsrc_t GmmRsrc;
 typedef __attribute__((address_space(3))) void* GmmLds;
 
-// A value that every lane has, in scalar registers (the compiler cannot tell behind the lanes' search for the
-// tile; a descriptor in vector registers costs a loop over the lanes per load).
-__device__ __forceinline__ int gmm_uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ const char* gmm_uniform(const char* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint64_t lo = (uint32_t)gmm_uniform((int)v), hi = (uint32_t)gmm_uniform((int)(v >> 32));
-  return reinterpret_cast<const char*>(lo | hi << 32);
-}
-
 __device__ __forceinline__ GmmRsrc gmm_rsrc(const char* base, uint32_t records) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, (int)records, 0x00020000);
 }
@@ -54,6 +45,7 @@ struct GmmLoadAlong {
   uint32_t off[kGmmLoads];  // lane's row and chunk of pieces w, w + 8, ...
   uint32_t chunk;      // the lane's chunk, in bytes (the same in each of the wave's pieces)
   uint32_t row_bytes;
+  int step0 = 0;       // first step of this item's range
 
   // rows: tile row rl is matrix row row_of(rl), relative to base
   template <class RowOf>
@@ -70,10 +62,10 @@ struct GmmLoadAlong {
       off[j] = (uint32_t)(row_of(rl) * ld) + chunk;
     }
   }
-  __device__ __forceinline__ void prefetch(int, int) {}
+  __device__ __forceinline__ void prefetch(int) {}
   template <int NL>
   __device__ __forceinline__ void issue(int step, char* stage, int wave) const {
-    const uint32_t kb = (uint32_t)step * kGmmStepBytes;
+    const uint32_t kb = (uint32_t)(step0 + step) * kGmmStepBytes;
     const bool in = kb + chunk < row_bytes;
     const GmmRsrc rs = gmm_rsrc(base, records);
 #pragma unroll
@@ -91,10 +83,11 @@ struct GmmLoadAcross {
   const char* base;    // first contraction row (gathered: the matrix), uniform
   int64_t ld;          // bytes between rows
   int depth;           // contraction rows
+  int step0 = 0;       // first step of this item's range
   uint32_t off[kGmmLoads];  // lane's row of the stage and column (gathered: column only)
   const int32_t* index;
   int32_t index_last;
-  int32_t rows[kGmmLoads], next[kGmmLoads];  // gathered: row numbers of the step issued next, and of the one after
+  int32_t rows, next;  // gathered: lane l's row number of the step issued next, and of the one after
 
   __device__ static __forceinline__ int stage_row(int wave, int j) {
     constexpr int kRowsPer = 1024 / (kGmmTile * T::kBytes);
@@ -113,33 +106,34 @@ struct GmmLoadAcross {
       const int r = stage_row(wave, j);
       const int c = L::chunk_at(r, (threadIdx.x & 63) % L::kChunks);
       off[j] = (uint32_t)(col0 * T::kBytes + c * 16) + (kGather ? 0u : (uint32_t)(r * ld));
-      next[j] = 0;
     }
+    rows = next = 0;
   }
-  // gathered: the row numbers of a step, read one step before its loads (issue(step - 1) follows)
-  __device__ __forceinline__ void prefetch(int step, int wave) {
+  // gathered: the 64 row numbers of a step, a lane each, read one step before its loads (issue(step - 1)
+  // follows)
+  __device__ __forceinline__ void prefetch(int step) {
     if constexpr (kGather) {
-#pragma unroll
-      for (int j = 0; j < kGmmLoads; ++j) {
-        rows[j] = next[j];
-        const uint32_t r = (uint32_t)(step * kRows + stage_row(wave, j));
-        next[j] = (int)r < depth ? index[r] : 0;
-      }
+      static_assert(kRows == 64, "a lane per row");
+      rows = next < 0 ? 0 : next > index_last ? index_last : next;
+      const uint32_t r = (uint32_t)((step0 + step) * kRows) + (threadIdx.x & 63);
+      next = (int)r < depth ? index[r] : 0;
     }
   }
   template <int NL>
   __device__ __forceinline__ void issue(int step, char* stage, int wave) const {
+    step += step0;
     int left = depth - step * kRows;
     left = left < 0 ? 0 : left > kRows ? kRows : left;
     if constexpr (kGather) {
       const GmmRsrc rs = gmm_rsrc(base, (uint32_t)gmm_uniform((int)((index_last + 1) * ld)));
 #pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        const int32_t i = rows[j] < 0 ? 0 : rows[j] > index_last ? index_last : rows[j];
+      for (int j = 0; j < NL; ++j) {  // two rows a piece, one for each half of the wave
+        const int r = (wave + kGmmWaves * j) * 2;
+        const uint32_t r0 = r < left ? (uint32_t)__builtin_amdgcn_readlane(rows, r) * (uint32_t)ld : kGmmOutside;
+        const uint32_t r1 = r + 1 < left ? (uint32_t)__builtin_amdgcn_readlane(rows, r + 1) * (uint32_t)ld : kGmmOutside;
+        const uint32_t o = threadIdx.x & 32 ? r1 : r0;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GmmLds)(stage + (wave + kGmmWaves * j) * 1024), 16,
-                                                 stage_row(wave, j) < left ? (uint32_t)i * (uint32_t)ld + off[j]
-                                                                           : kGmmOutside,
-                                                 0, 0, 0);
+                                                 o == kGmmOutside ? kGmmOutside : o + off[j], 0, 0, 0);
       }
     } else {
       const GmmRsrc rs = gmm_rsrc(gmm_uniform(base + (int64_t)step * kRows * ld),
@@ -149,28 +143,6 @@ struct GmmLoadAcross {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GmmLds)(stage + (wave + kGmmWaves * j) * 1024), 16, off[j], 0, 0,
                                                  0);
     }
-  }
-};
-
-// A wave's fragment reads: block i of its blocks is 16-row block b0 + kStride i of the stage.
-template <class L, int kStride>
-struct GmmFrags {
-  uint32_t off[L::kAlong ? 2 : 4];
-  __device__ __forceinline__ void init(int b0) {
-    const auto ln = L::lane();
-    if constexpr (L::kAlong) {
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) off[kk] = (uint32_t)(b0 * 16 * kGmmStepBytes + ln.off[kk]);
-    } else {  // (b0 + kStride m) below 8 per group of 8 units, so the swizzle stays inside it
-#pragma unroll
-      for (int m = 0; m < 4; ++m) off[m] = (uint32_t)(ln.row + ((b0 + kStride * m) ^ ln.s) * L::kUnit);
-    }
-  }
-  __device__ __forceinline__ gmm_u32x4 read(const char* st, int i, int kk) const {
-    if constexpr (L::kAlong)
-      return *reinterpret_cast<const gmm_u32x4*>(st + off[kk] + i * kStride * 16 * kGmmStepBytes);
-    else
-      return L::read_at(st + off[i & 3] + (i >> 2) * 4 * kStride * L::kUnit + kk * (L::kRows / 2) * L::kRowBytes);
   }
 };
 
@@ -225,7 +197,7 @@ __device__ __forceinline__ void gmm_step(LoadP& lp, LoadQ& lq, int kt, const Gmm
     if (f == NF - 2) {
       wait_vmcnt<kGmmLoads>();
       block_sync_lds();
-      lq.prefetch(kt + 4, wave);
+      lq.prefetch(kt + 4);
       lp.template issue<kPLoads>(kt + 2, r.p[D % 2], wave);
       lq.template issue<kGmmLoads>(kt + 3, r.q[D % 3], wave);
       __builtin_amdgcn_sched_barrier(0);
@@ -243,10 +215,10 @@ __device__ __forceinline__ void gmm_loop(LoadP& lp, LoadQ& lq, int nk, const Gmm
                                          int wave, typename T::Acc (&acc)[NB][4]) {
   constexpr int kPLoads = LoadP::kAllPieces ? kGmmLoads : (NB + 1) / 2;
   if (nk <= 0) return;
-  lq.prefetch(0, wave);
+  lq.prefetch(0);
   static_for<3>([&](auto ic) {  // Q0 P0 Q1 P1 Q2
     constexpr int j = decltype(ic)::value;
-    lq.prefetch(j + 1, wave);
+    lq.prefetch(j + 1);
     lq.template issue<kGmmLoads>(j, r.q[j], wave);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (j < 2) lp.template issue<kPLoads>(j, r.p[j], wave);
@@ -349,8 +321,7 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
 // dealt to the XCDs and run slab by slab with their tiles side by side: 32 work-groups of an XCD then
 // share kGmmSuper row tiles and 8 slabs in its L2.  With fewer, items go out in order, so that (8 slabs or
 // more) every tile's slab j runs on XCD j % 8.  False for padding.
-__device__ __forceinline__ bool gmm_item(int64_t tiles, int slabs, int64_t& tile, int& slab) {
-  const int64_t b = blockIdx.x;
+__device__ __forceinline__ bool gmm_item(int64_t b, int64_t tiles, int slabs, int64_t& tile, int& slab) {
   if (tiles < kXcds * kGmmSuper) {
     tile = b / slabs;
     slab = (int)(b % slabs);
@@ -376,7 +347,7 @@ inline int64_t gmm_item_grid(int64_t tiles, int slabs) {
 // NT and NN: output rows are rows of a group.
 template <GmmForm F, class T, int NB>
 __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& rings, int g, int64_t beg, int64_t end,
-                                              int64_t q0) {
+                                              int64_t q0, int sp) {
   using LP = GmmAlong<T, kGmmTile>;
   using LQ = GmmQ<F, T, kGmmTile>;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave >> 2, wc = wave & 3;
@@ -414,17 +385,26 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[i][s] = typename T::Acc{0, 0, 0, 0};
   constexpr int kStep = kGmmStepBytes / T::kBytes;
-  gmm_loop<T, NB>(lp, lq, (int)((depth + kStep - 1) / kStep), rings, fp, fq, wave, acc);
+  int nk;
+  gmm_range((int)((depth + kStep - 1) / kStep), a.split, sp, lp.step0, nk);
+  lq.step0 = lp.step0;
+  gmm_loop<T, NB>(lp, lq, nk, rings, fp, fq, wave, acc);
 
   GmmOut o;
-  const int e = a.out_bf16 ? 2 : 4;
-  o.out = static_cast<char*>(a.out) + (beg * q_len + q0) * e;
+  const int e = a.split == 1 && a.out_bf16 ? 2 : 4;
+  char* const out = a.split == 1 ? static_cast<char*>(a.out)
+                                 : reinterpret_cast<char*>(a.part + sp * a.max_rows * q_len);
+  o.out = out + (beg * q_len + q0) * e;
   o.ld = q_len;
   o.rows = rows;
   o.cols = (int)(q_len - q0 < kGmmTile ? q_len - q0 : kGmmTile);
-  o.bf16 = a.out_bf16;
-  o.pieces = (q_len * e) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  o.bf16 = e == 2;
+  o.pieces = (q_len * e) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   if constexpr (std::is_same_v<T, GmmI8>) {
+    if (a.split > 1) {  // int32 partial sums, as they are
+      gmm_store<NB>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return __int_as_float(acc[i][s][j]); });
+      return;
+    }
     float sx[NB], sw[4][4];
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -457,19 +437,20 @@ __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 
   MOE_GMM_SMEM
   int64_t t, beg, end;
   int slab, g;
-  if (!gmm_item(tiles, slabs, t, slab)) return;
+  [[maybe_unused]] const int sp = (int)(blockIdx.x % (unsigned)a.split);
+  if (!gmm_item(blockIdx.x / (unsigned)a.split, tiles, slabs, t, slab)) return;
   if (!gmm_find_tile(a.group_offsets, a.G, a.max_rows, kGmmTile, t, g, beg, end)) return;
 #if defined(__HIP_DEVICE_COMPILE__)
   const int64_t q0 = (int64_t)slab * kGmmTile;
   switch ((int)(end - beg + 31) / 32) {  // P blocks per wave
-    case 8: gmm_rows_body<F, T, 8>(a, rings, g, beg, end, q0); break;
-    case 7: gmm_rows_body<F, T, 7>(a, rings, g, beg, end, q0); break;
-    case 6: gmm_rows_body<F, T, 6>(a, rings, g, beg, end, q0); break;
-    case 5: gmm_rows_body<F, T, 5>(a, rings, g, beg, end, q0); break;
-    case 4: gmm_rows_body<F, T, 4>(a, rings, g, beg, end, q0); break;
-    case 3: gmm_rows_body<F, T, 3>(a, rings, g, beg, end, q0); break;
-    case 2: gmm_rows_body<F, T, 2>(a, rings, g, beg, end, q0); break;
-    default: gmm_rows_body<F, T, 1>(a, rings, g, beg, end, q0); break;
+    case 8: gmm_rows_body<F, T, 8>(a, rings, g, beg, end, q0, sp); break;
+    case 7: gmm_rows_body<F, T, 7>(a, rings, g, beg, end, q0, sp); break;
+    case 6: gmm_rows_body<F, T, 6>(a, rings, g, beg, end, q0, sp); break;
+    case 5: gmm_rows_body<F, T, 5>(a, rings, g, beg, end, q0, sp); break;
+    case 4: gmm_rows_body<F, T, 4>(a, rings, g, beg, end, q0, sp); break;
+    case 3: gmm_rows_body<F, T, 3>(a, rings, g, beg, end, q0, sp); break;
+    case 2: gmm_rows_body<F, T, 2>(a, rings, g, beg, end, q0, sp); break;
+    default: gmm_rows_body<F, T, 1>(a, rings, g, beg, end, q0, sp); break;
   }
 #else
   (void)rings;
@@ -483,7 +464,8 @@ __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 
   MOE_GMM_SMEM
   int64_t t;
   int slab;
-  if (!gmm_item(tiles, slabs, t, slab)) return;
+  [[maybe_unused]] const int sp = (int)(blockIdx.x % (unsigned)a.split);
+  if (!gmm_item(blockIdx.x / (unsigned)a.split, tiles, slabs, t, slab)) return;
 #if defined(__HIP_DEVICE_COMPILE__)
   using L = GmmAcross<T, kGmmTile>;
   const int g = (int)(t / p_tiles);
@@ -507,15 +489,20 @@ __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[i][s] = f32x4{0.f, 0.f, 0.f, 0.f};
-  gmm_loop<T, 8>(lp, lq, gmm_uniform((depth + L::kRows - 1) / L::kRows), rings, fp, fq, wave, acc);
+  int nk;
+  gmm_range(gmm_uniform((depth + L::kRows - 1) / L::kRows), a.split, sp, lp.step0, nk);
+  lq.step0 = lp.step0;
+  gmm_loop<T, 8>(lp, lq, nk, rings, fp, fq, wave, acc);
   GmmOut o;
-  const int e = a.out_bf16 ? 2 : 4;
-  o.out = static_cast<char*>(a.out) + (((int64_t)g * a.N + p0) * a.K + q0) * e;
+  const int e = a.split == 1 && a.out_bf16 ? 2 : 4;
+  char* const out = a.split == 1 ? static_cast<char*>(a.out)
+                                 : reinterpret_cast<char*>(a.part + (int64_t)sp * a.G * a.N * a.K);
+  o.out = out + (((int64_t)g * a.N + p0) * a.K + q0) * e;
   o.ld = a.K;
   o.rows = (int)(a.N - p0 < kGmmTile ? a.N - p0 : kGmmTile);
   o.cols = (int)(a.K - q0 < kGmmTile ? a.K - q0 : kGmmTile);
-  o.bf16 = a.out_bf16;
-  o.pieces = ((int64_t)a.K * e) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+  o.bf16 = e == 2;
+  o.pieces = ((int64_t)a.K * e) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   gmm_store<8>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return acc[i][s][j]; });
 #else
   (void)rings;
@@ -526,7 +513,7 @@ template <GmmForm F, class T>
 hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
   const int64_t tiles = gmm_max_tiles(a.max_rows, a.G, kGmmTile);
   const int slabs = ((F == GmmForm::kNT ? a.N : a.K) + kGmmTile - 1) / kGmmTile;
-  gmm_rows_kernel<F, T><<<dim3((unsigned)gmm_item_grid(tiles, slabs)), dim3(kGmmThreads), 0, s>>>(a, tiles, slabs);
+  gmm_rows_kernel<F, T><<<dim3((unsigned)(gmm_item_grid(tiles, slabs) * a.split)), dim3(kGmmThreads), 0, s>>>(a, tiles, slabs);
   return hipGetLastError();
 }
 

@@ -2,10 +2,16 @@
 #include "gmm_tile.h"
 
 namespace moe {
+int64_t gmm_tile_items(const GmmArgs& a) {
+  const int64_t slabs = ((a.form == GmmForm::kNT ? a.N : a.K) + kGmmTile - 1) / kGmmTile;
+  return slabs * (a.form == GmmForm::kTN ? (int64_t)a.G * ((a.N + kGmmTile - 1) / kGmmTile)
+                                         : gmm_max_tiles(a.max_rows, a.G, kGmmTile));
+}
+
 hipError_t launch_gmm_tile_tn(const GmmArgs& a, hipStream_t s) {
   const int p_tiles = (a.N + kGmmTile - 1) / kGmmTile, slabs = (a.K + kGmmTile - 1) / kGmmTile;
   const int64_t tiles = (int64_t)a.G * p_tiles;
-  const dim3 grid((unsigned)gmm_item_grid(tiles, slabs)), block(kGmmThreads);
+  const dim3 grid((unsigned)(gmm_item_grid(tiles, slabs) * a.split)), block(kGmmThreads);
   if (a.row_index)
     gmm_weights_kernel<GmmBf16, true><<<grid, block, 0, s>>>(a, tiles, slabs, p_tiles);
   else

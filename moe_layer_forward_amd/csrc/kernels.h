@@ -247,7 +247,13 @@ struct GmmArgs {
   const float* w_scales;         // kI8: [G, N]
   void* out;
   int32_t out_bf16;
+  // Set by launch_gmm: the contraction cut into `split` ranges whose partial sums (fp32; int32 for kI8) go
+  // to part, [split, output rows, output columns], for launch_gmm_join.
+  int32_t split = 1;
+  float* part = nullptr;
 };
+// The sum over the ranges, in range order, scaled and rounded once into out.
+hipError_t launch_gmm_join(const GmmArgs& a, hipStream_t s);
 // The product, on the kernel that its sizes and alignment call for, and the workspace bytes it needs
 // (decided by type, form and sizes alone).
 hipError_t launch_gmm(const GmmArgs& a, void* workspace, hipStream_t s);
@@ -257,6 +263,7 @@ bool gmm_grid_ok(const GmmArgs& a);
 // Any sizes and any element alignment.
 hipError_t launch_gmm_any(const GmmArgs& a, hipStream_t s);
 int64_t gmm_any_grid(const GmmArgs& a);
+int64_t gmm_tile_items(const GmmArgs& a);
 // 256 x 256 tiles on rows of whole 16-byte pieces (bf16; int8 for the forward).
 hipError_t launch_gmm_tile_nt(const GmmArgs& a, hipStream_t s);
 hipError_t launch_gmm_tile_i8(const GmmArgs& a, hipStream_t s);
