@@ -343,6 +343,7 @@ def moe_forward_fp8(cfg, x, w_router, f8, ws_gate=None, ws_up=None, ws_down=None
 
 
 # --------------------------------------------------------------------------- grouped matrix products
+# These calls are short (a few microseconds of kernel at decode sizes), so the marshalling below is kept lean.
 def _matmul_dtype(t, what):
     import torch
 
@@ -354,7 +355,7 @@ def _matmul_dtype(t, what):
 
 
 def _want(t, what, shape, dtype=None):
-    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+    if t.shape != shape or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{what} must be {tuple(shape)}{f' {dtype}' if dtype is not None else ''}, "
                          f"got {tuple(t.shape)} {t.dtype}")
 
@@ -388,13 +389,37 @@ def _out(out, shape, dtype, default, dev):
     return out, got
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _one_device(*tensors):
-    """The tensors' device and its current stream; every tensor must be there."""
-    dev, stream = _dev(*tensors)
+    """The device of the tensors (all contiguous, on one GPU)."""
+    dev = None
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("moe: every tensor must live on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("moe: tensors must be contiguous")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
             raise ValueError(f"moe: tensors on {t.device} and {dev}")
-    return dev, stream
+    return dev
+
+
+def _launch(dev, entry, *args):
+    """The C call on dev's current stream, with dev the current device (a stream belongs to its device)."""
+    import torch
+
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        _check(entry(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(entry(*args, stream))
 
 
 def moe_matmul_workspace_size(op: int, dtype: int, n_groups: int, max_rows: int, N: int, K: int) -> int:
@@ -405,24 +430,16 @@ def moe_matmul_workspace_size(op: int, dtype: int, n_groups: int, max_rows: int,
 
 
 def _matmul_ws(workspace, op, dtype, G, rows, N, K, dev):
-    """(tensor or None, bytes): the caller's workspace, or a new one of the size the call needs."""
+    """(tensor or None, address, bytes): the caller's workspace, or a new one of the size the call needs."""
     import torch
 
     if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     n = moe_matmul_workspace_size(op, dtype, G, rows, N, K)
-    return (torch.empty(n, dtype=torch.uint8, device=dev), n) if n else (None, 0)
-
-
-def _launch(dev, call):
-    """call() with dev current (a stream belongs to its device)."""
-    import torch
-
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(call())
-    else:
-        with torch.cuda.device(dev):
-            _check(call())
+    if n == 0:
+        return None, None, 0
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    return ws, ws.data_ptr(), n
 
 
 def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, workspace=None, out=None):
@@ -435,15 +452,15 @@ def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, worksp
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be [rows, K] and w [G, N, K]")
     G, N, K = w.shape
+    x_rows = x.shape[0]
     _want(w, "w", (G, N, x.shape[1]), x.dtype)
     _groups(group_offsets, row_index, G)
-    rows = x.shape[0] if row_index is None else row_index.shape[0]
-    dev, stream = _one_device(x, w, group_offsets, row_index, workspace, out)
+    rows = x_rows if row_index is None else row_index.shape[0]
+    dev = _one_device(x, w, group_offsets, row_index, workspace, out)
     y, ydt = _out(out, (rows, N), y_dtype, dt, dev)
-    ws, nb = _matmul_ws(workspace, MOE_MATMUL_FORWARD, dt, G, rows, N, K, dev)
-    _launch(dev, lambda: load_library().moe_grouped_matmul(dt, G, N, K, _ptr(group_offsets), rows, _ptr(x), x.shape[0],
-                                                           _ptr(row_index), _ptr(w), _ptr(y), ydt, _ptr(ws), nb,
-                                                           stream))
+    ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_FORWARD, dt, G, rows, N, K, dev)
+    _launch(dev, load_library().moe_grouped_matmul, dt, G, N, K, _addr(group_offsets), rows, x.data_ptr(), x_rows,
+            _addr(row_index), w.data_ptr(), y.data_ptr(), ydt, wp, nb)
     return y
 
 
@@ -454,14 +471,14 @@ def moe_grouped_matmul_dx(dy, w, group_offsets, dx_dtype=None, workspace=None, o
     if dy.dim() != 2 or w.dim() != 3:
         raise ValueError("dy must be [rows, N] and w [G, N, K]")
     G, N, K = w.shape
+    rows = dy.shape[0]
     _want(w, "w", (G, dy.shape[1], K), dy.dtype)
     _groups(group_offsets, None, G)
-    rows = dy.shape[0]
-    dev, stream = _one_device(dy, w, group_offsets, workspace, out)
+    dev = _one_device(dy, w, group_offsets, workspace, out)
     dx, odt = _out(out, (rows, K), dx_dtype, dt, dev)
-    ws, nb = _matmul_ws(workspace, MOE_MATMUL_DX, dt, G, rows, N, K, dev)
-    _launch(dev, lambda: load_library().moe_grouped_matmul_dx(dt, G, N, K, _ptr(group_offsets), rows, _ptr(dy), _ptr(w),
-                                                              _ptr(dx), odt, _ptr(ws), nb, stream))
+    ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_DX, dt, G, rows, N, K, dev)
+    _launch(dev, load_library().moe_grouped_matmul_dx, dt, G, N, K, _addr(group_offsets), rows, dy.data_ptr(),
+            w.data_ptr(), dx.data_ptr(), odt, wp, nb)
     return dx
 
 
@@ -476,12 +493,11 @@ def moe_grouped_matmul_dw(dy, x, group_offsets, row_index=None, dw_dtype=None, w
     (rows, N), (x_rows, K) = dy.shape, x.shape
     if (x_rows if row_index is None else row_index.shape[0]) != rows:
         raise ValueError(f"dy has {rows} rows, x (or row_index) {x_rows if row_index is None else row_index.shape[0]}")
-    dev, stream = _one_device(dy, x, group_offsets, row_index, workspace, out)
+    dev = _one_device(dy, x, group_offsets, row_index, workspace, out)
     dw, odt = _out(out, (G, N, K), dw_dtype, dt, dev)
-    ws, nb = _matmul_ws(workspace, MOE_MATMUL_DW, dt, G, rows, N, K, dev)
-    _launch(dev, lambda: load_library().moe_grouped_matmul_dw(dt, G, N, K, _ptr(group_offsets), rows, _ptr(dy), _ptr(x),
-                                                              x_rows, _ptr(row_index), _ptr(dw), odt, _ptr(ws), nb,
-                                                              stream))
+    ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_DW, dt, G, rows, N, K, dev)
+    _launch(dev, load_library().moe_grouped_matmul_dw, dt, G, N, K, _addr(group_offsets), rows, dy.data_ptr(),
+            x.data_ptr(), x_rows, _addr(row_index), dw.data_ptr(), odt, wp, nb)
     return dw
 
 
@@ -494,13 +510,17 @@ def moe_quantize_rows(x, swiglu=False, codes=None, scales=None):
     if x.dim() != 2 or (swiglu and x.shape[1] % 2):
         raise ValueError("x must be [rows, cols] (swiglu: [rows, 2 cols])")
     rows, cols = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
-    dev, stream = _one_device(x, codes, scales)
-    codes = codes if codes is not None else torch.empty((rows, cols), dtype=torch.int8, device=dev)
-    scales = scales if scales is not None else torch.empty(rows, dtype=torch.float32, device=dev)
-    _want(codes, "codes", (rows, cols), torch.int8)
-    _want(scales, "scales", (rows,), torch.float32)
-    _launch(dev, lambda: load_library().moe_quantize_rows(dt, rows, cols, int(bool(swiglu)), _ptr(x), _ptr(codes),
-                                                          _ptr(scales), stream))
+    dev = _one_device(x, codes, scales)
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    else:
+        _want(codes, "codes", (rows, cols), torch.int8)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _want(scales, "scales", (rows,), torch.float32)
+    _launch(dev, load_library().moe_quantize_rows, dt, rows, cols, 1 if swiglu else 0, x.data_ptr(), codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
@@ -516,18 +536,19 @@ def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_
     if x_codes.dim() != 2 or w_codes.dim() != 3:
         raise ValueError("x_codes must be [rows, K] and w_codes [G, N, K]")
     G, N, K = w_codes.shape
-    _want(x_codes, "x_codes", (x_codes.shape[0], K), torch.int8)
+    x_rows = x_codes.shape[0]
+    _want(x_codes, "x_codes", (x_rows, K), torch.int8)
     _want(w_codes, "w_codes", (G, N, K), torch.int8)
-    _want(x_scales, "x_scales", (x_codes.shape[0],), torch.float32)
+    _want(x_scales, "x_scales", (x_rows,), torch.float32)
     _want(w_scales, "w_scales", (G, N), torch.float32)
     _groups(group_offsets, row_index, G)
-    rows = x_codes.shape[0] if row_index is None else row_index.shape[0]
-    dev, stream = _one_device(x_codes, x_scales, w_codes, w_scales, group_offsets, row_index, workspace, out)
+    rows = x_rows if row_index is None else row_index.shape[0]
+    dev = _one_device(x_codes, x_scales, w_codes, w_scales, group_offsets, row_index, workspace, out)
     y, ydt = _out(out, (rows, N), y_dtype if out is None else None, MOE_BF16, dev)
-    ws, nb = _matmul_ws(workspace, MOE_MATMUL_I8, MOE_F32, G, rows, N, K, dev)
-    _launch(dev, lambda: load_library().moe_matmul_i8(G, N, K, _ptr(group_offsets), rows, _ptr(x_codes), _ptr(x_scales),
-                                                      x_codes.shape[0], _ptr(row_index), _ptr(w_codes), _ptr(w_scales),
-                                                      _ptr(y), ydt, _ptr(ws), nb, stream))
+    ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_I8, MOE_F32, G, rows, N, K, dev)
+    _launch(dev, load_library().moe_matmul_i8, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
+            x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
+            nb)
     return y
 
 

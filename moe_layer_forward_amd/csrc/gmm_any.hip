@@ -1,22 +1,21 @@
 // Grouped matrix products for any sizes, alignment and type: the kernel of the fp32 products and of rows
 // that are not whole 16-byte pieces.
 //
-// Tile 128 x 128, 4 waves in 2 x 2; a wave owns every other 16-row block of the P rows and 64 Q columns (4 x 4
-// accumulator blocks), and skips the blocks that its group has no rows for.  Both operands are read
-// into registers one step ahead, 16 bytes a lane at whatever alignment the rows have, with the ends of
-// rows filled with zeros element by element, and stored into one of two LDS stages while the other is
-// multiplied.  Contraction indices past the end are zero in both operands, so no neighbouring row's
-// values, finite or not, enter a sum.  Outputs leave through LDS as 16-byte pieces of rows.
-// Two work-groups share a CU (64 KiB of LDS each).  Bound: fp32 by v_mfma_f32_16x16x4_f32 (256 FLOP a
-// clock and CU); odd rows by the loads and their trip through registers.
+// Tile kTile x kTile (128 or 64), 4 waves in 2 x 2; a wave owns every other 16-row block of the P rows and half
+// the Q columns (4 x 4 or 2 x 2 accumulator blocks), and skips the blocks that its group has no rows for.
+// Both operands are read into registers two steps ahead, 16 bytes a lane at whatever alignment the rows
+// have, with the ends of rows filled with zeros element by element, and stored into one of two LDS
+// stages while the other is multiplied.  Contraction indices past the end are zero in both operands, so
+// no neighbouring row's values, finite or not, enter a sum.  Outputs leave through LDS as 16-byte
+// pieces of rows.  Two (128) or more (64) work-groups share a CU.  Bound: fp32 by
+// v_mfma_f32_16x16x4_f32 (256 FLOP a clock and CU); odd rows by the loads and their trip through registers;
+// small calls by the latency of a step's loads.
 #include "gmm_core.h"
 
 namespace moe {
 namespace {
 
-constexpr int kAnyTile = 128;
 constexpr int kAnyThreads = 256;
-constexpr int kAnyStage = kAnyTile * kGmmStepBytes;  // 16 KiB
 
 // nv of the n elements at p (n = 16 bytes of them), zeros after them.
 template <class T>
@@ -40,13 +39,14 @@ __device__ __forceinline__ gmm_u32x4 load_chunk(const char* p, int nv) {
   return v;
 }
 
-// One operand's share of a thread: 4 chunks of a stage (1024 chunks over 256 threads).
+// One operand's share of a thread: kC chunks of a stage (kTile rows of 8 chunks over 256 threads).
 // L = GmmAlong: chunk q is chunk q % 8 of tile row q / 8, whose elements run along the contraction.
 // L = GmmAcross: chunk q is columns of contraction row q / kChunks.
 template <class T, class L>
 struct AnyOperand {
   static constexpr int kN = 16 / T::kBytes;
-  const char* ptr[4];       // Along: the chunk's row, at its chunk of step 0.  Across (not gathered): likewise
+  static constexpr int kC = L::kStageBytes / 16 / kAnyThreads;
+  const char* ptr[kC];      // Along: the chunk's row, at its chunk of step 0.  Across (not gathered): likewise
   int n;                    // Along: elements of the row from the chunk of step 0 on.  Across: of the columns
   int have;                 // Along: bit j: the row of chunk j exists
   int64_t ld;               // Across: bytes between contraction rows
@@ -62,7 +62,7 @@ struct AnyOperand {
     n = depth_ - c;
     have = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kC; ++j) {
       const int r = (threadIdx.x + kAnyThreads * j) / L::kChunks;
       ptr[j] = b + (r < rows ? row_of(r) : 0) * ld_ + c * T::kBytes;
       have |= (r < rows) << j;
@@ -80,12 +80,12 @@ struct AnyOperand {
     index_last = (int32_t)index_rows - 1;
     base = b + (col0 + c) * T::kBytes;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ptr[j] = base + (int64_t)((threadIdx.x + kAnyThreads * j) / L::kChunks) * ld;
+    for (int j = 0; j < kC; ++j) ptr[j] = base + (int64_t)((threadIdx.x + kAnyThreads * j) / L::kChunks) * ld;
   }
 
-  __device__ __forceinline__ void load(int kt, gmm_u32x4 (&v)[4]) const {
+  __device__ __forceinline__ void load(int kt, gmm_u32x4 (&v)[kC]) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kC; ++j) {
       v[j] = gmm_u32x4{0, 0, 0, 0};
       if constexpr (L::kAlong) {
         const int nv = (have >> j) & 1 ? n - kt * (kGmmStepBytes / T::kBytes) : 0;
@@ -104,44 +104,46 @@ struct AnyOperand {
       }
     }
   }
-  __device__ static __forceinline__ void store(char* stage, const gmm_u32x4 (&v)[4]) {
+  __device__ static __forceinline__ void store(char* stage, const gmm_u32x4 (&v)[kC]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kC; ++j) {
       const int q = threadIdx.x + kAnyThreads * j;
       *reinterpret_cast<gmm_u32x4*>(stage + L::pos(q / L::kChunks, q % L::kChunks)) = v[j];
     }
   }
 };
 
-template <GmmForm F, class T>
-__global__ __launch_bounds__(kAnyThreads, 2) void gmm_any_kernel(GmmArgs a) {
-  using LP = GmmP<F, T, kAnyTile>;
-  using LQ = GmmQ<F, T, kAnyTile>;
+template <GmmForm F, class T, int kTile>
+__global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_kernel(GmmArgs a) {
+  using LP = GmmP<F, T, kTile>;
+  using LQ = GmmQ<F, T, kTile>;
+  constexpr int kAnyStage = kTile * kGmmStepBytes, kB = kTile / 32;  // 16-blocks of a wave's rows and columns
+  constexpr int kOutRow = kTile * 4;                                 // bytes of a staged output row
   static_assert(LP::kStageBytes == kAnyStage && LQ::kStageBytes == kAnyStage, "stages");
   __shared__ __align__(16) char lds[4 * kAnyStage];  // P stages 0, 1, Q stages 0, 1; then the output tile
 
   // which tile: NT / NN a row tile of a group x a column slab, TN a (group, n tile, k tile); which range
   const int64_t q_len = F == GmmForm::kNT ? a.N : a.K;
-  const int q_tiles = (int)((q_len + kAnyTile - 1) / kAnyTile);
+  const int q_tiles = (int)((q_len + kTile - 1) / kTile);
   const int sp = (int)(blockIdx.x % (unsigned)a.split);
   const int64_t item = blockIdx.x / (unsigned)a.split;
   const int64_t t = item / q_tiles;
-  const int64_t q0 = (item % q_tiles) * kAnyTile;
+  const int64_t q0 = (item % q_tiles) * kTile;
   int g;
   int64_t beg, end, p0 = 0;
   if constexpr (F == GmmForm::kTN) {
-    const int64_t p_tiles = ((int64_t)a.N + kAnyTile - 1) / kAnyTile;
+    const int64_t p_tiles = ((int64_t)a.N + kTile - 1) / kTile;
     g = (int)(t / p_tiles);
-    p0 = (t % p_tiles) * kAnyTile;
+    p0 = (t % p_tiles) * kTile;
     gmm_group_rows(a.group_offsets, a.max_rows, g, beg, end);
   } else {
-    if (!gmm_find_tile(a.group_offsets, a.G, a.max_rows, kAnyTile, t, g, beg, end)) return;
+    if (!gmm_find_tile(a.group_offsets, a.G, a.max_rows, kTile, t, g, beg, end)) return;
     beg = gmm_uniform((int)beg);
     end = gmm_uniform((int)end);
   }
   // output rows of this tile (TN: columns of dy, rows of dW[g])
-  const int rows = (int)(F == GmmForm::kTN ? (a.N - p0 < kAnyTile ? a.N - p0 : kAnyTile) : end - beg);
-  const int cols = (int)(q_len - q0 < kAnyTile ? q_len - q0 : kAnyTile);
+  const int rows = (int)(F == GmmForm::kTN ? (a.N - p0 < kTile ? a.N - p0 : kTile) : end - beg);
+  const int cols = (int)(q_len - q0 < kTile ? q_len - q0 : kTile);
   const int64_t ldn = (int64_t)a.N * T::kBytes, ldk = (int64_t)a.K * T::kBytes;
   const char* w = static_cast<const char*>(a.w);
   if (F != GmmForm::kTN) w += (int64_t)g * a.N * ldk;
@@ -175,64 +177,76 @@ __global__ __launch_bounds__(kAnyThreads, 2) void gmm_any_kernel(GmmArgs a) {
   GmmFrags<LP, 2> fp;
   fp.init(wr);
   GmmFrags<LQ, 1> fq;
-  fq.init(4 * wc);
-  typename T::Acc acc[4][4];
+  fq.init(kB * wc);
+  typename T::Acc acc[kB][kB];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kB; ++i)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) acc[i][s] = typename T::Acc{0, 0, 0, 0};
+    for (int s = 0; s < kB; ++s) acc[i][s] = typename T::Acc{0, 0, 0, 0};
 
   constexpr int kStep = kGmmStepBytes / T::kBytes;
   int first, nk;
   gmm_range(gmm_uniform((depth + kStep - 1) / kStep), a.split, sp, first, nk);
-  gmm_u32x4 pv[4], qv[4];
+  using OP = AnyOperand<T, LP>;
+  using OQ = AnyOperand<T, LQ>;
+  gmm_u32x4 pv[2][OP::kC], qv[2][OQ::kC];  // steps kt + 1 and kt + 2, by parity of the step
   if (nk > 0) {
-    p.load(first, pv);
-    q.load(first, qv);
-    p.store(lds, pv);
-    q.store(lds + 2 * kAnyStage, qv);
+    p.load(first, pv[0]);
+    q.load(first, qv[0]);
+  }
+  if (nk > 1) {
+    p.load(first + 1, pv[1]);
+    q.load(first + 1, qv[1]);
+  }
+  if (nk > 0) {
+    OP::store(lds, pv[0]);
+    OQ::store(lds + 2 * kAnyStage, qv[0]);
   }
   __syncthreads();
-  for (int kt = 0; kt < nk; ++kt) {
-    const int cur = kt & 1;
+  const auto step = [&](int kt, auto parity) {
+    constexpr int cur = decltype(parity)::value;
     const char *ps = lds + cur * kAnyStage, *qs = lds + (2 + cur) * kAnyStage;
-    if (kt + 1 < nk) {
-      p.load(first + kt + 1, pv);
-      q.load(first + kt + 1, qv);
+    if (kt + 2 < nk) {
+      p.load(first + kt + 2, pv[cur]);
+      q.load(first + kt + 2, qv[cur]);
     }
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      gmm_u32x4 qf[4];
+      gmm_u32x4 qf[kB];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) qf[s] = fq.read(qs, s, kk);
+      for (int s = 0; s < kB; ++s) qf[s] = fq.read(qs, s, kk);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kB; ++i) {
         if (wr + 2 * i < blocks) {
           const gmm_u32x4 pf = fp.read(ps, i, kk);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) acc[i][s] = T::mfma(qf[s], pf, acc[i][s]);
+          for (int s = 0; s < kB; ++s) acc[i][s] = T::mfma(qf[s], pf, acc[i][s]);
         }
       }
     }
     if (kt + 1 < nk) {
-      p.store(lds + (cur ^ 1) * kAnyStage, pv);
-      q.store(lds + (2 + (cur ^ 1)) * kAnyStage, qv);
+      OP::store(lds + (cur ^ 1) * kAnyStage, pv[cur ^ 1]);
+      OQ::store(lds + (2 + (cur ^ 1)) * kAnyStage, qv[cur ^ 1]);
     }
     __syncthreads();
+  };
+  for (int kt = 0; kt < nk; kt += 2) {
+    step(kt, std::integral_constant<int, 0>{});
+    if (kt + 1 < nk) step(kt + 1, std::integral_constant<int, 1>{});
   }
 
-  // The output tile through LDS, as fp32 (int32 partial sums as they are): row r of 512 bytes, its 16-byte
-  // piece c at c ^ (r & 15); the last barrier above freed the stages.
+  // The output tile through LDS, as fp32 (int32 partial sums as they are): row r of kOutRow bytes, its
+  // 16-byte piece c at c ^ (r & 15); the last barrier above freed the stages.
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kB; ++i) {
     const int r = 16 * (wr + 2 * i) + (lane & 15);
     if (wr + 2 * i < blocks) {
       float sx = 1.f;
       if constexpr (std::is_same_v<T, GmmI8>)
         if (a.split == 1) sx = a.x_scales[x_row(r < rows ? r : rows - 1)];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int col = 16 * (4 * wc + s) + 4 * (lane >> 4);
+      for (int s = 0; s < kB; ++s) {
+        const int col = 16 * (kB * wc + s) + 4 * (lane >> 4);
         f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -244,7 +258,7 @@ __global__ __launch_bounds__(kAnyThreads, 2) void gmm_any_kernel(GmmArgs a) {
             v[e] = acc[i][s][e];
           }
         }
-        *reinterpret_cast<f32x4*>(lds + r * 512 + (((col >> 2) ^ (r & 15)) << 4)) = v;
+        *reinterpret_cast<f32x4*>(lds + r * kOutRow + (((col >> 2) ^ (r & 15)) << 4)) = v;
       }
     }
   }
@@ -255,13 +269,13 @@ __global__ __launch_bounds__(kAnyThreads, 2) void gmm_any_kernel(GmmArgs a) {
   char* out = a.split == 1 ? static_cast<char*>(a.out) : reinterpret_cast<char*>(a.part + sp * out_rows * q_len);
   out += (out_row * q_len + q0) * (bf16 ? 2 : 4);
   // 8 columns a thread, at the alignment that the row has
-  for (int ch = threadIdx.x; ch < rows * 16; ch += kAnyThreads) {
-    const int r = ch >> 4, c = (ch & 15) * 8;
+  for (int ch = threadIdx.x; ch < rows * (kTile / 8); ch += kAnyThreads) {
+    const int r = ch / (kTile / 8), c = (ch % (kTile / 8)) * 8;
     if (c >= cols) continue;
     f32x4 v[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      v[h] = *reinterpret_cast<const f32x4*>(lds + r * 512 + (((c / 4 + h) ^ (r & 15)) << 4));
+      v[h] = *reinterpret_cast<const f32x4*>(lds + r * kOutRow + (((c / 4 + h) ^ (r & 15)) << 4));
     const int n = cols - c;
     if (bf16) {
       uint16_t h[8];
@@ -370,32 +384,36 @@ __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
 }
 
 template <GmmForm F, class T>
-hipError_t launch_any(const GmmArgs& a, hipStream_t s) {
-  gmm_any_kernel<F, T><<<dim3((unsigned)(gmm_any_grid(a) * a.split)), dim3(kAnyThreads), 0, s>>>(a);
+hipError_t launch_any(const GmmArgs& a, int tile, hipStream_t s) {
+  const dim3 grid((unsigned)(gmm_any_grid(a, tile) * a.split)), block(kAnyThreads);
+  if (tile == 64)
+    gmm_any_kernel<F, T, 64><<<grid, block, 0, s>>>(a);
+  else
+    gmm_any_kernel<F, T, 128><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gmm_any_grid(const GmmArgs& a) {
-  const int64_t q_tiles = ((a.form == GmmForm::kNT ? a.N : a.K) + kAnyTile - 1) / kAnyTile;
-  const int64_t p_tiles = a.form == GmmForm::kTN ? (int64_t)a.G * ((a.N + kAnyTile - 1) / kAnyTile)
-                                                 : gmm_max_tiles(a.max_rows, a.G, kAnyTile);
+int64_t gmm_any_grid(const GmmArgs& a, int tile) {
+  const int64_t q_tiles = ((a.form == GmmForm::kNT ? a.N : a.K) + tile - 1) / tile;
+  const int64_t p_tiles = a.form == GmmForm::kTN ? (int64_t)a.G * ((a.N + tile - 1) / tile)
+                                                 : gmm_max_tiles(a.max_rows, a.G, tile);
   return p_tiles * q_tiles;
 }
 
-hipError_t launch_gmm_any(const GmmArgs& a, hipStream_t s) {
+hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s) {
   switch (a.form) {
     case GmmForm::kNT:
-      if (a.type == GmmType::kI8) return launch_any<GmmForm::kNT, GmmI8>(a, s);
-      return a.type == GmmType::kBf16 ? launch_any<GmmForm::kNT, GmmBf16>(a, s)
-                                      : launch_any<GmmForm::kNT, GmmF32>(a, s);
+      if (a.type == GmmType::kI8) return launch_any<GmmForm::kNT, GmmI8>(a, tile, s);
+      return a.type == GmmType::kBf16 ? launch_any<GmmForm::kNT, GmmBf16>(a, tile, s)
+                                      : launch_any<GmmForm::kNT, GmmF32>(a, tile, s);
     case GmmForm::kNN:
-      return a.type == GmmType::kBf16 ? launch_any<GmmForm::kNN, GmmBf16>(a, s)
-                                      : launch_any<GmmForm::kNN, GmmF32>(a, s);
+      return a.type == GmmType::kBf16 ? launch_any<GmmForm::kNN, GmmBf16>(a, tile, s)
+                                      : launch_any<GmmForm::kNN, GmmF32>(a, tile, s);
     default:
-      return a.type == GmmType::kBf16 ? launch_any<GmmForm::kTN, GmmBf16>(a, s)
-                                      : launch_any<GmmForm::kTN, GmmF32>(a, s);
+      return a.type == GmmType::kBf16 ? launch_any<GmmForm::kTN, GmmBf16>(a, tile, s)
+                                      : launch_any<GmmForm::kTN, GmmF32>(a, tile, s);
   }
 }
 

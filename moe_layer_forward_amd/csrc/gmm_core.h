@@ -86,8 +86,9 @@ struct GmmAlong {
 // or 32 fp32 of them), OUTER columns wide.
 //   bf16: a fragment is two ds_read_b64_tr_b16.  Each transposes a 4 x 16 block per 16 lanes: lane i
 //     names 4 columns (i % 4) of row i / 4 and receives column i of the 4 rows.  The 16 columns of a
-//     block are one 32-byte unit; unit u of row r sits at u ^ s(r), s = (r & 3) | (r >> 1 & 4), so that
-//     the 8 rows x 32 bytes that 32 lanes read fall in all 64 banks.
+//     block are one 32-byte unit; unit u of row r sits at u ^ s(r), s = (r & 3) | (r >> 1 & 4) (rows
+//     of 128 bytes, two to a turn of the banks: (r >> 1 & 1) | (r >> 2 & 2)), so that the 8 rows x 32
+//     bytes that 32 lanes read, rows 8 g + 0..3 for two g, fall in all 64 banks.
 //   fp32: a fragment is four 4-byte reads (element t from row 4 (l / 16) + t); the 16 columns are one
 //     64-byte unit, at u ^ (r >> 2 & 3), so that the four rows of one read fall in all 64 banks.
 template <class T, int OUTER>
@@ -98,9 +99,10 @@ struct GmmAcross {
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kStageBytes = kRows * kRowBytes;
   static constexpr int kUnit = 16 * T::kBytes;  // bytes of 16 columns
-  static_assert(T::kBytes == 2 || T::kBytes == 4, "types");
+  static_assert((T::kBytes == 2 || T::kBytes == 4) && OUTER % 64 == 0, "types");
   __device__ static __forceinline__ int swz(int r) {
-    return T::kBytes == 2 ? (r & 3) | ((r >> 1) & 4) : (r >> 2) & 3;
+    if constexpr (T::kBytes == 4) return (r >> 2) & 3;
+    return kRowBytes >= 256 ? (r & 3) | ((r >> 1) & 4) : ((r >> 1) & 1) | ((r >> 2) & 2);
   }
   // chunk that belongs at chunk position p of row r, and (the same involution) the position of chunk c
   __device__ static __forceinline__ int chunk_at(int r, int p) {

@@ -41,13 +41,19 @@ int64_t max_steps(const GmmArgs& a) {
   return (depth * elem_bytes(a) + 127) / 128;
 }
 
-int any_split(const GmmArgs& a) { return split_of(gmm_any_grid(a), max_steps(a), 2 * kCus); }
+// Small tiles where the large ones would leave slots (two on a CU) empty.
+int any_tile(const GmmArgs& a) { return gmm_any_grid(a, 128) < 2 * kCus ? 64 : 128; }
+int any_split(const GmmArgs& a) {
+  const int tile = any_tile(a);
+  return split_of(gmm_any_grid(a, tile), max_steps(a), (tile == 64 ? 4 : 2) * kCus);
+}
 int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a), max_steps(a), kCus); }
 
 }  // namespace
 
-// Work-groups of 512 threads or fewer, a dealt grid at most twice the tiles.
-bool gmm_grid_ok(const GmmArgs& a) { return 2 * 512 * gmm_any_grid(a) < (int64_t(1) << 32); }
+// Grids of at most 2^32 threads: the 64 x 64 tiles are the most work-groups (of 256 threads); the 256 x 256 ones
+// (512 threads) are fewer even where their number is rounded up to twice.
+bool gmm_grid_ok(const GmmArgs& a) { return 512 * gmm_any_grid(a, 64) < (int64_t(1) << 32); }
 
 size_t gmm_workspace(const GmmArgs& a) {
   const int split = std::max(any_split(a), tile_sizes(a) ? tile_split(a) : 1);
@@ -61,7 +67,7 @@ hipError_t launch_gmm(const GmmArgs& args, void* workspace, hipStream_t s) {
   a.part = static_cast<float*>(workspace);
   hipError_t e;
   if (!tile)
-    e = launch_gmm_any(a, s);
+    e = launch_gmm_any(a, any_tile(a), s);
   else if (a.form == GmmForm::kNN)
     e = launch_gmm_tile_nn(a, s);
   else if (a.form == GmmForm::kTN)

@@ -260,9 +260,9 @@ hipError_t launch_gmm(const GmmArgs& a, void* workspace, hipStream_t s);
 size_t gmm_workspace(const GmmArgs& a);
 // Whether every kernel's grid fits a launch (fewer than 2^32 threads).
 bool gmm_grid_ok(const GmmArgs& a);
-// Any sizes and any element alignment.
-hipError_t launch_gmm_any(const GmmArgs& a, hipStream_t s);
-int64_t gmm_any_grid(const GmmArgs& a);
+// Any sizes and any element alignment, in tiles of 64 x 64 or 128 x 128 (gmm_any_grid of them at most).
+hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s);
+int64_t gmm_any_grid(const GmmArgs& a, int tile);
 int64_t gmm_tile_items(const GmmArgs& a);
 // 256 x 256 tiles on rows of whole 16-byte pieces (bf16; int8 for the forward).
 hipError_t launch_gmm_tile_nt(const GmmArgs& a, hipStream_t s);
