@@ -137,9 +137,10 @@ __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_ker
     p0 = (t % p_tiles) * kTile;
     gmm_group_rows(a.group_offsets, a.max_rows, g, beg, end);
   } else {
-    if (!gmm_find_tile(a.group_offsets, a.G, a.max_rows, kTile, t, g, beg, end)) return;
-    beg = gmm_uniform((int)beg);
-    end = gmm_uniform((int)end);
+    GmmTiles tiles;
+    tiles.count(a.group_offsets, a.G, a.max_rows, kTile);
+    if (t >= tiles.full + tiles.partial) return;
+    tiles.find(a.group_offsets, a.G, a.max_rows, kTile, (int)t, g, beg, end);
   }
   // output rows of this tile (TN: columns of dy, rows of dW[g])
   const int rows = (int)(F == GmmForm::kTN ? (a.N - p0 < kTile ? a.N - p0 : kTile) : end - beg);

@@ -194,59 +194,67 @@ __device__ __forceinline__ void gmm_group_rows(const int32_t* off, int64_t max_r
   end = end < beg ? beg : end > max_rows ? max_rows : end;
 }
 
-// The t-th row tile of bm rows, counting every group's tiles in group order: its group and rows.  Every
-// wave of the work-group finds it by itself: lane l sums the tile counts of ceil(G / 64) consecutive
-// groups, a scan over the lanes finds the lane, and the wave walks that lane's groups.  No plan launch
-// and no workspace; G = 384 costs six loads per lane.  False past the last tile.
-__device__ __forceinline__ bool gmm_find_tile(const int32_t* off, int G, int64_t max_rows, int bm, int64_t t, int& g,
-                                              int64_t& beg, int64_t& end) {
-  if (!off || G == 1) {
-    g = 0;
-    gmm_group_rows(off, max_rows, 0, beg, end);
-    beg += t * bm;
-    if (beg >= end) return false;
-    end = beg + bm < end ? beg + bm : end;
+// The row tiles of the groups, bm rows each: the full ones first (in group order), then every group's last,
+// partial one.  Every wave of a work-group counts and finds them by itself: lane l sums over ceil(G / 64)
+// consecutive groups, a scan over the lanes finds the lane, and the wave walks that lane's groups.  No
+// plan launch and no workspace; G = 384 costs six loads per lane.
+struct GmmTiles {
+  int full = 0, partial = 0;        // tiles of the call
+  int full_to = 0, partial_to = 0;  // up to and including this lane's groups
+  int full_n = 0, partial_n = 0;    // of this lane's groups
+
+  __device__ __forceinline__ void count(const int32_t* off, int G, int64_t max_rows, int bm) {
+    const int lane = threadIdx.x & 63;
+    const int per = (G + 63) / 64;
+    for (int j = 0; j < per; ++j) {
+      const int gg = lane * per + j;
+      if (gg < G) {
+        int64_t b, e;
+        gmm_group_rows(off, max_rows, gg, b, e);
+        const int rows = (int)(e - b);
+        full_n += rows / bm;
+        partial_n += rows % bm != 0;
+      }
+    }
+    full_to = full_n;
+    partial_to = partial_n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int f = __shfl_up(full_to, d, 64), p = __shfl_up(partial_to, d, 64);
+      if (lane >= d) {
+        full_to += f;
+        partial_to += p;
+      }
+    }
+    full = __builtin_amdgcn_readlane(full_to, 63);
+    partial = __builtin_amdgcn_readlane(partial_to, 63);
+  }
+
+  // Tile t (below full + partial): its group and rows.
+  __device__ __forceinline__ void find(const int32_t* off, int G, int64_t max_rows, int bm, int t, int& g,
+                                       int64_t& beg, int64_t& end) const {
+    const bool is_full = t < full;
+    int rel = is_full ? t : t - full;
+    const int to = is_full ? full_to : partial_to, n = is_full ? full_n : partial_n;
+    const int owner = __ffsll((unsigned long long)__ballot(to > rel)) - 1;
+    rel -= __builtin_amdgcn_readlane(to - n, owner);
+    const int per = (G + 63) / 64;
+    g = owner * per;
+    int64_t b, e;
+    for (;; ++g) {  // ends inside this lane's groups, whose tiles number more than rel
+      gmm_group_rows(off, max_rows, g, b, e);
+      const int rows = (int)(e - b), k = is_full ? rows / bm : rows % bm != 0;
+      if (rel < k || g + 1 >= G) break;
+      rel -= k;
+    }
+    const int64_t rows = e - b;
+    g = __builtin_amdgcn_readfirstlane(g);
+    beg = is_full ? b + (int64_t)rel * bm : b + rows / bm * bm;
+    end = is_full ? beg + bm : e;
     beg = __builtin_amdgcn_readfirstlane((int)beg);  // rows fit 31 bits
     end = __builtin_amdgcn_readfirstlane((int)end);
-    return true;
   }
-  const int lane = threadIdx.x & 63;
-  const int per = (G + 63) / 64;
-  int n = 0;
-  for (int j = 0; j < per; ++j) {
-    const int gg = lane * per + j;
-    if (gg < G) {
-      int64_t b, e;
-      gmm_group_rows(off, max_rows, gg, b, e);
-      n += (int)((e - b + bm - 1) / bm);
-    }
-  }
-  int incl = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += v;
-  }
-  const uint64_t past = __ballot((int64_t)incl > t);
-  if (!past) return false;
-  const int owner = __ffsll((unsigned long long)past) - 1;
-  int64_t rel = t - __shfl(incl - n, owner, 64);
-  for (int j = 0; j < per; ++j) {
-    const int gg = owner * per + j;
-    if (gg >= G) return false;
-    int64_t b, e;
-    gmm_group_rows(off, max_rows, gg, b, e);
-    const int64_t tiles = (e - b + bm - 1) / bm;
-    if (rel < tiles) {
-      g = __builtin_amdgcn_readfirstlane(gg);
-      beg = __builtin_amdgcn_readfirstlane((int)(b + rel * bm));  // rows fit 31 bits
-      end = __builtin_amdgcn_readfirstlane((int)(b + (rel + 1) * bm < e ? b + (rel + 1) * bm : e));
-      return true;
-    }
-    rel -= tiles;
-  }
-  return false;
-}
+};
 
 // Share sp of nk contraction steps cut into `split` nearly equal ranges.
 __device__ __forceinline__ void gmm_range(int nk, int split, int sp, int& first, int& n) {

@@ -316,28 +316,58 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
   });
 }
 
-// Work item of this work-group among tiles x slabs (tiles: row tiles; TN: a group's n tiles).  The hardware
-// deals work-group b to XCD b % 8.  With 8 kGmmSuper tiles or more, blocks of kGmmSuper consecutive tiles are
-// dealt to the XCDs and run slab by slab with their tiles side by side: 32 work-groups of an XCD then
-// share kGmmSuper row tiles and 8 slabs in its L2.  With fewer, items go out in order, so that (8 slabs or
-// more) every tile's slab j runs on XCD j % 8.  False for padding.
-__device__ __forceinline__ bool gmm_item(int64_t b, int64_t tiles, int slabs, int64_t& tile, int& slab) {
-  if (tiles < kXcds * kGmmSuper) {
-    tile = b / slabs;
-    slab = (int)(b % slabs);
-    return tile < tiles;
-  }
-  const int64_t local = b / kXcds, blk = local / ((int64_t)kGmmSuper * slabs);
-  const int rem = (int)(local % ((int64_t)kGmmSuper * slabs));
-  tile = (blk * kXcds + b % kXcds) * kGmmSuper + rem % kGmmSuper;
-  slab = rem / kGmmSuper;
-  return tile < tiles;
+// Work items are tiles x slabs, numbered so that kGmmSuper tiles run slab by slab, side by side: 32
+// work-groups of an XCD then share kGmmSuper tiles' rows and 8 slabs in its L2.
+__device__ __forceinline__ void gmm_unnumber(int64_t item, int64_t tiles, int slabs, int64_t& tile, int& slab) {
+  const int64_t sup = item / ((int64_t)kGmmSuper * slabs), first = sup * kGmmSuper;
+  const int rem = (int)(item - first * slabs);
+  const int n = tiles - first < kGmmSuper ? (int)(tiles - first) : kGmmSuper;
+  tile = first + rem % n;
+  slab = rem / n;
 }
 
-inline int64_t gmm_item_grid(int64_t tiles, int slabs) {
-  if (tiles < kXcds * kGmmSuper) return tiles * slabs;
-  const int64_t per = (int64_t)kXcds * kGmmSuper;
-  return (tiles + per - 1) / per * per * slabs;
+// The hardware deals work-group b to XCD b % 8.  The items of the full tiles are cut into one contiguous range per
+// XCD, and after them those of the partial tiles: every XCD gets the same share of both (to within one
+// item), and the short items come last, where they fill the chip's last round.  False for padding.
+__device__ __forceinline__ bool gmm_row_item(int64_t b, const GmmTiles& t, int slabs, int& tile, int& slab) {
+  const int64_t xcd = b % kXcds;
+  int64_t local = b / kXcds, nf = (int64_t)t.full * slabs, np = (int64_t)t.partial * slabs, tt;
+  const int64_t per_f = (nf + kXcds - 1) / kXcds, per_p = (np + kXcds - 1) / kXcds;
+  if (local < per_f) {
+    const int64_t item = xcd * per_f + local;
+    if (item >= nf) return false;
+    gmm_unnumber(item, t.full, slabs, tt, slab);
+    tile = (int)tt;
+    return true;
+  }
+  local -= per_f;
+  const int64_t item = xcd * per_p + local;
+  if (local >= per_p || item >= np) return false;
+  gmm_unnumber(item, t.partial, slabs, tt, slab);
+  tile = t.full + (int)tt;
+  return true;
+}
+
+// Work-groups that cover the items of any grouping of max_rows rows.
+inline int64_t gmm_row_grid(const GmmArgs& a, int slabs) {
+  const int64_t full = a.max_rows / kGmmTile, partial = a.max_rows < a.G ? a.max_rows : a.G;
+  const auto per = [&](int64_t tiles) { return (tiles * slabs + kXcds - 1) / kXcds; };
+  return (per(full) + per(partial)) * kXcds;
+}
+
+// TN: groups x n tiles x slabs, dealt to the XCDs in chunks of consecutive items (groups differ in length, so
+// that long contiguous ranges could leave XCDs idle): 32 of them, what an XCD runs at once, when every
+// XCD gets 4 chunks or more, else 8.
+__device__ __forceinline__ bool gmm_weight_item(int64_t b, int64_t tiles, int slabs, int chunk, int64_t& tile, int& slab) {
+  const int64_t local = b / kXcds, item = (local / chunk * kXcds + b % kXcds) * chunk + local % chunk;
+  if (item >= tiles * slabs) return false;
+  gmm_unnumber(item, tiles, slabs, tile, slab);
+  return true;
+}
+inline int gmm_weight_chunk(int64_t items) { return items >= 8 * 32 * 4 ? 32 : 8; }
+inline int64_t gmm_weight_grid(int64_t items) {
+  const int64_t turn = (int64_t)kXcds * gmm_weight_chunk(items);
+  return (items + turn - 1) / turn * turn;
 }
 
 #define MOE_GMM_SMEM                                                                                       \
@@ -432,14 +462,15 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
 
 template <GmmForm F, class T>
 __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void gmm_rows_kernel(GmmArgs a,
-                                                                                                     int64_t tiles,
                                                                                                      int slabs) {
   MOE_GMM_SMEM
-  int64_t t, beg, end;
-  int slab, g;
+  int64_t beg, end;
+  int t, slab, g;
   [[maybe_unused]] const int sp = (int)(blockIdx.x % (unsigned)a.split);
-  if (!gmm_item(blockIdx.x / (unsigned)a.split, tiles, slabs, t, slab)) return;
-  if (!gmm_find_tile(a.group_offsets, a.G, a.max_rows, kGmmTile, t, g, beg, end)) return;
+  GmmTiles tiles;
+  tiles.count(a.group_offsets, a.G, a.max_rows, kGmmTile);
+  if (!gmm_row_item(blockIdx.x / (unsigned)a.split, tiles, slabs, t, slab)) return;
+  tiles.find(a.group_offsets, a.G, a.max_rows, kGmmTile, t, g, beg, end);
 #if defined(__HIP_DEVICE_COMPILE__)
   const int64_t q0 = (int64_t)slab * kGmmTile;
   switch ((int)(end - beg + 31) / 32) {  // P blocks per wave
@@ -460,12 +491,12 @@ __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 
 // TN: output rows are columns of dy.
 template <class T, bool kGather>
 __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void gmm_weights_kernel(
-    GmmArgs a, int64_t tiles, int slabs, int p_tiles) {
+    GmmArgs a, int64_t tiles, int slabs, int p_tiles, int chunk) {
   MOE_GMM_SMEM
   int64_t t;
   int slab;
   [[maybe_unused]] const int sp = (int)(blockIdx.x % (unsigned)a.split);
-  if (!gmm_item(blockIdx.x / (unsigned)a.split, tiles, slabs, t, slab)) return;
+  if (!gmm_weight_item(blockIdx.x / (unsigned)a.split, tiles, slabs, chunk, t, slab)) return;
 #if defined(__HIP_DEVICE_COMPILE__)
   using L = GmmAcross<T, kGmmTile>;
   const int g = (int)(t / p_tiles);
@@ -511,9 +542,8 @@ __global__ __launch_bounds__(kGmmThreads) __attribute__((amdgpu_waves_per_eu(2, 
 
 template <GmmForm F, class T>
 hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
-  const int64_t tiles = gmm_max_tiles(a.max_rows, a.G, kGmmTile);
   const int slabs = ((F == GmmForm::kNT ? a.N : a.K) + kGmmTile - 1) / kGmmTile;
-  gmm_rows_kernel<F, T><<<dim3((unsigned)(gmm_item_grid(tiles, slabs) * a.split)), dim3(kGmmThreads), 0, s>>>(a, tiles, slabs);
+  gmm_rows_kernel<F, T><<<dim3((unsigned)(gmm_row_grid(a, slabs) * a.split)), dim3(kGmmThreads), 0, s>>>(a, slabs);
   return hipGetLastError();
 }
 
