@@ -1,5 +1,6 @@
 // Which kernel a grouped product runs on, and into how many ranges its contraction is cut.
 #include <algorithm>
+#include <cstdlib>
 
 #include "kernels.h"
 
@@ -47,7 +48,15 @@ int any_split(const GmmArgs& a) {
   const int tile = any_tile(a);
   return split_of(gmm_any_grid(a, tile), max_steps(a), (tile == 64 ? 4 : 2) * kCus);
 }
-int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a), max_steps(a), kCus); }
+// Waves of the tile kernel's work-groups.
+int tile_waves(const GmmArgs& a) {
+  if (const char* e = getenv("GMM_W")) return atoi(e);
+  return 8;
+}
+int tile_split(const GmmArgs& a) {
+  const int waves = tile_waves(a);
+  return split_of(gmm_tile_items(a, waves), max_steps(a), waves == 8 ? kCus : 2 * kCus);
+}
 
 }  // namespace
 
@@ -65,15 +74,16 @@ hipError_t launch_gmm(const GmmArgs& args, void* workspace, hipStream_t s) {
   const bool tile = tile_ok(a);
   a.split = tile ? tile_split(a) : any_split(a);
   a.part = static_cast<float*>(workspace);
+  const int waves = tile_waves(a);
   hipError_t e;
   if (!tile)
     e = launch_gmm_any(a, any_tile(a), s);
   else if (a.form == GmmForm::kNN)
-    e = launch_gmm_tile_nn(a, s);
+    e = launch_gmm_tile_nn(a, waves, s);
   else if (a.form == GmmForm::kTN)
-    e = launch_gmm_tile_tn(a, s);
+    e = launch_gmm_tile_tn(a, waves, s);
   else
-    e = a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, s) : launch_gmm_tile_nt(a, s);
+    e = a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, waves, s) : launch_gmm_tile_nt(a, waves, s);
   return e == hipSuccess && a.split > 1 ? launch_gmm_join(a, s) : e;
 }
 

@@ -2,5 +2,7 @@
 #include "gmm_tile.h"
 
 namespace moe {
-hipError_t launch_gmm_tile_nt(const GmmArgs& a, hipStream_t s) { return gmm_launch_rows<GmmForm::kNT, GmmBf16>(a, s); }
+hipError_t launch_gmm_tile_nt(const GmmArgs& a, int waves, hipStream_t s) {
+  return waves == 8 ? gmm_launch_rows<GmmForm::kNT, GmmBf16, 8>(a, s) : gmm_launch_rows<GmmForm::kNT, GmmBf16, 4>(a, s);
+}
 }  // namespace moe

@@ -263,12 +263,13 @@ bool gmm_grid_ok(const GmmArgs& a);
 // Any sizes and any element alignment, in tiles of 64 x 64 or 128 x 128 (gmm_any_grid of them at most).
 hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s);
 int64_t gmm_any_grid(const GmmArgs& a, int tile);
-int64_t gmm_tile_items(const GmmArgs& a);
-// 256 x 256 tiles on rows of whole 16-byte pieces (bf16; int8 for the forward).
-hipError_t launch_gmm_tile_nt(const GmmArgs& a, hipStream_t s);
-hipError_t launch_gmm_tile_i8(const GmmArgs& a, hipStream_t s);
-hipError_t launch_gmm_tile_nn(const GmmArgs& a, hipStream_t s);
-hipError_t launch_gmm_tile_tn(const GmmArgs& a, hipStream_t s);
+// Tiles of 32 waves x 32 waves (waves 8 or 4 per work-group) on rows of whole 16-byte pieces (bf16; int8 for the
+// forward); gmm_tile_items of them at most.
+hipError_t launch_gmm_tile_nt(const GmmArgs& a, int waves, hipStream_t s);
+hipError_t launch_gmm_tile_i8(const GmmArgs& a, int waves, hipStream_t s);
+hipError_t launch_gmm_tile_nn(const GmmArgs& a, int waves, hipStream_t s);
+hipError_t launch_gmm_tile_tn(const GmmArgs& a, int waves, hipStream_t s);
+int64_t gmm_tile_items(const GmmArgs& a, int waves);
 
 // codes[r] = rint(127 v / max|v|), scales[r] = max|v| / 127 of each row v (swiglu: v = SiLU(gate) * up of a
 // row gate | up of 2 cols values).
