@@ -279,16 +279,15 @@ __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_ker
       v[h] = *reinterpret_cast<const f32x4*>(lds + r * kOutRow + (((c / 4 + h) ^ (r & 15)) << 4));
     const int n = cols - c;
     if (bf16) {
-      uint16_t h[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = f32_to_bf16(v[e >> 2][e & 3]);
+      const uint32_t h[4] = {gmm_bf16x2(v[0][0], v[0][1]), gmm_bf16x2(v[0][2], v[0][3]), gmm_bf16x2(v[1][0], v[1][1]),
+                             gmm_bf16x2(v[1][2], v[1][3])};
       char* o = out + ((int64_t)r * q_len + c) * 2;
       if (n >= 8) {
         __builtin_memcpy(o, h, 16);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (e < n) reinterpret_cast<uint16_t*>(o)[e] = h[e];
+          if (e < n) reinterpret_cast<uint16_t*>(o)[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
       }
     } else {
       char* o = out + ((int64_t)r * q_len + c) * 4;
@@ -362,15 +361,13 @@ __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
   }
   if (a.out_bf16) {
     uint16_t* o = static_cast<uint16_t*>(a.out) + row * q_len + col;
-    uint16_t h[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = f32_to_bf16(sum[e]);
+    const uint32_t h[2] = {gmm_bf16x2(sum[0], sum[1]), gmm_bf16x2(sum[2], sum[3])};
     if (n == 4) {
       __builtin_memcpy(o, h, 8);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < n) o[e] = h[e];
+        if (e < n) o[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
     }
   } else {
     float* o = static_cast<float*>(a.out) + row * q_len + col;

@@ -58,6 +58,13 @@ struct GmmF32 {
 
 constexpr int kGmmStepBytes = 128;  // bytes of an operand row per contraction step
 
+// Two fp32 values rounded to bf16 (nearest even), the first in the low half: one v_cvt_pk_bf16_f32.
+__device__ __forceinline__ uint32_t gmm_bf16x2(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // LDS stage of an operand whose rows run along the contraction: OUTER rows of 128 bytes, 16-byte chunk c
 // of row r at c ^ ((r >> 1) & 7), so that the 16 rows of one fragment read fall in 16 bank groups.
 template <class T, int OUTER>

@@ -1,6 +1,5 @@
 // Which kernel a grouped product runs on, and into how many ranges its contraction is cut.
 #include <algorithm>
-#include <cstdlib>
 
 #include "kernels.h"
 
@@ -48,10 +47,26 @@ int any_split(const GmmArgs& a) {
   const int tile = any_tile(a);
   return split_of(gmm_any_grid(a, tile), max_steps(a), (tile == 64 ? 4 : 2) * kCus);
 }
-// Waves of the tile kernel's work-groups.
+int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
+
+// Waves of the tile kernel's work-groups: 8 (256 x 256 tiles, one work-group to a CU) move half the bytes per
+// product through LDS, 4 (128 x 128, two to a CU) waste less of a small matrix, fill the chip with fewer
+// tiles and hide one another's starts and ends.  Measured over 90 drawn sizes: 8 waves win where there
+// are 512 tiles or more, or 160 with sums of 12 steps or more (4 groups, 3045 rows, N = 2952, K = 4808: 116 us
+// against 146), unless whole tiles pad the output more (two groups, 37557 rows, K = 104: 34 against 27) or
+// groups have few rows (48 groups, 512 rows, int8: 150 against 140).
 int tile_waves(const GmmArgs& a) {
-  if (const char* e = getenv("GMM_W")) return atoi(e);
-  return 8;
+  const int64_t q = a.form == GmmForm::kNT ? a.N : a.K, rows = a.max_rows / a.G;
+  int64_t large = padded(q, 256), small = padded(q, 128);
+  if (a.form == GmmForm::kTN) {
+    large *= padded(a.N, 256);
+    small *= padded(a.N, 128);
+  }
+  if (large * 100 > small * 115) return 4;
+  if (a.form != GmmForm::kTN && rows < 32) return 4;
+  const int64_t items = gmm_tile_items(a, 8);
+  const int64_t steps = a.form == GmmForm::kTN ? rows / 64 : max_steps(a);
+  return items >= 512 || (items >= 160 && steps >= 12) ? 8 : 4;
 }
 int tile_split(const GmmArgs& a) {
   const int waves = tile_waves(a);

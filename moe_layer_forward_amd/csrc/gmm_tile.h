@@ -40,6 +40,8 @@ constexpr int kGmmQLoads = 4;       // ... and of a step of Q
 constexpr uint32_t kGmmOutside = 0xfffffff0u;  // an offset past every record count
 constexpr int kGmmSuper = 4;        // row tiles that run side by side on one XCD
 
+#define MOE_GMM_INLINE __attribute__((always_inline))
+
 typedef __amdgpu_buffer_rsrc_t GmmRsrc;
 typedef __attribute__((address_space(3))) void* GmmLds;
 
@@ -207,20 +209,20 @@ __device__ __forceinline__ void gmm_read_first(char* const (&p)[2], const char* 
 // make a wait stricter, never laxer.  With one block (NB = 1) there is one half and one meeting.
 // Steps past the last are loaded too: they lie past the ends, read nothing and put zeros into arrays that
 // nobody multiplies, so that every step is the same code with the same waits.
-template <class T, int W, int NB, int D, class LoadP, class LoadQ, class FP, class FQ>
-__device__ __forceinline__ void gmm_step(LoadP (&lp)[2], LoadQ& lq, int kt, const GmmRings& r, const FP& fp,
-                                         const FQ& fq, int wave, GmmCarry& c, typename T::Acc (&acc)[NB][4]) {
+// kMidWait, kEndWait: operations that may be in flight at the two meetings; mid(), end(): what is loaded there.
+template <class T, int W, int NB, int kMidWait, int kEndWait, class FP, class FQ, class Mid, class End>
+__device__ __forceinline__ void gmm_step(char* const (&ps)[2], const char* qs, char* const (&ps_next)[2],
+                                         const char* qs_next, const FP& fp, const FQ& fq, GmmCarry& c,
+                                         typename T::Acc (&acc)[NB][4], const Mid& mid, const End& end) {
   using O = GmmOrder<W, NB>;
   constexpr int NF = 2 * NB, kMid = 2 * O::kH0 - 2;
   constexpr int kSecond = O::kH0 >= 2 ? O::kH0 - 2 : 0;
-  constexpr int n0 = O::kLoads0, n1 = O::kLoads1;
-  const char* qs = r.q[D % 3];
   gmm_u32x4 q[2][4], p[NF];
 #pragma unroll
   for (int s = 0; s < 4; ++s) q[0][s] = c.q[s];
   p[0] = c.p[0];
   if (NB > 1) p[1] = c.p[1];
-  else p[1] = gmm_read_p<W, NB>(r.p[D % 2], fp, 1);
+  else p[1] = gmm_read_p<W, NB>(ps, fp, 1);
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
     if (f == kSecond) {
@@ -228,27 +230,41 @@ __device__ __forceinline__ void gmm_step(LoadP (&lp)[2], LoadQ& lq, int kt, cons
       for (int s = 0; s < 4; ++s) q[1][s] = fq.read(qs, s, 1);
     }
     if (f == kMid) {
-      wait_vmcnt<NB == 1 ? kGmmQLoads : kGmmQLoads + n0 + n1>();
+      wait_vmcnt<kMidWait>();
       block_sync_lds();
-      lq.prefetch(kt + 4);
-      lp[0].template issue<n0>(kt + 2, r.p[D % 2][0], wave);
-      lq.template issue<kGmmQLoads>(kt + 3, r.q[D % 3], wave);
+      mid();
       __builtin_amdgcn_sched_barrier(0);
     }
     if (f == NF - 2) {
       if (NB > 1) {
-        wait_vmcnt<2 * kGmmQLoads + n0 + n1>();
+        wait_vmcnt<kEndWait>();
         block_sync_lds();
-        lp[1].template issue<n1>(kt + 2, r.p[D % 2][1], wave);
+        end();
         __builtin_amdgcn_sched_barrier(0);
       }
-      gmm_read_first<W, NB>(r.p[(D + 1) % 2], r.q[(D + 1) % 3], fp, fq, c);
+      gmm_read_first<W, NB>(ps_next, qs_next, fp, fq, c);
     }
-    if (f + 2 < NF) p[f + 2] = gmm_read_p<W, NB>(r.p[D % 2], fp, f + 2);
+    if (f + 2 < NF) p[f + 2] = gmm_read_p<W, NB>(ps, fp, f + 2);
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[O::acc(f)][s] = T::mfma(q[O::kk(f)][s], p[f], acc[O::acc(f)][s]);
     __builtin_amdgcn_sched_barrier(0);
   }
+}
+
+// Step kt (kt % 6 == D) of an item's loop.
+template <class T, int W, int NB, int D, class LoadP, class LoadQ, class FP, class FQ>
+__device__ __forceinline__ void gmm_loop_step(LoadP (&lp)[2], LoadQ& lq, int kt, const GmmRings& r, const FP& fp,
+                                              const FQ& fq, int wave, GmmCarry& c, typename T::Acc (&acc)[NB][4]) {
+  using O = GmmOrder<W, NB>;
+  constexpr int n0 = O::kLoads0, n1 = O::kLoads1;
+  gmm_step<T, W, NB, NB == 1 ? kGmmQLoads : kGmmQLoads + n0 + n1, 2 * kGmmQLoads + n0 + n1>(
+      r.p[D % 2], r.q[D % 3], r.p[(D + 1) % 2], r.q[(D + 1) % 3], fp, fq, c, acc,
+      [&] {
+        lq.prefetch(kt + 4);
+        lp[0].template issue<n0>(kt + 2, r.p[D % 2][0], wave);
+        lq.template issue<kGmmQLoads>(kt + 3, r.q[D % 3], wave);
+      },
+      [&] { lp[1].template issue<n1>(kt + 2, r.p[D % 2][1], wave); });
 }
 
 // The nk steps of the contraction.  Every load has landed when it returns.
@@ -283,17 +299,17 @@ __device__ __forceinline__ void gmm_loop(LoadP (&lp)[2], LoadQ& lq, int nk, cons
   gmm_read_first<W, NB>(r.p[0], r.q[0], fp, fq, c);
   // step 0 by itself, and no exits inside the unrolled loop: with either the compiler's own wait before the
   // loop head's first read drains every load in flight
-  gmm_step<T, W, NB, 0>(lp, lq, 0, r, fp, fq, wave, c, acc);
+  gmm_loop_step<T, W, NB, 0>(lp, lq, 0, r, fp, fq, wave, c, acc);
   int kt = 1;
   for (; kt + 6 <= nk; kt += 6) {
     static_for<6>([&](auto ic) {
       constexpr int j = decltype(ic)::value;
-      gmm_step<T, W, NB, (j + 1) % 6>(lp, lq, kt + j, r, fp, fq, wave, c, acc);
+      gmm_loop_step<T, W, NB, (j + 1) % 6>(lp, lq, kt + j, r, fp, fq, wave, c, acc);
     });
   }
   static_for<5>([&](auto ic) {  // the last 0 .. 5 steps
     constexpr int j = decltype(ic)::value;
-    if (kt + j < nk) gmm_step<T, W, NB, (j + 1) % 6>(lp, lq, kt + j, r, fp, fq, wave, c, acc);
+    if (kt + j < nk) gmm_loop_step<T, W, NB, (j + 1) % 6>(lp, lq, kt + j, r, fp, fq, wave, c, acc);
   });
   wait_vmcnt<0>();
 }
@@ -328,11 +344,11 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
       for (int s = 0; s < 4; ++s) {
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         const int col = 64 * wc + 16 * s + 4 * (lane >> 4);
-        uint16_t h[4];
+        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = f32_to_bf16(value(i, s, e, row, col + e));
+        for (int e = 0; e < 4; ++e) v[e] = value(i, s, e, row, col + e);
         *reinterpret_cast<u32x2*>(st + (((col >> 3) ^ (row & 15)) << 4) + (col & 7) * 2) =
-            u32x2{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
+            u32x2{gmm_bf16x2(v[0], v[1]), gmm_bf16x2(v[2], v[3])};
       }
     });
     block_sync_lds();
