@@ -414,9 +414,13 @@ def _launch(dev, entry, *args):
     """The C call on dev's current stream, with dev the current device (a stream belongs to its device)."""
     import torch
 
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    # the raw handle of the current stream, without building a Stream object around it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    stream = raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
     if dev.index == torch.cuda.current_device():
-        _check(entry(*args, stream))
+        status = entry(*args, stream)
+        if status != MOE_OK:
+            _check(status)
     else:
         with torch.cuda.device(dev):
             _check(entry(*args, stream))
