@@ -37,6 +37,7 @@ struct GmmShape {
 };
 constexpr int kGmmPLoads = 2;       // 1 KiB loads per wave of a half of P
 constexpr int kGmmQLoads = 4;       // ... and of a step of Q
+constexpr int kGmmNonTemporal = 2;  // the loads' cache policy operand: nt
 constexpr uint32_t kGmmOutside = 0xfffffff0u;  // an offset past every record count
 constexpr int kGmmSuper = 4;        // row tiles that run side by side on one XCD
 
@@ -49,8 +50,9 @@ __device__ __forceinline__ GmmRsrc gmm_rsrc(const char* base, uint32_t records) 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, (int)records, 0x00020000);
 }
 
-// Loads of NL KiB per wave of an operand whose rows run along the contraction.
-template <class T, int W, int NL>
+// Loads of NL KiB per wave of an operand whose rows run along the contraction.  kOnce: nothing reads these bytes
+// again soon (non-temporal policy).
+template <class T, int W, int NL, bool kOnce>
 struct GmmLoadAlong {
   const char* base;    // uniform
   uint32_t records;
@@ -84,13 +86,13 @@ struct GmmLoadAlong {
 #pragma unroll
     for (int j = 0; j < n; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GmmLds)(stage + (wave + W * j) * 1024), 16,
-                                               in ? off[j] + kb : kGmmOutside, 0, 0, 0);
+                                               in ? off[j] + kb : kGmmOutside, 0, 0, kOnce ? kGmmNonTemporal : 0);
   }
 };
 
 // Loads of NL KiB per wave of an operand whose rows run across the contraction (NL * 8 W columns), optionally
 // gathered.
-template <class T, int W, int NL, bool kGather>
+template <class T, int W, int NL, bool kGather, bool kOnce>
 struct GmmLoadAcross {
   using L = GmmAcross<T, NL * W * 8>;
   static constexpr int kRows = L::kRows, kRowsPer = 1024 / L::kRowBytes;  // rows of a step, of a piece
@@ -153,7 +155,7 @@ struct GmmLoadAcross {
 #pragma unroll
       for (int j = 0; j < n; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GmmLds)(stage + (wave + W * j) * 1024), 16, off[j], 0, 0,
-                                                 0);
+                                                 kOnce ? kGmmNonTemporal : 0);
     }
   }
 };
@@ -452,7 +454,7 @@ inline int64_t gmm_weight_grid(int64_t items) {
   const GmmRings rings{{{p00_, p01_}, {p10_, p11_}}, {q0_, q1_, q2_}};
 
 // NT and NN: output rows are rows of a group.
-template <GmmForm F, class T, int W, int NB>
+template <GmmForm F, class T, int W, bool kOnce, int NB>
 __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& rings, int g, int64_t beg, int64_t end,
                                               int64_t q0, int sp) {
   using S = GmmShape<W>;
@@ -463,7 +465,7 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
   const int64_t ldp = depth * T::kBytes;
   const int rows = (int)(end - beg);
   const int32_t* index = F == GmmForm::kNT ? a.row_index : nullptr;
-  GmmLoadAlong<T, W, kGmmPLoads> lp[2];
+  GmmLoadAlong<T, W, kGmmPLoads, false> lp[2];
   {
     const char* p = static_cast<const char*>(F == GmmForm::kNT ? a.x : a.dy) + (index ? 0 : beg * ldp);
     // rows past the end re-read the last one
@@ -479,7 +481,9 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
       });
   }
   const char* w = static_cast<const char*>(a.w) + (int64_t)g * a.N * a.K * T::kBytes;
-  std::conditional_t<F == GmmForm::kNT, GmmLoadAlong<T, W, kGmmQLoads>, GmmLoadAcross<T, W, kGmmQLoads, false>> lq;
+  std::conditional_t<F == GmmForm::kNT, GmmLoadAlong<T, W, kGmmQLoads, kOnce>,
+                     GmmLoadAcross<T, W, kGmmQLoads, false, kOnce>>
+      lq;
   if constexpr (F == GmmForm::kNT) {
     const int cols = (int)(q_len - q0 < S::kTile ? q_len - q0 : S::kTile);
     lq.init(w + q0 * ldp, (uint32_t)(cols * ldp), ldp, wave, [&](int rl) -> int64_t { return rl < cols ? rl : cols - 1; });
@@ -541,7 +545,7 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
   }
 }
 
-template <GmmForm F, class T, int W>
+template <GmmForm F, class T, int W, bool kOnce>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void gmm_rows_kernel(GmmArgs a,
                                                                                                     int slabs) {
   MOE_GMM_SMEM(W)
@@ -558,7 +562,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const int nb = (int)(end - beg + 31) / 32;  // P blocks per wave
 #define MOE_GMM_CASE(N) \
   if constexpr (N <= W) \
-    if (nb == N) return gmm_rows_body<F, T, W, N>(a, rings, g, beg, end, q0, sp);
+    if (nb == N) return gmm_rows_body<F, T, W, kOnce, N>(a, rings, g, beg, end, q0, sp);
   MOE_GMM_CASE(8)
   MOE_GMM_CASE(7)
   MOE_GMM_CASE(6)
@@ -593,11 +597,11 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / (W / 2), wc = wave % (W / 2);
   const int64_t ldn = (int64_t)a.N * T::kBytes, ldk = (int64_t)a.K * T::kBytes;
   const int depth = (int)(end - beg);
-  GmmLoadAcross<T, W, kGmmPLoads, false> lp[2];
+  GmmLoadAcross<T, W, kGmmPLoads, false, false> lp[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     lp[h].init(static_cast<const char*>(a.dy) + beg * ldn, ldn, depth, p0 + h * S::kHalf, wave, nullptr, 0);
-  GmmLoadAcross<T, W, kGmmQLoads, kGather> lq;
+  GmmLoadAcross<T, W, kGmmQLoads, kGather, false> lq;
   lq.init(static_cast<const char*>(a.x) + (kGather ? 0 : beg * ldk), ldk, depth, q0, wave,
           kGather ? a.row_index + beg : nullptr, a.x_rows);
   GmmFrags<LP, 2> fp;
@@ -629,13 +633,24 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #endif
 }
 
-template <GmmForm F, class T, int W>
+template <GmmForm F, class T, int W, bool kOnce>
 hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
   using S = GmmShape<W>;
   const int slabs = ((F == GmmForm::kNT ? a.N : a.K) + S::kTile - 1) / S::kTile;
-  gmm_rows_kernel<F, T, W>
+  gmm_rows_kernel<F, T, W, kOnce>
       <<<dim3((unsigned)(gmm_row_grid(a, slabs, S::kTile) * a.split)), dim3(S::kThreads), 0, s>>>(a, slabs);
   return hipGetLastError();
+}
+
+// The weights are read with the non-temporal policy where nothing reads them twice: groups of about one row tile,
+// whose weights together exceed the 256 MB of last-level cache that a next call could find them in
+// (gm decode, 384 groups of 1.3 rows: 1.44 -> 1.32 ms; int8, 48 groups: 141 -> 127 us; a 132 MB int8 weight
+// called again and again: 36 us with the default policy, 40 with this one).
+template <GmmForm F, class T>
+hipError_t gmm_launch_rows(const GmmArgs& a, int waves, hipStream_t s) {
+  const bool once = a.max_rows <= (int64_t)a.G * 32 * waves && (int64_t)a.G * a.N * a.K * T::kBytes > (256 << 20);
+  if (waves == 8) return once ? gmm_launch_rows<F, T, 8, true>(a, s) : gmm_launch_rows<F, T, 8, false>(a, s);
+  return once ? gmm_launch_rows<F, T, 4, true>(a, s) : gmm_launch_rows<F, T, 4, false>(a, s);
 }
 
 }  // namespace

@@ -3,6 +3,6 @@
 
 namespace moe {
 hipError_t launch_gmm_tile_nt(const GmmArgs& a, int waves, hipStream_t s) {
-  return waves == 8 ? gmm_launch_rows<GmmForm::kNT, GmmBf16, 8>(a, s) : gmm_launch_rows<GmmForm::kNT, GmmBf16, 4>(a, s);
+  return gmm_launch_rows<GmmForm::kNT, GmmBf16>(a, waves, s);
 }
 }  // namespace moe
