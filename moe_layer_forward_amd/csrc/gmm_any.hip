@@ -17,22 +17,30 @@ namespace {
 
 constexpr int kAnyThreads = 256;
 
-// nv of the n elements at p (n = 16 bytes of them), zeros after them.
+// nv of the n elements at p (n = 16 bytes of them), zeros after them.  before: elements of the row in front of p; the
+// last elements of a row of 16 bytes or more come from the 16 bytes that end with it, shifted down.
 template <class T>
-__device__ __forceinline__ gmm_u32x4 load_chunk(const char* p, int nv) {
+__device__ __forceinline__ gmm_u32x4 load_chunk(const char* p, int nv, int64_t before) {
   constexpr int kN = 16 / T::kBytes;
   gmm_u32x4 v = {0, 0, 0, 0};
   if (nv >= kN) {
     __builtin_memcpy(&v, p, 16);
   } else if (nv > 0) {
+    const int drop = kN - nv;
+    if (before >= drop) {
+      unsigned __int128 u;
+      __builtin_memcpy(&u, p - drop * T::kBytes, 16);
+      v = __builtin_bit_cast(gmm_u32x4, u >> (8 * T::kBytes * drop));
+    } else {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (i < nv) {
-        uint32_t u;
-        if constexpr (T::kBytes == 1) u = *reinterpret_cast<const uint8_t*>(p + i);
-        if constexpr (T::kBytes == 2) u = *reinterpret_cast<const uint16_t*>(p + 2 * i);
-        if constexpr (T::kBytes == 4) u = *reinterpret_cast<const uint32_t*>(p + 4 * i);
-        v[i * T::kBytes / 4] |= u << (8 * T::kBytes * (i % (4 / T::kBytes)));
+      for (int i = 0; i < kN; ++i) {
+        if (i < nv) {
+          uint32_t u;
+          if constexpr (T::kBytes == 1) u = *reinterpret_cast<const uint8_t*>(p + i);
+          if constexpr (T::kBytes == 2) u = *reinterpret_cast<const uint16_t*>(p + 2 * i);
+          if constexpr (T::kBytes == 4) u = *reinterpret_cast<const uint32_t*>(p + 4 * i);
+          v[i * T::kBytes / 4] |= u << (8 * T::kBytes * (i % (4 / T::kBytes)));
+        }
       }
     }
   }
@@ -48,6 +56,7 @@ struct AnyOperand {
   static constexpr int kC = L::kStageBytes / 16 / kAnyThreads;
   const char* ptr[kC];      // Along: the chunk's row, at its chunk of step 0.  Across (not gathered): likewise
   int n;                    // Along: elements of the row from the chunk of step 0 on.  Across: of the columns
+  int64_t before;           // elements of the row in front of the chunk (Along: of step 0)
   int have;                 // Along: bit j: the row of chunk j exists
   int64_t ld;               // Across: bytes between contraction rows
   int depth;                // Across: contraction rows
@@ -60,6 +69,7 @@ struct AnyOperand {
   __device__ __forceinline__ void init_along(const char* b, int64_t ld_, int depth_, int rows, RowOf row_of) {
     const int c = (threadIdx.x % L::kChunks) * kN;  // 256 threads: the same chunk of each of the four rows
     n = depth_ - c;
+    before = c;
     have = 0;
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
@@ -74,6 +84,7 @@ struct AnyOperand {
     const int c = (threadIdx.x % L::kChunks) * kN;
     const int64_t left = cols - col0 - c;
     n = left > kN ? kN : (int)left;
+    before = col0 + c;
     ld = ld_;
     depth = depth_;
     index = index_;
@@ -89,7 +100,7 @@ struct AnyOperand {
       v[j] = gmm_u32x4{0, 0, 0, 0};
       if constexpr (L::kAlong) {
         const int nv = (have >> j) & 1 ? n - kt * (kGmmStepBytes / T::kBytes) : 0;
-        if (nv > 0) v[j] = load_chunk<T>(ptr[j] + (int64_t)kt * kGmmStepBytes, nv);
+        if (nv > 0) v[j] = load_chunk<T>(ptr[j] + (int64_t)kt * kGmmStepBytes, nv, before + kt * (kGmmStepBytes / T::kBytes));
       } else {
         const int r = kt * L::kRows + (threadIdx.x + kAnyThreads * j) / L::kChunks;
         if (r < depth && n > 0) {
@@ -99,7 +110,7 @@ struct AnyOperand {
             i = i < 0 ? 0 : i > index_last ? index_last : i;
             p = base + (int64_t)i * ld;
           }
-          v[j] = load_chunk<T>(p, n);
+          v[j] = load_chunk<T>(p, n, before);
         }
       }
     }

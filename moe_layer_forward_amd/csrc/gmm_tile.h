@@ -316,21 +316,20 @@ __device__ __forceinline__ void gmm_loop(LoadP (&lp)[2], LoadQ& lq, int nk, cons
   wait_vmcnt<0>();
 }
 
-// Where an output tile goes: rows [0, rows) x columns [0, cols) of out (leading dimension ld, in
-// elements); pieces: whole 16-byte pieces of rows may be stored (ld and the start are multiples of 16
-// bytes).
+// Where an output tile goes: rows [0, rows) x columns [0, cols) of out (leading dimension ld, in elements).  Rows
+// leave as 16-byte pieces at whatever alignment they have, the last one of a row element by element.
 struct GmmOut {
   char* out;
   int64_t ld;
   int rows, cols;
-  bool bf16, pieces;
+  bool bf16;
 };
 
 // value(row block i, Q block s, element e, row, col) -> fp32
 template <int W, int NB, class Value>
 __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, int wr, int wc, const Value& value) {
   const int lane = threadIdx.x & 63;
-  if (o.bf16 && o.pieces) {
+  if (o.bf16) {
     // staged as rows of 64 W bytes, 32 rows to each array or half of one; 16-byte piece c of row x at c ^ (x & 15)
     using S = GmmShape<W>;
     constexpr int kRowB = S::kTile * 2, kPieces = kRowB / 16;
@@ -361,7 +360,14 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
         const int x = threadIdx.x / kPieces + 16 * h, c = threadIdx.x % kPieces, row = 32 * b + x;
         if (row >= o.rows || 8 * c >= o.cols) continue;
         const gmm_u32x4 v = *reinterpret_cast<const gmm_u32x4*>(stage[b] + x * kRowB + ((c ^ (row & 15)) << 4));
-        *reinterpret_cast<gmm_u32x4*>(o.out + (row * o.ld + 8 * c) * 2) = v;
+        char* const to = o.out + (row * o.ld + 8 * c) * 2;
+        if (8 * c + 8 <= o.cols) {
+          __builtin_memcpy(to, &v, 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (8 * c + e < o.cols) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
       }
     });
     return;
@@ -376,18 +382,13 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = value(i, s, e, row, col + e);
-        if (!o.bf16 && o.pieces) {  // rows of whole 16-byte pieces: four columns exist or none
-          if (col < o.cols)
-            *reinterpret_cast<f32x4*>(o.out + (row * o.ld + col) * 4) = f32x4{v[0], v[1], v[2], v[3]};
-          continue;
-        }
+        char* const to = o.out + (row * o.ld + col) * 4;
+        if (col + 4 <= o.cols) {
+          __builtin_memcpy(to, v, 16);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (col + e >= o.cols) continue;
-          if (o.bf16)
-            *reinterpret_cast<uint16_t*>(o.out + (row * o.ld + col + e) * 2) = f32_to_bf16(v[e]);
-          else
-            *reinterpret_cast<float*>(o.out + (row * o.ld + col + e) * 4) = v[e];
+          for (int e = 0; e < 4; ++e)
+            if (col + e < o.cols) reinterpret_cast<float*>(to)[e] = v[e];
         }
       }
     }
@@ -514,7 +515,6 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
   o.rows = rows;
   o.cols = (int)(q_len - q0 < S::kTile ? q_len - q0 : S::kTile);
   o.bf16 = e == 2;
-  o.pieces = (q_len * e) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   if constexpr (std::is_same_v<T, GmmI8>) {
     if (a.split > 1) {  // int32 partial sums, as they are
       gmm_store<W, NB>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return __int_as_float(acc[i][s][j]); });
@@ -626,7 +626,6 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   o.rows = (int)(a.N - p0 < S::kTile ? a.N - p0 : S::kTile);
   o.cols = (int)(a.K - q0 < S::kTile ? a.K - q0 : S::kTile);
   o.bf16 = e == 2;
-  o.pieces = ((int64_t)a.K * e) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
   gmm_store<W, W>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return acc[i][s][j]; });
 #else
   (void)rings;
