@@ -323,7 +323,9 @@ struct GmmOut {
   int64_t ld;
   int rows, cols;
   bool bf16;
+  bool once;  // non-temporal stores: an output that no cache holds until its reader comes
 };
+constexpr int64_t kGmmCacheBytes = 256 << 20;  // the last-level cache
 
 // value(row block i, Q block s, element e, row, col) -> fp32
 template <int W, int NB, class Value>
@@ -360,9 +362,13 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
         const int x = threadIdx.x / kPieces + 16 * h, c = threadIdx.x % kPieces, row = 32 * b + x;
         if (row >= o.rows || 8 * c >= o.cols) continue;
         const gmm_u32x4 v = *reinterpret_cast<const gmm_u32x4*>(stage[b] + x * kRowB + ((c ^ (row & 15)) << 4));
+        typedef gmm_u32x4 Unaligned __attribute__((aligned(2)));
         char* const to = o.out + (row * o.ld + 8 * c) * 2;
         if (8 * c + 8 <= o.cols) {
-          __builtin_memcpy(to, &v, 16);
+          if (o.once)
+            __builtin_nontemporal_store(v, reinterpret_cast<Unaligned*>(to));
+          else
+            *reinterpret_cast<Unaligned*>(to) = v;
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -515,6 +521,7 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
   o.rows = rows;
   o.cols = (int)(q_len - q0 < S::kTile ? q_len - q0 : S::kTile);
   o.bf16 = e == 2;
+  o.once = a.max_rows * q_len * 2 >= kGmmCacheBytes;
   if constexpr (std::is_same_v<T, GmmI8>) {
     if (a.split > 1) {  // int32 partial sums, as they are
       gmm_store<W, NB>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return __int_as_float(acc[i][s][j]); });
@@ -626,6 +633,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   o.rows = (int)(a.N - p0 < S::kTile ? a.N - p0 : S::kTile);
   o.cols = (int)(a.K - q0 < S::kTile ? a.K - q0 : S::kTile);
   o.bf16 = e == 2;
+  o.once = (int64_t)a.G * a.N * a.K * 2 >= kGmmCacheBytes;
   gmm_store<W, W>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return acc[i][s][j]; });
 #else
   (void)rings;
@@ -647,7 +655,7 @@ hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
 // called again and again: 36 us with the default policy, 40 with this one).
 template <GmmForm F, class T>
 hipError_t gmm_launch_rows(const GmmArgs& a, int waves, hipStream_t s) {
-  const bool once = a.max_rows <= (int64_t)a.G * 32 * waves && (int64_t)a.G * a.N * a.K * T::kBytes > (256 << 20);
+  const bool once = a.max_rows <= (int64_t)a.G * 32 * waves && (int64_t)a.G * a.N * a.K * T::kBytes > kGmmCacheBytes;
   if (waves == 8) return once ? gmm_launch_rows<F, T, 8, true>(a, s) : gmm_launch_rows<F, T, 8, false>(a, s);
   return once ? gmm_launch_rows<F, T, 4, true>(a, s) : gmm_launch_rows<F, T, 4, false>(a, s);
 }
