@@ -28,25 +28,28 @@ int64_t out_elems(const GmmArgs& a) {
   return a.form == GmmForm::kTN ? (int64_t)a.G * a.N * a.K : a.max_rows * (a.form == GmmForm::kNT ? a.N : a.K);
 }
 
-// Ranges of the contraction for `items` output tiles (an upper bound) of at most `steps` steps, when `slots`
-// work-groups run at once: enough to fill the chip, each range at least kMinSteps steps.
-int split_of(int64_t items, int64_t steps, int64_t slots) {
-  constexpr int64_t kMinSteps = 6, kMaxSplit = 16;
-  if (items <= 0 || items > slots / 2) return 1;
-  return (int)std::max<int64_t>(1, std::min({slots / items, steps / kMinSteps, kMaxSplit}));
+// Ranges of the contraction for `items` output tiles (an upper bound) of about `steps` steps each: as many as let
+// `slots` work-groups run, while every range keeps min_steps steps.  Joining them costs another launch and the
+// partial sums' traffic, so a few long sums are split and a chip that is half full is left alone.
+int split_of(int64_t items, int64_t steps, int64_t slots, int64_t min_steps) {
+  constexpr int64_t kMaxSplit = 16;
+  if (items <= 0) return 1;
+  return (int)std::max<int64_t>(1, std::min({slots / items, steps / min_steps, kMaxSplit}));
 }
 
-int64_t max_steps(const GmmArgs& a) {
-  const int64_t depth = a.form == GmmForm::kNT ? a.K : a.form == GmmForm::kNN ? a.N : a.max_rows;
+// Steps of a sum (TN: of the average group's).
+int64_t steps_of(const GmmArgs& a) {
+  const int64_t depth = a.form == GmmForm::kNT ? a.K : a.form == GmmForm::kNN ? a.N : a.max_rows / a.G;
   return (depth * elem_bytes(a) + 127) / 128;
 }
 
 // Small tiles where the large ones would leave slots (two on a CU) empty.
 int any_tile(const GmmArgs& a) { return gmm_any_grid(a, 128) < 2 * kCus ? 64 : 128; }
-int any_split(const GmmArgs& a) {
-  const int tile = any_tile(a);
-  return split_of(gmm_any_grid(a, tile), max_steps(a), (tile == 64 ? 4 : 2) * kCus);
-}
+// Three work-groups to a CU, ranges of 6 steps: fp32 sums are bound by the matrix cores of few CUs (9 groups, 777
+// rows, 1001 x 515, 32 steps: 56 us in one range, 29 in four; 16 groups, 128 rows, 8 steps: 9 us in one, 13 in
+// two).
+int any_split(const GmmArgs& a) { return split_of(gmm_any_grid(a, any_tile(a)), steps_of(a), 3 * kCus, 6); }
+
 int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
 
 // Waves of the tile kernel's work-groups: 8 (256 x 256 tiles, one work-group to a CU) move half the bytes per
@@ -65,13 +68,11 @@ int tile_waves(const GmmArgs& a) {
   if (large * 100 > small * 115) return 4;
   if (a.form != GmmForm::kTN && rows < 32) return 4;
   const int64_t items = gmm_tile_items(a, 8);
-  const int64_t steps = a.form == GmmForm::kTN ? rows / 64 : max_steps(a);
-  return items >= 512 || (items >= 160 && steps >= 12) ? 8 : 4;
+  return items >= 512 || (items >= 160 && steps_of(a) >= 12) ? 8 : 4;
 }
-int tile_split(const GmmArgs& a) {
-  const int waves = tile_waves(a);
-  return split_of(gmm_tile_items(a, waves), max_steps(a), waves == 8 ? kCus : 2 * kCus);
-}
+// One work-group to a CU, ranges of 8 steps (64 rows, 7168 x 7168: 39 us in one range, 25.5 in four, 30 in
+// eight; int8, 64 rows, 18432 x 7168, 144 tiles: 24.6 us in one range, 35.5 in two).
+int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a, tile_waves(a)), steps_of(a), kCus, 8); }
 
 }  // namespace
 

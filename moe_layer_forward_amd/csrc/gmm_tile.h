@@ -8,12 +8,9 @@
 //     across it).  LDS holds two steps of P, each as two halves of 128 rows, and three of Q: 160 KiB, every
 //     piece its own __shared__ array and the loop unrolled by six, so that every access names its array
 //     and the compiler's own waits stay exact.
-//   * A load takes about 1.3 us from issue to LDS when the chip is busy (one step of products is 0.95 us), so
-//     what bounds the loop is how long before its use a load is issued.  A step multiplies its first half
-//     of P, then its second; by then all its Q fragments are in registers.  So the first half and
-//     Q are reloaded in the middle of the step and the second half at its end: every P load leads its
-//     use by 1.5 steps, every Q load by 2.5 (reloading all of P at the end of a step leads by 1:
-//     KEPT_FIGURE).
+//   * A step multiplies its first half of P, then its second; by then all its Q fragments are in registers.
+//     So the first half and Q are reloaded in the middle of the step and the second half at its end: a P
+//     load leads its use by 1.5 steps, a Q load by 2.5.
 //   * Ends: a chunk past the end of a row gets an offset past the descriptor's record count, a
 //     contraction row past the end lies past the count itself; both put zeros into LDS and read nothing.
 //     So the sums see zeros past the end on both sides, never a neighbour's values.  P rows and Q columns
@@ -21,6 +18,20 @@
 //   * The loop is instantiated per number of P blocks a wave multiplies, so that rows a group does not
 //     have cost no products and no loads.
 //   * Outputs are staged in LDS and leave as 16-byte pieces of whole rows.
+// W = 4 is the same with 128 x 128 outputs and 80 KiB of LDS, two work-groups to a CU; tile_waves says when.
+//
+// What bounds it, measured on 16384 x 4096 x 7168 bf16 in one group (four full tiles per CU, 727 us,
+// 1.32 PFLOP/s; a library product of the same sizes takes 644 us): a step of 64 KiB takes 1.62 us.  Loads
+// alone (products and LDS reads taken out) take 1.33 us a step, 23 bytes a clock and CU, whatever the order,
+// the row length or the lead of the loads; products alone take 1.2 us, the matrix cores then busy at the 1.7 GHz
+// that the chip holds under them (zeros as inputs run 16% faster).  Reloading all of P at the end of a step, wave
+// priorities around products or loads, and 2, 6 or 8 tiles side by side on an XCD all measured within 2%.
+// With about 170 rows a group (384 groups, K = 7168) the weights' stream bounds it: 5.1 TB/s, the same with the
+// products taken out.  A short item pays its ends: about 5 us from launch to the first product and 4 us to
+// store 128 KiB (a sum of 3 steps takes 4 us in between).
+// Tried and not kept for short sums: work-groups that stay and issue an item's first loads before storing the
+// last one's outputs (48 groups of 170 rows, 7168 x 2048: 530 us against 543, but 4 to 16% slower at 8 and
+// more steps, where it needs registers the loop does not have); stores straight from the registers (690 us).
 #pragma once
 #include "gmm_core.h"
 #include "tile_core.h"

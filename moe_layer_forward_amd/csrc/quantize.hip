@@ -13,13 +13,14 @@
 // Bound: HBM, each value read once: a row stays in registers between the maximum and the codes (16-byte loads
 // of 8 values a lane, up to kHeld of them); only what is longer is read again.  Short rows are taken by
 // one wave each (no barrier), long ones by four.  About 10 vector instructions a value (a division per value
-// took 20 and bound the kernel: 8192 x 7168 bf16 rows in 50 us).  QUANT_FIGURES
+// took 20 and bound the kernel: 8192 x 7168 bf16 rows in 50 us).
+// Now 8192 x 7168: bf16 44 us (4.0 TB/s of reads and writes), fp32 54 us (5.5 TB/s); 65536 x 2048 bf16 79 us (5.1).
 #include "kernels.h"
 
 namespace moe {
 namespace {
 
-constexpr int kHeld = 8;          // chunks of 8 values a lane holds: 64 registers
+constexpr int kHeld = 8;  // chunks of 8 values a lane holds: 64 registers
 constexpr int kQuantThreads = 256;
 
 template <class In>
