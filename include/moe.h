@@ -271,7 +271,7 @@ int moe_forward_fp8(const moe_config* cfg, int64_t T, const void* x, const void*
 /* ------------------------------------------------------------------------------------------------
  * Grouped matrix products: the products an expert layer is made of, by themselves, with their gradients
  * (for training such a layer) and in 8-bit integers (for serving it).  The grouped GEMM of [QA] Q8.3
- * over the dispatch order of [DEEP] §10.2 Step 6; the pages give no sizes limits, gradients or 8-bit
+ * over the dispatch order of [DEEP] §10.2 Step 6; the pages give no size limits, gradients or 8-bit
  * integer format for it, so these are stated here.
  *
  * A row space [0, max_rows) is cut into n_groups groups: group g is rows

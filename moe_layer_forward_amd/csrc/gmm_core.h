@@ -20,6 +20,7 @@
 #pragma once
 #include <type_traits>
 
+#include "gmm.h"
 #include "kernels.h"
 
 namespace moe {

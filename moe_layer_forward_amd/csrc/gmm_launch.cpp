@@ -1,7 +1,7 @@
 // Which kernel a grouped product runs on, and into how many ranges its contraction is cut.
 #include <algorithm>
 
-#include "kernels.h"
+#include "gmm.h"
 
 namespace moe {
 namespace {

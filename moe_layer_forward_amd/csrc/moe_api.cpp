@@ -10,6 +10,7 @@
 #include <mutex>
 #include <string>
 
+#include "gmm.h"
 #include "kernels.h"
 #include "moe.h"
 

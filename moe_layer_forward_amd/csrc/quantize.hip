@@ -15,6 +15,7 @@
 // one wave each (no barrier), long ones by four.  About 10 vector instructions a value (a division per value
 // took 20 and bound the kernel: 8192 x 7168 bf16 rows in 50 us).
 // Now 8192 x 7168: bf16 44 us (4.0 TB/s of reads and writes), fp32 54 us (5.5 TB/s); 65536 x 2048 bf16 79 us (5.1).
+#include "gmm.h"
 #include "kernels.h"
 
 namespace moe {
