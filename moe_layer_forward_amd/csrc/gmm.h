@@ -24,9 +24,12 @@ struct GmmArgs {
   const float* w_scales;         // kI8: [G, N]
   void* out;
   int32_t out_bf16;
-  // Set by launch_gmm: the contraction cut into `split` ranges whose partial sums (fp32; int32 for kI8) go
-  // to part, [split, output rows, output columns], for launch_gmm_join.
+  // Set by launch_gmm.  NT, NN: the contraction cut into `split` ranges whose partial sums (fp32; int32 for kI8)
+  // go to part, [split, output rows, output columns], for launch_gmm_join.
   int32_t split = 1;
+  // TN: the rows of a group cut into ranges of range_rows (0: not cut); those of groups with more than one go to
+  // part, [2 ceil(max_rows / range_rows), N, K] (gmm_core.h says where).
+  int64_t range_rows = 0;
   float* part = nullptr;
 };
 // The sum over the ranges, in range order, scaled and rounded once into out.

@@ -10,6 +10,8 @@
 // pieces of rows.  Two (128) or more (64) work-groups share a CU.  Bound: fp32 by
 // v_mfma_f32_16x16x4_f32 (256 FLOP a clock and CU); odd rows by the loads and their trip through registers;
 // small calls by the latency of a step's loads.
+#include <algorithm>
+
 #include "gmm_core.h"
 
 namespace moe {
@@ -124,6 +126,16 @@ struct AnyOperand {
   }
 };
 
+// TN: whether the ranges are shorter than the average group; the sums of the grid, then a multiple of 8 where they
+// are many.
+__host__ __device__ inline bool any_sums_first(const GmmArgs& a) {
+  return a.range_rows && a.range_rows * a.G < a.max_rows;
+}
+__host__ __device__ inline int64_t any_sums(const GmmArgs& a) {
+  const int64_t n = gmm_max_sums(a);
+  return any_sums_first(a) && n >= 2 * kXcds ? (n + kXcds - 1) / kXcds * kXcds : n;
+}
+
 template <GmmForm F, class T, int kTile>
 __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_kernel(GmmArgs a) {
   using LP = GmmP<F, T, kTile>;
@@ -137,16 +149,27 @@ __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_ker
   const int64_t q_len = F == GmmForm::kNT ? a.N : a.K;
   const int q_tiles = (int)((q_len + kTile - 1) / kTile);
   const int sp = (int)(blockIdx.x % (unsigned)a.split);
-  const int64_t item = blockIdx.x / (unsigned)a.split;
+  int64_t item = blockIdx.x / (unsigned)a.split;
+  if constexpr (F == GmmForm::kTN) {
+    // Where every group is cut, consecutive work-groups take different sums: the tiles of one read the same rows,
+    // and so fall on few XCDs (work-group b runs on XCD b % 8), whose L2 hold them.
+    if (any_sums_first(a)) {
+      const int64_t tiles = ((int64_t)a.N + kTile - 1) / kTile * q_tiles, sums = any_sums(a);
+      item = item % sums * tiles + item / sums;
+    }
+  }
   const int64_t t = item / q_tiles;
   const int64_t q0 = (item % q_tiles) * kTile;
   int g;
   int64_t beg, end, p0 = 0;
+  [[maybe_unused]] GmmSum sum;
   if constexpr (F == GmmForm::kTN) {
     const int64_t p_tiles = ((int64_t)a.N + kTile - 1) / kTile;
-    g = (int)(t / p_tiles);
+    if (!sum.find(a, t / p_tiles)) return;
     p0 = (t % p_tiles) * kTile;
-    gmm_group_rows(a.group_offsets, a.max_rows, g, beg, end);
+    g = sum.g;
+    beg = sum.beg;
+    end = sum.end;
   } else {
     GmmTiles tiles;
     tiles.count(a.group_offsets, a.G, a.max_rows, kTile);
@@ -275,11 +298,11 @@ __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_ker
     }
   }
   __syncthreads();
-  const int64_t out_row = F == GmmForm::kTN ? (int64_t)g * a.N + p0 : beg;
-  const int64_t out_rows = F == GmmForm::kTN ? (int64_t)a.G * a.N : a.max_rows;
-  const bool bf16 = a.split == 1 && a.out_bf16;
-  char* out = a.split == 1 ? static_cast<char*>(a.out) : reinterpret_cast<char*>(a.part + sp * out_rows * q_len);
-  out += (out_row * q_len + q0) * (bf16 ? 2 : 4);
+  const bool whole = F == GmmForm::kTN ? sum.whole : a.split == 1, bf16 = whole && a.out_bf16;
+  char* out = F == GmmForm::kTN ? sum.matrix(a)
+              : whole           ? static_cast<char*>(a.out)
+                                : reinterpret_cast<char*>(a.part + sp * a.max_rows * q_len);
+  out += ((F == GmmForm::kTN ? p0 : beg) * q_len + q0) * (bf16 ? 2 : 4);
   // 8 columns a thread, at the alignment that the row has
   for (int ch = threadIdx.x; ch < rows * (kTile / 8); ch += kAnyThreads) {
     const int r = ch / (kTile / 8), c = (ch % (kTile / 8)) * 8;
@@ -313,15 +336,38 @@ __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_ker
   }
 }
 
-// out = the sum over the ranges of part, in range order; one work-group per 1024 columns of a row.
+// 4 (or n) values of out from element i on, rounded once
+__device__ __forceinline__ void store_sums(const GmmArgs& a, int64_t i, int n, const float (&sum)[4]) {
+  if (a.out_bf16) {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + i;
+    const uint32_t h[2] = {gmm_bf16x2(sum[0], sum[1]), gmm_bf16x2(sum[2], sum[3])};
+    if (n == 4) {
+      __builtin_memcpy(o, h, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) o[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    float* o = static_cast<float*>(a.out) + i;
+    if (n == 4) {
+      __builtin_memcpy(o, sum, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) o[e] = sum[e];
+    }
+  }
+}
+
+// NT, NN: out = the sum over the ranges of part, in range order; one work-group per 1024 columns of a row.
 template <GmmForm F, bool kI8>
 __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
   const int64_t q_len = F == GmmForm::kNT ? a.N : a.K;
-  const int64_t out_rows = F == GmmForm::kTN ? (int64_t)a.G * a.N : a.max_rows;
   const int per_row = (int)((q_len + 1023) / 1024);
   const int64_t row = blockIdx.x / per_row;
   const int64_t col = (int64_t)(blockIdx.x % per_row) * 1024 + threadIdx.x * 4;
-  if (F != GmmForm::kTN && a.group_offsets) {  // rows past the last group have no sums
+  if (a.group_offsets) {  // rows past the last group have no sums
     int64_t beg, end;
     gmm_group_rows(a.group_offsets, a.max_rows, a.G - 1, beg, end);
     if (row >= end) return;
@@ -331,7 +377,7 @@ __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   int isum[4] = {0, 0, 0, 0};
   const float* p = a.part + row * q_len + col;
-  for (int s = 0; s < a.split; ++s, p += out_rows * q_len) {
+  for (int s = 0; s < a.split; ++s, p += a.max_rows * q_len) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (n == 4) {
       __builtin_memcpy(v, p, 16);
@@ -370,26 +416,44 @@ __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] = (float)isum[e] * sx * (e < n ? sw[e] : 0.f);
   }
-  if (a.out_bf16) {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + row * q_len + col;
-    const uint32_t h[2] = {gmm_bf16x2(sum[0], sum[1]), gmm_bf16x2(sum[2], sum[3])};
-    if (n == 4) {
-      __builtin_memcpy(o, h, 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < n) o[e] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
-    }
-  } else {
-    float* o = static_cast<float*>(a.out) + row * q_len + col;
-    if (n == 4) {
-      __builtin_memcpy(o, sum, 16);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < n) o[e] = sum[e];
-    }
+  store_sums(a, row * q_len + col, n, sum);
+}
+
+// TN: the same for the groups of more than one range; one work-group per 1024 elements of a group's matrix.  Where
+// groups are more than further ranges can be, a group is found by its second range, and work-groups of other
+// ranges do nothing.
+__global__ __launch_bounds__(256) void gmm_join_sums_kernel(GmmArgs a, int per_matrix) {
+  const int64_t range = a.range_rows;
+  int g = (int)(blockIdx.x / (unsigned)per_matrix);
+  int64_t b, e, second = -1;
+  if (a.G > a.max_rows / range) {
+    GmmSum sum;
+    if (!sum.find(a, (int64_t)a.G + g)) return;
+    g = sum.g;
+    second = sum.beg;
   }
+  gmm_group_rows(a.group_offsets, a.max_rows, g, b, e);
+  if (second >= 0 ? second != b + range : e - b <= range) return;
+  const int64_t all = (int64_t)a.N * a.K;
+  const int64_t i = (int64_t)(blockIdx.x % (unsigned)per_matrix) * 1024 + threadIdx.x * 4;
+  const int n = all - i < 4 ? (int)(all - i) : 4;
+  if (n <= 0) return;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int64_t r = b; r < e; r += range) {
+    const float* p = a.part + GmmSum::place(r, e - r, range) * all + i;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (n == 4) {
+      __builtin_memcpy(v, p, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) v[j] = p[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] += v[j];
+  }
+  store_sums(a, g * all + i, n, sum);
 }
 
 template <GmmForm F, class T>
@@ -406,7 +470,7 @@ hipError_t launch_any(const GmmArgs& a, int tile, hipStream_t s) {
 
 int64_t gmm_any_grid(const GmmArgs& a, int tile) {
   const int64_t q_tiles = ((a.form == GmmForm::kNT ? a.N : a.K) + tile - 1) / tile;
-  const int64_t p_tiles = a.form == GmmForm::kTN ? (int64_t)a.G * ((a.N + tile - 1) / tile)
+  const int64_t p_tiles = a.form == GmmForm::kTN ? any_sums(a) * ((a.N + tile - 1) / tile)
                                                  : gmm_max_tiles(a.max_rows, a.G, tile);
   return p_tiles * q_tiles;
 }
@@ -427,17 +491,20 @@ hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s) {
 }
 
 hipError_t launch_gmm_join(const GmmArgs& a, hipStream_t s) {
+  const dim3 block(256);
+  if (a.form == GmmForm::kTN) {
+    const int64_t per_matrix = ((int64_t)a.N * a.K + 1023) / 1024;
+    gmm_join_sums_kernel<<<dim3((unsigned)(std::min<int64_t>(a.G, a.max_rows / a.range_rows) * per_matrix)), block, 0, s>>>(a, (int)per_matrix);
+    return hipGetLastError();
+  }
   const int64_t q_len = a.form == GmmForm::kNT ? a.N : a.K;
-  const int64_t rows = a.form == GmmForm::kTN ? (int64_t)a.G * a.N : a.max_rows;
-  const dim3 grid((unsigned)(rows * ((q_len + 1023) / 1024))), block(256);
+  const dim3 grid((unsigned)(a.max_rows * ((q_len + 1023) / 1024)));
   if (a.type == GmmType::kI8)
     gmm_join_kernel<GmmForm::kNT, true><<<grid, block, 0, s>>>(a);
   else if (a.form == GmmForm::kNT)
     gmm_join_kernel<GmmForm::kNT, false><<<grid, block, 0, s>>>(a);
-  else if (a.form == GmmForm::kNN)
-    gmm_join_kernel<GmmForm::kNN, false><<<grid, block, 0, s>>>(a);
   else
-    gmm_join_kernel<GmmForm::kTN, false><<<grid, block, 0, s>>>(a);
+    gmm_join_kernel<GmmForm::kNN, false><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -270,6 +270,73 @@ __device__ __forceinline__ void gmm_range(int nk, int split, int sp, int& first,
   n = (int)((int64_t)nk * (sp + 1) / split) - first;
 }
 
+// What a work-group of the TN form sums: rows [beg, end) of group g, all of them (whole) or one range of
+// range_rows.  Sum t < G is group t's, or its first range; the further ranges of all groups follow in order, found as
+// GmmTiles finds tiles.  The partial sums of full ranges go to the even places of part, those of a group's
+// last, shorter one to the odd ones, numbered by where the range starts: two full ranges, and two last ones of
+// groups that have a full one, start range_rows or more apart.
+struct GmmSum {
+  int g;
+  int64_t beg, end;
+  bool whole;
+
+  // false past the last sum
+  __device__ __forceinline__ bool find(const GmmArgs& a, int64_t t) {
+    const int64_t range = a.range_rows;
+    whole = true;
+    if (t < a.G) {
+      g = (int)t;
+      gmm_group_rows(a.group_offsets, a.max_rows, g, beg, end);
+      if (range && end - beg > range) {
+        whole = false;
+        end = beg + range;
+      }
+      return true;
+    }
+    const int lane = threadIdx.x & 63, per = (a.G + 63) / 64;
+    const auto further = [&](int gg) {
+      gmm_group_rows(a.group_offsets, a.max_rows, gg, beg, end);
+      return end > beg ? (int)(end - beg - 1) / (int)range : 0;
+    };
+    int n = 0;
+    for (int j = 0; j < per; ++j)
+      if (lane * per + j < a.G) n += further(lane * per + j);
+    int to = n, rel = (int)(t - a.G);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(to, d, 64);
+      if (lane >= d) to += v;
+    }
+    if (rel >= __builtin_amdgcn_readlane(to, 63)) return false;
+    const int owner = __ffsll((unsigned long long)__ballot(to > rel)) - 1;
+    rel -= __builtin_amdgcn_readlane(to - n, owner);
+    for (g = owner * per;; ++g) {  // ends inside this lane's groups, which have more than rel
+      const int k = further(g);
+      if (rel < k || g + 1 >= a.G) break;
+      rel -= k;
+    }
+    whole = false;
+    g = __builtin_amdgcn_readfirstlane(g);
+    beg = __builtin_amdgcn_readfirstlane((int)(beg + (rel + 1) * range));
+    end = __builtin_amdgcn_readfirstlane((int)end);
+    end = end - beg > range ? beg + range : end;
+    return true;
+  }
+  // its place in part
+  __device__ __forceinline__ static int64_t place(int64_t beg, int64_t rows, int64_t range_rows) {
+    return 2 * (beg / range_rows) + (rows < range_rows);
+  }
+  // first element of its matrix
+  __device__ __forceinline__ char* matrix(const GmmArgs& a) const {
+    const int64_t n = (int64_t)a.N * a.K;
+    return whole ? static_cast<char*>(a.out) + g * n * (a.out_bf16 ? 2 : 4)
+                 : reinterpret_cast<char*>(a.part + place(beg, end - beg, a.range_rows) * n);
+  }
+};
+
+// Most sums that the groups have.
+__host__ __device__ inline int64_t gmm_max_sums(const GmmArgs& a) { return a.G + (a.range_rows ? a.max_rows / a.range_rows : 0); }
+
 // Most row tiles of bm rows that G groups over max_rows rows can have.
 inline int64_t gmm_max_tiles(int64_t max_rows, int G, int bm) {
   const int64_t full = max_rows / bm + G;

@@ -37,6 +37,36 @@ int split_of(int64_t items, int64_t steps, int64_t slots, int64_t min_steps) {
   return (int)std::max<int64_t>(1, std::min({slots / items, steps / min_steps, kMaxSplit}));
 }
 
+// TN: rows of the ranges that a group's sum is cut into, 0: none cut.  One group's matrix is `tiles` output tiles;
+// `slots` work-groups run.  Group sizes are known on the device alone, so the rule goes by their number and all rows, and
+// a group that fits one range is written as if nothing was cut.  Ranges keep min_steps steps.
+//   * Groups that leave slots idle: as many ranges as fill them (with 1/32 to spare, so that nearly equal
+//     groups have equally many).  10 groups, 12688 skewed rows, 1088 x 120 in bf16: 19 us, 29 with as many ranges to
+//     every group.
+//   * Groups that fill the slots: ranges of twice the average group, for the one that holds more than others, where a
+//     quarter of all rows in one sum would take half again as long as the rest and 8 steps more (an item's start
+//     and end counted as 6 steps).  fp32, skewed rows, not cut -> cut: 279 groups, 20499 rows, 448 x 110: 590 ->
+//     100 us; 194 groups, 5082 rows, 384 x 64: 103 -> 45.  The join's launch costs equal groups 3 to 4 us (218
+//     groups, 13206 rows, 128 x 256: 10 -> 13.6).  Without the condition: 130 groups, 8237 skewed rows, 1280 x 576:
+//     70 -> 80.
+int64_t range_of(const GmmArgs& a, int64_t tiles, int64_t slots, int64_t min_steps) {
+  const int64_t step = 128 / elem_bytes(a), steps = (a.max_rows + step - 1) / step, mean = (a.max_rows + a.G - 1) / a.G;
+  int64_t each = std::min(slots / (tiles * a.G), mean / (min_steps * step));
+  if (const int64_t e8 = each * a.G / 8 * 8 / a.G; e8 >= 2) each = e8;  // the same number on each XCD
+  int64_t rows;
+  if (each >= 2) {
+    rows = (mean + each - 1) / each;
+    if (a.G > 1) rows += rows / 32;
+  } else {
+    const int64_t others = tiles * a.G * (steps / a.G + 6) / slots;
+    if (tiles * 2 > slots || steps / 4 <= others * 3 / 2 + 8) return 0;
+    rows = std::max({2 * mean, a.max_rows * tiles / slots, min_steps * step});
+  }
+  rows = (rows + step - 1) / step * step;
+  return rows < a.max_rows ? rows : 0;
+}
+int64_t matrix_tiles(const GmmArgs& a, int64_t tile) { return ((a.N + tile - 1) / tile) * ((a.K + tile - 1) / tile); }
+
 // Steps of a sum (TN: of the average group's).
 int64_t steps_of(const GmmArgs& a) {
   const int64_t depth = a.form == GmmForm::kNT ? a.K : a.form == GmmForm::kNN ? a.N : a.max_rows / a.G;
@@ -49,6 +79,7 @@ int any_tile(const GmmArgs& a) { return gmm_any_grid(a, 128) < 2 * kCus ? 64 : 1
 // rows, 1001 x 515, 32 steps: 56 us in one range, 29 in four; 16 groups, 128 rows, 8 steps: 9 us in one, 13 in
 // two).
 int any_split(const GmmArgs& a) { return split_of(gmm_any_grid(a, any_tile(a)), steps_of(a), 3 * kCus, 6); }
+int64_t any_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, any_tile(a)), 3 * kCus, 6); }
 
 int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
 
@@ -73,6 +104,11 @@ int tile_waves(const GmmArgs& a) {
 // One work-group to a CU, ranges of 8 steps (64 rows, 7168 x 7168: 39 us in one range, 25.5 in four, 30 in
 // eight; int8, 64 rows, 18432 x 7168, 144 tiles: 24.6 us in one range, 35.5 in two).
 int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a, tile_waves(a)), steps_of(a), kCus, 8); }
+int64_t tile_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, 32 * tile_waves(a)), kCus, 8); }
+
+size_t range_bytes(const GmmArgs& a, int64_t range) {
+  return range ? (size_t)(2 * ((a.max_rows + range - 1) / range)) * a.N * a.K * sizeof(float) : 0;
+}
 
 }  // namespace
 
@@ -81,6 +117,8 @@ int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a, tile_waves(
 bool gmm_grid_ok(const GmmArgs& a) { return 512 * gmm_any_grid(a, 64) < (int64_t(1) << 32); }
 
 size_t gmm_workspace(const GmmArgs& a) {
+  if (a.form == GmmForm::kTN)
+    return std::max(range_bytes(a, any_range(a)), tile_sizes(a) ? range_bytes(a, tile_range(a)) : 0);
   const int split = std::max(any_split(a), tile_sizes(a) ? tile_split(a) : 1);
   return split > 1 ? (size_t)split * out_elems(a) * sizeof(float) : 0;
 }
@@ -88,19 +126,22 @@ size_t gmm_workspace(const GmmArgs& a) {
 hipError_t launch_gmm(const GmmArgs& args, void* workspace, hipStream_t s) {
   GmmArgs a = args;
   const bool tile = tile_ok(a);
-  a.split = tile ? tile_split(a) : any_split(a);
+  const int waves = tile_waves(a), edge = any_tile(a);
   a.part = static_cast<float*>(workspace);
-  const int waves = tile_waves(a);
+  if (a.form == GmmForm::kTN)
+    a.range_rows = tile ? tile_range(a) : any_range(a);
+  else
+    a.split = tile ? tile_split(a) : any_split(a);
   hipError_t e;
   if (!tile)
-    e = launch_gmm_any(a, any_tile(a), s);
+    e = launch_gmm_any(a, edge, s);
   else if (a.form == GmmForm::kNN)
     e = launch_gmm_tile_nn(a, waves, s);
   else if (a.form == GmmForm::kTN)
     e = launch_gmm_tile_tn(a, waves, s);
   else
     e = a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, waves, s) : launch_gmm_tile_nt(a, waves, s);
-  return e == hipSuccess && a.split > 1 ? launch_gmm_join(a, s) : e;
+  return e == hipSuccess && (a.split > 1 || a.range_rows) ? launch_gmm_join(a, s) : e;
 }
 
 }  // namespace moe

@@ -451,7 +451,7 @@ inline int64_t gmm_row_grid(const GmmArgs& a, int slabs, int tile) {
   return (per(full) + per(partial)) * kXcds;
 }
 
-// TN: groups x n tiles x slabs, dealt to the XCDs in chunks of consecutive items (groups differ in length, so
+// TN: sums x n tiles x slabs, dealt to the XCDs in chunks of consecutive items (groups differ in length, so
 // that long contiguous ranges could leave XCDs idle): 32 of them, what an XCD runs at once, when every
 // XCD gets 4 chunks or more, else 8.
 __device__ __forceinline__ bool gmm_weight_item(int64_t b, int64_t tiles, int slabs, int chunk, int64_t& tile, int& slab) {
@@ -602,19 +602,17 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   MOE_GMM_SMEM(W)
   int64_t t;
   int slab;
-  [[maybe_unused]] const int sp = (int)(blockIdx.x % (unsigned)a.split);
-  if (!gmm_weight_item(blockIdx.x / (unsigned)a.split, tiles, slabs, chunk, t, slab)) return;
+  if (!gmm_weight_item(blockIdx.x, tiles, slabs, chunk, t, slab)) return;
 #if defined(__HIP_DEVICE_COMPILE__)
   using S = GmmShape<W>;
   using LP = GmmAcross<T, S::kHalf>;
   using LQ = GmmAcross<T, S::kTile>;
-  const int g = (int)(t / p_tiles);
-  const int64_t p0 = (t % p_tiles) * S::kTile, q0 = (int64_t)slab * S::kTile;
-  int64_t beg, end;
-  gmm_group_rows(a.group_offsets, a.max_rows, g, beg, end);
+  GmmSum sum;
+  if (!sum.find(a, t / p_tiles)) return;
+  const int64_t p0 = (t % p_tiles) * S::kTile, q0 = (int64_t)slab * S::kTile, beg = sum.beg, end = sum.end;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave / (W / 2), wc = wave % (W / 2);
   const int64_t ldn = (int64_t)a.N * T::kBytes, ldk = (int64_t)a.K * T::kBytes;
-  const int depth = (int)(end - beg);
+  const int depth = gmm_uniform((int)(end - beg));
   GmmLoadAcross<T, W, kGmmPLoads, false, false> lp[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -631,15 +629,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   for (int i = 0; i < W; ++i)
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[i][s] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int nk;
-  gmm_range(gmm_uniform((depth + LQ::kRows - 1) / LQ::kRows), a.split, sp, lq.step0, nk);
-  lp[0].step0 = lp[1].step0 = lq.step0;
-  gmm_loop<T, W, W>(lp, lq, nk, rings, fp, fq, wave, acc);
+  gmm_loop<T, W, W>(lp, lq, (depth + LQ::kRows - 1) / LQ::kRows, rings, fp, fq, wave, acc);
   GmmOut o;
-  const int e = a.split == 1 && a.out_bf16 ? 2 : 4;
-  char* const out = a.split == 1 ? static_cast<char*>(a.out)
-                                 : reinterpret_cast<char*>(a.part + (int64_t)sp * a.G * a.N * a.K);
-  o.out = out + (((int64_t)g * a.N + p0) * a.K + q0) * e;
+  const int e = sum.whole && a.out_bf16 ? 2 : 4;
+  o.out = sum.matrix(a) + (p0 * a.K + q0) * e;
   o.ld = a.K;
   o.rows = (int)(a.N - p0 < S::kTile ? a.N - p0 : S::kTile);
   o.cols = (int)(a.K - q0 < S::kTile ? a.K - q0 : S::kTile);

@@ -153,6 +153,22 @@ def test_gradient_for_weights(size, dt, gather):
             assert bool((dw[g] == 0).all()), f"empty group {g} has a gradient"
 
 
+# few output tiles and long sums: groups whose rows are cut into ranges, beside groups that are one range or none
+LONG_SUMS = [(1, 5000, 64, 64, "even"), (2, 4099, 200, 136, "even"), (5, 2500, 200, 136, "skew"),
+             (9, 4100, 65, 67, "skew"), (40, 3000, 96, 72, "first"), (40, 3001, 96, 72, "last"),
+             (300, 6000, 128, 264, "skew"), (7, 9000, 520, 8, "skew")]
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gathered"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("size", LONG_SUMS, ids=["-".join(map(str, s)) for s in LONG_SUMS])
+def test_gradient_for_weights_of_long_groups(size, dt, gather):
+    test_gradient_for_weights(size, dt, gather)
+    off, idx, x, _, dy, d_off, d_idx = _case(size, dt, gather, seed=6)
+    dw = moe.moe_grouped_matmul_dw(dy, x, d_off, row_index=d_idx)
+    assert _torch().equal(dw, moe.moe_grouped_matmul_dw(dy, x, d_off, row_index=d_idx))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_one_group_without_offsets(dt):
     torch = _torch()
