@@ -73,15 +73,29 @@ int64_t steps_of(const GmmArgs& a) {
   return (depth * elem_bytes(a) + 127) / 128;
 }
 
-// Small tiles where the large ones would leave slots (two on a CU) empty.
-int any_tile(const GmmArgs& a) { return gmm_any_grid(a, 128) < 2 * kCus ? 64 : 128; }
+int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
+
+// Small tiles where the large ones would leave slots (two on a CU) empty, and where they pad the output by over 15%
+// more, in fp32, which the matrix cores bound (72 groups, 50704 rows, 3608 -> 133: 735 us against 1009), and in the
+// weight gradient, whose sums are short (358 groups, 4008 rows, 192 x 471 in bf16: 48 against 68).  Not for rows of
+// bytes, which the loads bound (63951 rows, 6722 -> 320: 833 against 668).
+int any_tile(const GmmArgs& a) {
+  if (gmm_any_grid(a, 128) < 2 * kCus) return 64;
+  if (a.type != GmmType::kF32 && a.form != GmmForm::kTN) return 128;
+  const int64_t q = a.form == GmmForm::kNT ? a.N : a.K;
+  int64_t large = padded(q, 128), small = padded(q, 64);
+  if (a.form == GmmForm::kTN) {
+    large *= padded(a.N, 128);
+    small *= padded(a.N, 64);
+  }
+  return large * 100 > small * 115 ? 64 : 128;
+}
 // Three work-groups to a CU, ranges of 6 steps: fp32 sums are bound by the matrix cores of few CUs (9 groups, 777
 // rows, 1001 x 515, 32 steps: 56 us in one range, 29 in four; 16 groups, 128 rows, 8 steps: 9 us in one, 13 in
 // two).
 int any_split(const GmmArgs& a) { return split_of(gmm_any_grid(a, any_tile(a)), steps_of(a), 3 * kCus, 6); }
 int64_t any_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, any_tile(a)), 3 * kCus, 6); }
 
-int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
 
 // Waves of the tile kernel's work-groups: 8 (256 x 256 tiles, one work-group to a CU) move half the bytes per
 // product through LDS, 4 (128 x 128, two to a CU) waste less of a small matrix, fill the chip with fewer
