@@ -425,10 +425,12 @@ __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
   store_sums(a, row * q_len + col, n, sum);
 }
 
-// TN: the same for the groups of more than one range; one work-group per 1024 elements of a group's matrix.  Where
-// groups are more than further ranges can be, a group is found by its second range, and work-groups of other
-// ranges do nothing.
-__global__ __launch_bounds__(256) void gmm_join_sums_kernel(GmmArgs a, int per_matrix) {
+// TN: the same for the groups of more than one range; one work-group per `share` elements of a group's matrix.
+// Where groups are more than further ranges can be, a group is found by its second range, and work-groups of
+// other ranges do nothing.  Many of those cost more than the fewer, longer joins of a larger share: 173 groups, 26129
+// rows, 86 x 2320 (7215 work-groups of 1024 elements): equal groups 92 us, 86 with 4096; 279 groups, 20499 skewed
+// rows, 448 x 110 (5194 of them): 100 us, 122 with 4096.
+__global__ __launch_bounds__(256) void gmm_join_sums_kernel(GmmArgs a, int per_matrix, int share) {
   const int64_t range = a.range_rows;
   int g = (int)(blockIdx.x / (unsigned)per_matrix);
   int64_t b, e, second = -1;
@@ -441,25 +443,26 @@ __global__ __launch_bounds__(256) void gmm_join_sums_kernel(GmmArgs a, int per_m
   gmm_group_rows(a.group_offsets, a.max_rows, g, b, e);
   if (second >= 0 ? second != b + range : e - b <= range) return;
   const int64_t all = (int64_t)a.N * a.K;
-  const int64_t i = (int64_t)(blockIdx.x % (unsigned)per_matrix) * 1024 + threadIdx.x * 4;
-  const int n = all - i < 4 ? (int)(all - i) : 4;
-  if (n <= 0) return;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t first = (int64_t)(blockIdx.x % (unsigned)per_matrix) * share;
+  for (int64_t i = first + threadIdx.x * 4; i < first + share && i < all; i += 1024) {
+    const int n = all - i < 4 ? (int)(all - i) : 4;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int64_t r = b; r < e; r += range) {
-    const float* p = a.part + GmmSum::place(r, e - r, range) * all + i;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (n == 4) {
-      __builtin_memcpy(v, p, 16);
-    } else {
+    for (int64_t r = b; r < e; r += range) {
+      const float* p = a.part + GmmSum::place(r, e - r, range) * all + i;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (n == 4) {
+        __builtin_memcpy(v, p, 16);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < n) v[j] = p[j];
+        for (int j = 0; j < 4; ++j)
+          if (j < n) v[j] = p[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += v[j];
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] += v[j];
+    store_sums(a, g * all + i, n, sum);
   }
-  store_sums(a, g * all + i, n, sum);
 }
 
 template <GmmForm F, class T>
@@ -499,8 +502,11 @@ hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s) {
 hipError_t launch_gmm_join(const GmmArgs& a, hipStream_t s) {
   const dim3 block(256);
   if (a.form == GmmForm::kTN) {
-    const int64_t per_matrix = ((int64_t)a.N * a.K + 1023) / 1024;
-    gmm_join_sums_kernel<<<dim3((unsigned)(std::min<int64_t>(a.G, a.max_rows / a.range_rows) * per_matrix)), block, 0, s>>>(a, (int)per_matrix);
+    const int64_t further = a.max_rows / a.range_rows;
+    const int64_t all = (int64_t)a.N * a.K, turns = std::min<int64_t>(a.G, further);
+    const int share = a.G > further && turns * all > 6144 * 1024 ? 4096 : 1024;
+    const int per_matrix = (int)((all + share - 1) / share);
+    gmm_join_sums_kernel<<<dim3((unsigned)(turns * per_matrix)), block, 0, s>>>(a, per_matrix, share);
     return hipGetLastError();
   }
   const int64_t q_len = a.form == GmmForm::kNT ? a.N : a.K;
