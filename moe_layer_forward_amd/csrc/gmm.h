@@ -24,7 +24,7 @@ struct GmmArgs {
   const float* w_scales;         // kI8: [G, N]
   void* out;
   int32_t out_bf16;
-  // Set by launch_gmm.  NT, NN: the contraction cut into `split` ranges whose partial sums (fp32; int32 for kI8)
+  // Set by gmm_plan.  NT, NN: the contraction cut into `split` ranges whose partial sums (fp32; int32 for kI8)
   // go to part, [split, output rows, output columns], for launch_gmm_join.
   int32_t split = 1;
   // TN: the rows of a group cut into ranges of range_rows (0: not cut); those of groups with more than one go to
@@ -34,9 +34,18 @@ struct GmmArgs {
 };
 // The sum over the ranges, in range order, scaled and rounded once into out.
 hipError_t launch_gmm_join(const GmmArgs& a, hipStream_t s);
-// The product, on the kernel that its sizes and alignment call for, and the workspace bytes it needs
-// (decided by type, form and sizes alone).
-hipError_t launch_gmm(const GmmArgs& a, void* workspace, hipStream_t s);
+// The kernel that a product's sizes and alignment call for, and how its sums are split.
+struct GmmPlan {
+  GmmArgs args;      // with split, range_rows and part
+  bool tile;         // the tile kernel, with work-groups of `waves`; or the plain one, with tiles of `edge`
+  int waves, edge;
+  bool once;         // tile: weights read with the non-temporal policy
+  bool join;         // launch_gmm_join follows
+  const char* name;  // of the kernel
+};
+GmmPlan gmm_plan(const GmmArgs& a, void* workspace);
+hipError_t launch_gmm(const GmmPlan& p, hipStream_t s);
+// The workspace bytes it needs (decided by type, form and sizes alone).
 size_t gmm_workspace(const GmmArgs& a);
 // Whether every kernel's grid fits a launch (fewer than 2^32 threads).
 bool gmm_grid_ok(const GmmArgs& a);
@@ -45,11 +54,12 @@ hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s);
 int64_t gmm_any_grid(const GmmArgs& a, int tile);
 // Tiles of 32 waves x 32 waves (waves 8 or 4 per work-group) on rows of whole 16-byte pieces (bf16; int8 for the
 // forward); gmm_tile_items of them at most.
-hipError_t launch_gmm_tile_nt(const GmmArgs& a, int waves, hipStream_t s);
-hipError_t launch_gmm_tile_i8(const GmmArgs& a, int waves, hipStream_t s);
-hipError_t launch_gmm_tile_nn(const GmmArgs& a, int waves, hipStream_t s);
+hipError_t launch_gmm_tile_nt(const GmmArgs& a, int waves, bool once, hipStream_t s);
+hipError_t launch_gmm_tile_i8(const GmmArgs& a, int waves, bool once, hipStream_t s);
+hipError_t launch_gmm_tile_nn(const GmmArgs& a, int waves, bool once, hipStream_t s);
 hipError_t launch_gmm_tile_tn(const GmmArgs& a, int waves, hipStream_t s);
 int64_t gmm_tile_items(const GmmArgs& a, int waves);
+constexpr int64_t kGmmCacheBytes = 256 << 20;  // the last-level cache
 
 // codes[r] = rint(127 v / max|v|), scales[r] = max|v| / 127 of each row v (swiglu: v = SiLU(gate) * up of a
 // row gate | up of 2 cols values).

@@ -120,6 +120,15 @@ int tile_waves(const GmmArgs& a) {
 int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a, tile_waves(a)), steps_of(a), kCus, 8); }
 int64_t tile_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, 32 * tile_waves(a)), kCus, 8); }
 
+// The weights are read with the non-temporal policy where nothing reads them twice: groups of about one row tile,
+// whose weights together exceed the 256 MB of last-level cache that a next call could find them in
+// (gm decode, 384 groups of 1.3 rows: 1.44 -> 1.32 ms; int8, 48 groups: 141 -> 127 us; a 132 MB int8 weight
+// called again and again: 36 us with the default policy, 40 with this one).
+bool tile_once(const GmmArgs& a, int waves) {
+  return a.form != GmmForm::kTN && a.max_rows <= (int64_t)a.G * 32 * waves &&
+         (int64_t)a.G * a.N * a.K * elem_bytes(a) > kGmmCacheBytes;
+}
+
 size_t range_bytes(const GmmArgs& a, int64_t range) {
   return range ? (size_t)(2 * ((a.max_rows + range - 1) / range)) * a.N * a.K * sizeof(float) : 0;
 }
@@ -137,25 +146,27 @@ size_t gmm_workspace(const GmmArgs& a) {
   return split > 1 ? (size_t)split * out_elems(a) * sizeof(float) : 0;
 }
 
-hipError_t launch_gmm(const GmmArgs& args, void* workspace, hipStream_t s) {
-  GmmArgs a = args;
-  const bool tile = tile_ok(a);
-  const int waves = tile_waves(a), edge = any_tile(a);
+GmmPlan gmm_plan(const GmmArgs& args, void* workspace) {
+  static const char* const kNames[2][2] = {{"matmul_tile128", "matmul_tile128_nt"}, {"matmul_tile256", "matmul_tile256_nt"}};
+  GmmPlan p{args, tile_ok(args), tile_waves(args), any_tile(args), false, false, nullptr};
+  GmmArgs& a = p.args;
   a.part = static_cast<float*>(workspace);
   if (a.form == GmmForm::kTN)
-    a.range_rows = tile ? tile_range(a) : any_range(a);
+    a.range_rows = p.tile ? tile_range(a) : any_range(a);
   else
-    a.split = tile ? tile_split(a) : any_split(a);
-  hipError_t e;
-  if (!tile)
-    e = launch_gmm_any(a, edge, s);
-  else if (a.form == GmmForm::kNN)
-    e = launch_gmm_tile_nn(a, waves, s);
-  else if (a.form == GmmForm::kTN)
-    e = launch_gmm_tile_tn(a, waves, s);
-  else
-    e = a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, waves, s) : launch_gmm_tile_nt(a, waves, s);
-  return e == hipSuccess && (a.split > 1 || a.range_rows) ? launch_gmm_join(a, s) : e;
+    a.split = p.tile ? tile_split(a) : any_split(a);
+  p.once = p.tile && tile_once(a, p.waves);
+  p.join = a.split > 1 || a.range_rows;
+  p.name = p.tile ? kNames[p.waves == 8][p.once] : p.edge == 64 ? "matmul_any64" : "matmul_any128";
+  return p;
+}
+
+hipError_t launch_gmm(const GmmPlan& p, hipStream_t s) {
+  const GmmArgs& a = p.args;
+  if (!p.tile) return launch_gmm_any(a, p.edge, s);
+  if (a.form == GmmForm::kNN) return launch_gmm_tile_nn(a, p.waves, p.once, s);
+  if (a.form == GmmForm::kTN) return launch_gmm_tile_tn(a, p.waves, s);
+  return a.type == GmmType::kI8 ? launch_gmm_tile_i8(a, p.waves, p.once, s) : launch_gmm_tile_nt(a, p.waves, p.once, s);
 }
 
 }  // namespace moe

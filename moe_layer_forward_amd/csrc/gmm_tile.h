@@ -336,7 +336,6 @@ struct GmmOut {
   bool bf16;
   bool once;  // non-temporal stores: an output that no cache holds until its reader comes
 };
-constexpr int64_t kGmmCacheBytes = 256 << 20;  // the last-level cache
 
 // value(row block i, Q block s, element e, row, col) -> fp32
 template <int W, int NB, class Value>
@@ -653,13 +652,8 @@ hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The weights are read with the non-temporal policy where nothing reads them twice: groups of about one row tile,
-// whose weights together exceed the 256 MB of last-level cache that a next call could find them in
-// (gm decode, 384 groups of 1.3 rows: 1.44 -> 1.32 ms; int8, 48 groups: 141 -> 127 us; a 132 MB int8 weight
-// called again and again: 36 us with the default policy, 40 with this one).
 template <GmmForm F, class T>
-hipError_t gmm_launch_rows(const GmmArgs& a, int waves, hipStream_t s) {
-  const bool once = a.max_rows <= (int64_t)a.G * 32 * waves && (int64_t)a.G * a.N * a.K * T::kBytes > kGmmCacheBytes;
+hipError_t gmm_launch_rows(const GmmArgs& a, int waves, bool once, hipStream_t s) {
   if (waves == 8) return once ? gmm_launch_rows<F, T, 8, true>(a, s) : gmm_launch_rows<F, T, 8, false>(a, s);
   return once ? gmm_launch_rows<F, T, 4, true>(a, s) : gmm_launch_rows<F, T, 4, false>(a, s);
 }

@@ -572,12 +572,14 @@ int matmul_type(const char* fn, int32_t dtype, moe::GmmType* t) {
   return MOE_OK;
 }
 
-int run_matmul(const char* fn, const char* kernel, const moe::GmmArgs& a, void* workspace, size_t workspace_bytes,
-               void* stream) {
+int run_matmul(const char* fn, const moe::GmmArgs& a, void* workspace, size_t workspace_bytes, void* stream) {
   const int st = check_ws(workspace, workspace_bytes, moe::gmm_workspace(a));
   if (st) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return device_status(timed(kernel, s, [&] { return moe::launch_gmm(a, workspace, s); }), fn);
+  const moe::GmmPlan p = moe::gmm_plan(a, workspace);
+  hipError_t e = timed(p.name, s, [&] { return moe::launch_gmm(p, s); });
+  if (e == hipSuccess && p.join) e = timed("matmul_join", s, [&] { return moe::launch_gmm_join(p.args, s); });
+  return device_status(e, fn);
 }
 
 // ----------------------------------------------------------------------------- no-allocation forward
@@ -955,7 +957,7 @@ int moe_grouped_matmul(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, co
                                {x, elem_bytes(dtype), "x"}, {w, elem_bytes(dtype), "w"},
                                {y, elem_bytes(y_dtype), "y"}})))
     return st;
-  return run_matmul(fn, "grouped_matmul", a, workspace, workspace_bytes, stream);
+  return run_matmul(fn, a, workspace, workspace_bytes, stream);
 }
 
 int moe_grouped_matmul_dx(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
@@ -982,7 +984,7 @@ int moe_grouped_matmul_dx(int32_t dtype, int32_t n_groups, int32_t N, int32_t K,
   if ((st = check_aligned(fn, {{group_offsets, 4, "group_offsets"}, {dy, elem_bytes(dtype), "dy"},
                                {w, elem_bytes(dtype), "w"}, {dx, elem_bytes(dx_dtype), "dx"}})))
     return st;
-  return run_matmul(fn, "grouped_matmul_dx", a, workspace, workspace_bytes, stream);
+  return run_matmul(fn, a, workspace, workspace_bytes, stream);
 }
 
 int moe_grouped_matmul_dw(int32_t dtype, int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets,
@@ -1013,7 +1015,7 @@ int moe_grouped_matmul_dw(int32_t dtype, int32_t n_groups, int32_t N, int32_t K,
                                {dy, elem_bytes(dtype), "dy"}, {x, elem_bytes(dtype), "x"},
                                {dw, elem_bytes(dw_dtype), "dw"}})))
     return st;
-  return run_matmul(fn, "grouped_matmul_dw", a, workspace, workspace_bytes, stream);
+  return run_matmul(fn, a, workspace, workspace_bytes, stream);
 }
 
 int moe_quantize_rows(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, int8_t* codes,
@@ -1070,7 +1072,7 @@ int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_o
                                {x_scales, 4, "x_scales"}, {w_scales, 4, "w_scales"},
                                {y, elem_bytes(y_dtype), "y"}})))
     return st;
-  return run_matmul(fn, "matmul_i8", a, workspace, workspace_bytes, stream);
+  return run_matmul(fn, a, workspace, workspace_bytes, stream);
 }
 
 const char* moe_last_error(void) { return g_last_error.c_str(); }
