@@ -56,3 +56,153 @@ def test_profile_has_one_entry_per_launch():
         _, got = _launched(call)
         assert [k for k, _ in got] == want
         assert all(ms > 0 for _, ms in got)
+
+
+# --------------------------------------------------------------------------- the 256 x 256 and non-temporal kernels
+# Small whole numbers: every partial sum is a whole number below 2^24, so that fp32 sums are exact in any
+# order and each output has to equal the formula's, rounded once.  A term that is lost, doubled or taken from a
+# neighbour (a wait too few, a wrong stage or row) shows by itself.
+TOP = 4
+
+
+def _ints(gen, *shape, top=TOP):
+    torch = _torch()
+    return torch.randint(-top, top + 1, shape, generator=gen, device="cuda", dtype=torch.int8)
+
+
+def _offsets(sizes):
+    torch = _torch()
+    off = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    return off, torch.from_numpy(off).cuda()
+
+
+def _exact(a, b, out_dtype, scale=None):
+    """a b of whole numbers (float64 holds them), rounded once to out_dtype."""
+    torch = _torch()
+    y = a.double() @ b.double().contiguous()
+    if scale is not None:
+        y = y * scale
+    return y.float().to(out_dtype) if out_dtype == torch.bfloat16 else y.to(out_dtype)
+
+
+# a partial tile of 1 to 8 blocks of 32 rows, alone and after a full tile; an empty group between them
+ALL_BLOCKS = [20, 256 + 50, 90, 0, 120, 256 + 150, 190, 256 + 220, 250]
+
+
+def _rows_case(op, sizes, N, K, gather, seed):
+    torch = _torch()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    off, d_off = _offsets(sizes)
+    rows, G = int(off[-1]), len(sizes)
+    depth = N if op == "dx" else K
+    x_rows = rows // 3 if gather else rows
+    x = _ints(gen, x_rows, depth)
+    w = _ints(gen, G, N, K)
+    idx = torch.randint(0, x_rows, (rows,), generator=gen, device="cuda", dtype=torch.int32) if gather else None
+    return off, d_off, x, w, idx
+
+
+def _check_rows(op, kernel, sizes, N, K, gather, out_name, seed):
+    torch = _torch()
+    off, d_off, x, w, idx = _rows_case(op, sizes, N, K, gather, seed)
+    out_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[out_name]
+    out = torch.full((int(off[-1]), K if op == "dx" else N), float("nan"), dtype=out_dtype, device="cuda")
+    xs = ws = None
+    if op == "i8":
+        # powers of two, so that the scaled values are exact too
+        xs = 2.0 ** (torch.arange(x.shape[0], device="cuda") % 5 - 2).float()
+        ws = 2.0 ** (torch.arange(len(sizes) * N, device="cuda") % 7 - 3).float().view(len(sizes), N)
+
+        def call():
+            return moe.moe_matmul_i8(x, xs, w, ws, d_off, row_index=idx, out=out)
+    else:
+        xb, wb = x.bfloat16(), w.bfloat16()
+
+        def call():
+            if op == "dx":
+                return moe.moe_grouped_matmul_dx(xb, wb, d_off, out=out)
+            return moe.moe_grouped_matmul(xb, wb, d_off, row_index=idx, out=out)
+
+    _, names = _launched(call)
+    assert [k for k, _ in names] == [kernel]
+    first = out.clone()
+    rows_x = x if idx is None else x[idx.long()]
+    for g in range(len(sizes)):
+        r = slice(int(off[g]), int(off[g + 1]))
+        scale = None
+        if op == "i8":
+            rs = xs if idx is None else xs[idx.long()]
+            scale = rs[r, None].double() * ws[g].double()
+        want = _exact(rows_x[r], w[g] if op == "dx" else w[g].T, out_dtype, scale)
+        assert torch.equal(first[r], want), f"group {g}: {int((first[r] != want).sum())} values differ"
+    for _ in range(3):  # behind one another, over the last results
+        call()
+    assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("steps", range(1, 15))
+@pytest.mark.parametrize("op", ["forward", "dx", "i8"])
+def test_rows_in_256_tiles(op, steps):
+    """Sums of 1 to 14 steps: the first step, the six-fold loop and each of its tails, in every number of blocks."""
+    depth = {"forward": 64 * steps - 40, "dx": 64 * steps - 40, "i8": 128 * steps - 48}[op]
+    if steps % 3 == 0:  # whole steps
+        depth = (128 if op == "i8" else 64) * steps
+    N, K = (depth, 8072) if op == "dx" else (8072, depth)
+    _check_rows(op, "matmul_tile256", ALL_BLOCKS, N, K, op != "dx" and steps % 2 == 1,
+                "f32" if steps % 4 < 2 else "bf16", steps)
+
+
+@pytest.mark.parametrize("out_name", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["forward", "dx", "i8"])
+@pytest.mark.parametrize("rows,kernel", [("many", "matmul_tile256_nt"), ("few", "matmul_tile128_nt")])
+def test_streamed_weights(op, out_name, rows, kernel):
+    """More than 256 MB of weights, read once: groups of about a tile of rows (one has several tiles) and of few."""
+    sizes = [60, 0, 250, 700, 33, 1] + [20] * 18 if rows == "many" else [8, 0, 1, 60, 131] + [0] * 19
+    K = 5616 if op == "i8" else 2808
+    _check_rows(op, kernel, sizes, 2024, K, op != "dx" and out_name == "f32", out_name, 50)
+
+
+def _check_weights(sizes, N, K, gather, out_name, names, seed):
+    torch = _torch()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    off, d_off = _offsets(sizes)
+    rows, G = int(off[-1]), len(sizes)
+    x_rows = rows // 3 if gather else rows
+    dy, x = _ints(gen, rows, N), _ints(gen, x_rows, K)
+    idx = torch.randint(0, x_rows, (rows,), generator=gen, device="cuda", dtype=torch.int32) if gather else None
+    out_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[out_name]
+    out = torch.full((G, N, K), float("nan"), dtype=out_dtype, device="cuda")
+    dyb, xb = dy.bfloat16(), x.bfloat16()
+
+    def call():
+        return moe.moe_grouped_matmul_dw(dyb, xb, d_off, row_index=idx, out=out)
+
+    _, got = _launched(call)
+    assert [k for k, _ in got] == names
+    first = out.clone()
+    xr = x if idx is None else x[idx.long()]
+    for g in range(G):
+        r = slice(int(off[g]), int(off[g + 1]))
+        want = _exact(dy[r].T, xr[r], out_dtype)
+        assert torch.equal(first[g], want), f"group {g}: {int((first[g] != want).sum())} values differ"
+    for _ in range(3):
+        call()
+    assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("out_name", ["bf16", "f32"])
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gathered"])
+def test_weights_in_256_tiles(gather, out_name):
+    """Groups of 0 to 14 steps of 64 rows, and rows that end inside a step, in one call."""
+    sizes = [0, 1, 63, 64, 65, 130, 192, 250, 320, 384, 447, 512, 570, 640, 700, 769, 830, 896]
+    _check_weights(sizes, 1000, 2024, gather, out_name, ["matmul_tile256"], 60)
+
+
+@pytest.mark.parametrize("out_name", ["bf16", "f32"])
+@pytest.mark.parametrize("gather", [False, True], ids=["rows", "gathered"])
+def test_weights_in_256_tiles_of_cut_groups(gather, out_name):
+    """One group holds most of the rows and is cut into ranges; the others are written at once."""
+    sizes = [9000, 0, 1700, 1] + [331] * 15 + [334]
+    _check_weights(sizes, 696, 696, gather, out_name, ["matmul_tile256", "matmul_join"], 61)
