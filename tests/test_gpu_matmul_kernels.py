@@ -206,3 +206,73 @@ def test_weights_in_256_tiles_of_cut_groups(gather, out_name):
     """One group holds most of the rows and is cut into ranges; the others are written at once."""
     sizes = [9000, 0, 1700, 1] + [331] * 15 + [334]
     _check_weights(sizes, 696, 696, gather, out_name, ["matmul_tile256", "matmul_join"], 61)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("long,gather", [("rows_in", False), ("rows_out", False), ("rows_out", True)],
+                         ids=["rows_in", "rows_out", "rows_out_gathered"])
+def test_rows_past_4_gib(long, dt, gather):
+    """dy or x of more than 4 GiB, a long group that crosses the boundary and short ones wholly past it: all three
+    products, exact (sums of at most 400,000 products of up to 2^4 stay below 2^24).  A gathered x is below 4 GiB."""
+    torch = _torch()
+    wide = 4096 if dt == "bf16" else 2048  # 8 KiB a row: row 524,288 is the first past 4 GiB
+    N, K = (16, wide) if long == "rows_in" else (wide, 16)
+    sizes = [300_000, 100, 299_900, 0, 101, 65, 3, 99_831]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    off, d_off = _offsets(sizes)
+    rows, G = int(off[-1]), len(sizes)
+    x_rows = 5000 if gather else rows
+    x, dy, w = _ints(gen, x_rows, K), _ints(gen, rows, N), _ints(gen, G, N, K)
+    idx = torch.randint(0, x_rows, (rows,), generator=gen, device="cuda", dtype=torch.int32) if gather else None
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    xb, dyb, wb = x.to(dtype), dy.to(dtype), w.to(dtype)
+    y = moe.moe_grouped_matmul(xb, wb, d_off, row_index=idx)
+    dx = moe.moe_grouped_matmul_dx(dyb, wb, d_off)
+    dw = moe.moe_grouped_matmul_dw(dyb, xb, d_off, row_index=idx, dw_dtype=moe.MOE_F32)
+    xr = x if idx is None else x[idx.long()]
+    for g in range(G):
+        b, e = int(off[g]), int(off[g + 1])
+        parts = [slice(b, e)] if e - b < 1000 else [slice(b, b + 300), slice(e - 300, e)]
+        if b < 524_288 < e:
+            parts.append(slice(524_288 - 200, 524_288 + 200))
+        for r in parts:
+            assert torch.equal(y[r], _exact(xr[r], w[g].T, dtype)), f"y, group {g}, rows {r}"
+            assert torch.equal(dx[r], _exact(dy[r], w[g], dtype)), f"dx, group {g}, rows {r}"
+        want = torch.zeros((N, K), dtype=torch.float64, device="cuda")
+        for i in range(b, e, 50_000):
+            r = slice(i, min(i + 50_000, e))
+            want += dy[r].double().T @ xr[r].double()
+        assert torch.equal(dw[g].double(), want), f"dw of group {g}"
+
+
+@pytest.mark.parametrize("size", [(3, 120, 72, 56), (5, 600, 264, 136)])
+def test_gradients_against_differences_along_their_signs(size):
+    """As the product is linear, <dy, y(x + d) - y(x - d)> / 2 = <dx, d> without truncation error.  Along d = the
+    sign of the formula's gradient the right side is the sum of its magnitudes, so that no wrong gradient comes
+    near it: the bound is 2^-13 of that sum, and the fp32 roundings of both sides, of relative size
+    sqrt(depth) 2^-24 and independent from output to output, are two orders below it."""
+    torch = _torch()
+    G, rows, N, K = size
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(12)
+    cuts = np.sort(np.random.default_rng(4).integers(0, rows + 1, G - 1))
+    off, d_off = _offsets(np.diff(np.concatenate([[0], cuts, [rows]])))
+    x = torch.randn((rows // 3, K), generator=gen, device="cuda")
+    w = torch.randn((G, N, K), generator=gen, device="cuda")
+    dy = torch.randn((rows, N), generator=gen, device="cuda")
+    idx = torch.randint(0, rows // 3, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    xr = x[idx.long()].contiguous()
+    d, e = torch.zeros_like(xr), torch.zeros_like(w)
+    for g in range(G):
+        r = slice(int(off[g]), int(off[g + 1]))
+        d[r] = torch.sign(dy[r].double() @ w[g].double()).float()
+        e[g] = torch.sign(dy[r].double().T @ xr[r].double()).float()
+    dx = moe.moe_grouped_matmul_dx(dy, w, d_off).double()
+    plus, minus = (moe.moe_grouped_matmul(xr + s * d, w, d_off).double() for s in (1, -1))
+    lhs, rhs = float(((plus - minus) / 2 * dy.double()).sum()), float((dx * d.double()).sum())
+    assert rhs > 0 and abs(lhs - rhs) <= 2.0 ** -13 * lhs
+    dw = moe.moe_grouped_matmul_dw(dy, x, d_off, row_index=idx).double()
+    plus, minus = (moe.moe_grouped_matmul(x, w + s * e, d_off, row_index=idx).double() for s in (1, -1))
+    lhs, rhs = float(((plus - minus) / 2 * dy.double()).sum()), float((dw * e.double()).sum())
+    assert rhs > 0 and abs(lhs - rhs) <= 2.0 ** -13 * lhs
