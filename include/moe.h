@@ -285,8 +285,9 @@ int moe_forward_fp8(const moe_config* cfg, int64_t T, const void* x, const void*
  *   x_rows     rows x has; row_index NULL: x_rows >= max_rows and row r reads x[r]
  *   row_index  [max_rows] int32 or NULL: row r reads x[row_index[r]], each in [0, x_rows) (others are
  *              moved inside: they read no memory outside x, their results are unspecified)
- * Sizes: any N, K from 1 to 2^20, any max_rows, 1 <= n_groups <= 4096; one group's weight and, with a
- * row_index, all of x below 4 GiB (else MOE_ERR_UNSUPPORTED).  Matrices need only start on a boundary of
+ * Sizes: any N, K from 1 to 2^20, 0 <= max_rows, x_rows <= 2^31-1, 1 <= n_groups <= 4096; one group's weight and, with a
+ * row_index, all of x below 4 GiB; an output of at most 2^31 tiles of 64 x 64, counting a partial tile of every
+ * group (16 TiB of bf16) (else MOE_ERR_UNSUPPORTED).  Matrices need only start on a boundary of
  * their element size; those that start on 16 bytes and whose rows are multiples of 16 bytes run on the
  * fast kernels.
  * Infinities and NaN follow the sums they are part of: a value in one row (or group) never reaches the
@@ -328,7 +329,7 @@ int moe_grouped_matmul_dw(int32_t dtype, int32_t n_groups, int32_t N, int32_t K,
  * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up side by side, and
  * v = SiLU(gate) * up in fp32.  A row with an infinity or NaN in v gets the scale NaN and codes 0.
  *   x of x_dtype (MOE_BF16 or MOE_F32); codes [rows, cols] int8 out; scales [rows] fp32 out
- * 1 <= cols <= 2^20.  No workspace. */
+ * 1 <= cols <= 2^20, rows <= 2^31-1.  No workspace. */
 int moe_quantize_rows(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, int8_t* codes,
                       float* scales, void* stream);
 

@@ -47,7 +47,14 @@ GmmPlan gmm_plan(const GmmArgs& a, void* workspace);
 hipError_t launch_gmm(const GmmPlan& p, hipStream_t s);
 // The workspace bytes it needs (decided by type, form and sizes alone).
 size_t gmm_workspace(const GmmArgs& a);
-// Whether every kernel's grid fits a launch (fewer than 2^32 threads).
+// A grid of n work-groups (n < 2^32): a launch takes fewer than 2^32 threads in each dimension, so those past
+// kGmmGridX go to further rows of the grid.  A multiple of 8, so that work-group n still runs on XCD n % 8.
+// The last row may have work-groups past n: kernels return for them.
+constexpr unsigned kGmmGridX = 1u << 22;
+inline dim3 gmm_grid(int64_t n) {
+  return n <= kGmmGridX ? dim3((unsigned)n) : dim3(kGmmGridX, (unsigned)((n + kGmmGridX - 1) / kGmmGridX));
+}
+// Whether the work-groups of every kernel number fewer than 2^32.
 bool gmm_grid_ok(const GmmArgs& a);
 // Any sizes and any element alignment, in tiles of 64 x 64 or 128 x 128 (gmm_any_grid of them at most).
 hipError_t launch_gmm_any(const GmmArgs& a, int tile, hipStream_t s);

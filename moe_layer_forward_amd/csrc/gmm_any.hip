@@ -154,8 +154,8 @@ __global__ __launch_bounds__(kAnyThreads, kTile == 128 ? 2 : 4) void gmm_any_ker
   // which tile: NT / NN a row tile of a group x a column slab, TN a (group, n tile, k tile); which range
   const int64_t q_len = F == GmmForm::kNT ? a.N : a.K;
   const int q_tiles = (int)((q_len + kTile - 1) / kTile);
-  const int sp = (int)(blockIdx.x % (unsigned)a.split);
-  int64_t item = blockIdx.x / (unsigned)a.split;
+  const int sp = (int)(gmm_block() % (unsigned)a.split);
+  int64_t item = gmm_block() / (unsigned)a.split;
   if constexpr (F == GmmForm::kTN) {
     // Where every group is cut, consecutive work-groups take different sums: the tiles of one read the same rows,
     // and so fall on few XCDs (work-group b runs on XCD b % 8), whose L2 hold them.
@@ -467,7 +467,7 @@ __global__ __launch_bounds__(256) void gmm_join_sums_kernel(GmmArgs a, int per_m
 
 template <GmmForm F, class T>
 hipError_t launch_any(const GmmArgs& a, int tile, hipStream_t s) {
-  const dim3 grid((unsigned)(gmm_any_grid(a, tile) * a.split)), block(kAnyThreads);
+  const dim3 grid = gmm_grid(gmm_any_grid(a, tile) * a.split), block(kAnyThreads);
   if (tile == 64)
     gmm_any_kernel<F, T, 64><<<grid, block, 0, s>>>(a);
   else

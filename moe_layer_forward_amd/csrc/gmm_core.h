@@ -264,6 +264,9 @@ struct GmmTiles {
   }
 };
 
+// Work-group number of a grid of gmm_grid.
+__device__ __forceinline__ unsigned gmm_block() { return blockIdx.y * kGmmGridX + blockIdx.x; }
+
 // Share sp of nk contraction steps cut into `split` nearly equal ranges.
 __device__ __forceinline__ void gmm_range(int nk, int split, int sp, int& first, int& n) {
   first = (int)((int64_t)nk * sp / split);
@@ -293,6 +296,7 @@ struct GmmSum {
       }
       return true;
     }
+    if (!range) return false;
     const int lane = threadIdx.x & 63, per = (a.G + 63) / 64;
     const auto further = [&](int gg) {
       gmm_group_rows(a.group_offsets, a.max_rows, gg, beg, end);

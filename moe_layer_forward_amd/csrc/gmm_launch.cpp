@@ -135,9 +135,8 @@ size_t range_bytes(const GmmArgs& a, int64_t range) {
 
 }  // namespace
 
-// Grids of at most 2^32 threads: the 64 x 64 tiles are the most work-groups (of 256 threads); the 256 x 256 ones
-// (512 threads) are fewer even where their number is rounded up to twice.
-bool gmm_grid_ok(const GmmArgs& a) { return 512 * gmm_any_grid(a, 64) < (int64_t(1) << 32); }
+// The 64 x 64 tiles are the most work-groups; the others are fewer even where their number is rounded up to twice.
+bool gmm_grid_ok(const GmmArgs& a) { return gmm_any_grid(a, 64) <= (int64_t(1) << 31); }
 
 size_t gmm_workspace(const GmmArgs& a) {
   if (a.form == GmmForm::kTN)

@@ -569,10 +569,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   using S = GmmShape<W>;
   int64_t beg, end;
   int t, slab, g;
-  [[maybe_unused]] const int sp = (int)(blockIdx.x % (unsigned)a.split);
+  [[maybe_unused]] const int sp = (int)(gmm_block() % (unsigned)a.split);
   GmmTiles tiles;
   tiles.count(a.group_offsets, a.G, a.max_rows, S::kTile);
-  if (!gmm_row_item(blockIdx.x / (unsigned)a.split, tiles, slabs, t, slab)) return;
+  if (!gmm_row_item(gmm_block() / (unsigned)a.split, tiles, slabs, t, slab)) return;
   tiles.find(a.group_offsets, a.G, a.max_rows, S::kTile, t, g, beg, end);
 #if defined(__HIP_DEVICE_COMPILE__)
   const int64_t q0 = (int64_t)slab * S::kTile;
@@ -601,7 +601,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   MOE_GMM_SMEM(W)
   int64_t t;
   int slab;
-  if (!gmm_weight_item(blockIdx.x, tiles, slabs, chunk, t, slab)) return;
+  if (!gmm_weight_item(gmm_block(), tiles, slabs, chunk, t, slab)) return;
 #if defined(__HIP_DEVICE_COMPILE__)
   using S = GmmShape<W>;
   using LP = GmmAcross<T, S::kHalf>;
@@ -648,7 +648,7 @@ hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
   using S = GmmShape<W>;
   const int slabs = ((F == GmmForm::kNT ? a.N : a.K) + S::kTile - 1) / S::kTile;
   gmm_rows_kernel<F, T, W, kOnce>
-      <<<dim3((unsigned)(gmm_row_grid(a, slabs, S::kTile) * a.split)), dim3(S::kThreads), 0, s>>>(a, slabs);
+      <<<gmm_grid(gmm_row_grid(a, slabs, S::kTile) * a.split), dim3(S::kThreads), 0, s>>>(a, slabs);
   return hipGetLastError();
 }
 

@@ -10,7 +10,7 @@ hipError_t launch_weights(const GmmArgs& a, hipStream_t s) {
   const int p_tiles = (a.N + kTile - 1) / kTile, slabs = (a.K + kTile - 1) / kTile;
   const int64_t tiles = gmm_max_sums(a) * p_tiles, items = tiles * slabs;
   const int chunk = gmm_weight_chunk(items);
-  const dim3 grid((unsigned)gmm_weight_grid(items)), block(64 * W);
+  const dim3 grid = gmm_grid(gmm_weight_grid(items)), block(64 * W);
   if (a.row_index)
     gmm_weights_kernel<GmmBf16, W, true><<<grid, block, 0, s>>>(a, tiles, slabs, p_tiles, chunk);
   else

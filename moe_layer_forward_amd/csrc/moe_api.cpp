@@ -549,9 +549,8 @@ int check_matmul(const char* fn, const moe::GmmArgs& a, int32_t out_dtype) {
     return fail(MOE_ERR_UNSUPPORTED, "%s: N and K must be at most %d", fn, kMaxMatmulSide);
   if (a.type == GmmType::kI8 && a.K > kMaxI8Depth)
     return fail(MOE_ERR_UNSUPPORTED, "%s: K must be at most %d for exact int32 sums", fn, kMaxI8Depth);
-  // 32-bit offsets in the kernels' descriptors, with room for one past every end
-  constexpr int64_t kSpan = (int64_t(1) << 32) - 256;
-  if ((int64_t)a.N * a.K * e > kSpan)
+  constexpr int64_t kSpan = int64_t(1) << 32;  // 32-bit byte offsets
+  if ((int64_t)a.N * a.K * e >= kSpan)
     return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weight must stay below 4 GiB", fn);
   if (!a.group_offsets && a.G != 1)
     return fail(MOE_ERR_INVALID_ARG, "%s: group_offsets may be NULL for one group only", fn);
@@ -559,10 +558,10 @@ int check_matmul(const char* fn, const moe::GmmArgs& a, int32_t out_dtype) {
     if (a.x_rows < 0 || (a.row_index ? a.x_rows == 0 && a.max_rows > 0 : a.x_rows < a.max_rows))
       return fail(MOE_ERR_INVALID_ARG, "%s: x has too few rows (%lld)", fn, (long long)a.x_rows);
     if (a.x_rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: x_rows exceeds 2^31-1", fn);
-    if (a.row_index && a.x_rows * a.K * e >= (int64_t(1) << 32))
+    if (a.row_index && a.x_rows * a.K * e >= kSpan)
       return fail(MOE_ERR_UNSUPPORTED, "%s: a gathered x must stay below 4 GiB", fn);
   }
-  if (!moe::gmm_grid_ok(a)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many output tiles for one launch", fn);
+  if (!moe::gmm_grid_ok(a)) return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 output tiles", fn);
   return MOE_OK;
 }
 
@@ -1029,7 +1028,7 @@ int moe_quantize_rows(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swigl
   if (cols < 1) return fail(MOE_ERR_INVALID_ARG, "%s: cols must be positive", fn);
   if (swiglu != 0 && swiglu != 1) return fail(MOE_ERR_INVALID_ARG, "%s: swiglu must be 0 or 1", fn);
   if (cols > kMaxMatmulSide) return fail(MOE_ERR_UNSUPPORTED, "%s: cols must be at most %d", fn, kMaxMatmulSide);
-  if (rows > (1 << 23)) return fail(MOE_ERR_UNSUPPORTED, "%s: rows must be at most 2^23", fn);
+  if (rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: rows exceeds 2^31-1", fn);
   if (rows == 0) return ok();
   if (!x || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "%s: x, codes and scales are required", fn);
   if ((st = check_aligned(fn, {{x, elem_bytes(x_dtype), "x"}, {scales, 4, "scales"}}))) return st;

@@ -126,8 +126,8 @@ template <class In, bool kSwiglu, int kLanes>
 __global__ __launch_bounds__(kQuantThreads) void quantize_rows_kernel(const In* x, int64_t rows, int64_t cols,
                                                                       int8_t* codes, float* scales) {
   const int lane = threadIdx.x % kLanes;
-  const int64_t r = (int64_t)blockIdx.x * (kQuantThreads / kLanes) + threadIdx.x / kLanes;
-  if (kLanes < kQuantThreads && r >= rows) return;  // a whole wave; the work-group form has one row each
+  const int64_t r = ((int64_t)blockIdx.y * kGmmGridX + blockIdx.x) * (kQuantThreads / kLanes) + threadIdx.x / kLanes;
+  if (r >= rows) return;  // a whole wave or work-group
   const In* row = x + r * cols * (kSwiglu ? 2 : 1);
   float held[kHeld][8];
   uint32_t m = 0;
@@ -184,11 +184,10 @@ hipError_t launch_q(const void* x, int64_t rows, int64_t cols, int8_t* codes, fl
   const In* p = static_cast<const In*>(x);
   if (cols <= 64 * 8 * kHeld / 2) {  // half the held chunks: a wave still has loads of several rows in flight
     const int64_t grid = (rows + kQuantThreads / 64 - 1) / (kQuantThreads / 64);
-    quantize_rows_kernel<In, kSwiglu, 64><<<dim3((unsigned)grid), dim3(kQuantThreads), 0, s>>>(p, rows, cols, codes,
-                                                                                              scales);
+    quantize_rows_kernel<In, kSwiglu, 64><<<gmm_grid(grid), dim3(kQuantThreads), 0, s>>>(p, rows, cols, codes, scales);
   } else {
-    quantize_rows_kernel<In, kSwiglu, kQuantThreads><<<dim3((unsigned)rows), dim3(kQuantThreads), 0, s>>>(
-        p, rows, cols, codes, scales);
+    quantize_rows_kernel<In, kSwiglu, kQuantThreads><<<gmm_grid(rows), dim3(kQuantThreads), 0, s>>>(p, rows, cols, codes,
+                                                                                                   scales);
   }
   return hipGetLastError();
 }

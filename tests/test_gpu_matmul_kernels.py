@@ -276,3 +276,33 @@ def test_gradients_against_differences_along_their_signs(size):
     plus, minus = (moe.moe_grouped_matmul(x, w + s * e, d_off, row_index=idx).double() for s in (1, -1))
     lhs, rhs = float(((plus - minus) / 2 * dy.double()).sum()), float((dw * e.double()).sum())
     assert rhs > 0 and abs(lhs - rhs) <= 2.0 ** -13 * lhs
+
+
+# --------------------------------------------------------------------------- very many output tiles
+@pytest.mark.parametrize("op,depth,kernel", [
+    ("forward", 8, "matmul_tile128_nt"), ("dx", 8, "matmul_tile128_nt"), ("i8", 16, "matmul_tile128_nt"),
+    ("forward", 1, "matmul_any128"), ("dx", 1, "matmul_any128"), ("i8", 1, "matmul_any128")])
+def test_rows_of_four_million_tiles(op, depth, kernel):
+    """513 groups of 8192 tiles each: more work-groups than one row of the grid holds."""
+    sizes = [1, 2, 0] + [1] * 510
+    N, K = (depth, 1 << 20) if op == "dx" else (1 << 20, depth)
+    # dx, depth 1: rows of W are whole 16-byte pieces, rows of dy (one value) are not
+    _check_rows(op, kernel, sizes, N, K, op != "dx", "bf16", 70)
+
+
+@pytest.mark.parametrize("K,kernel", [(8, "matmul_tile128"), (1, "matmul_any64")])
+def test_weights_of_four_million_tiles(K, kernel):
+    _check_weights([1, 2, 0] + [1] * 510, 1 << 20, K, True, "bf16", [kernel], 71)
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 24) + 5, 8), ((1 << 22) + 3, 2056)])
+def test_quantize_more_rows_than_a_grid_row(rows, cols):
+    torch = _torch()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(9)
+    x = _ints(gen, rows, cols, top=127).bfloat16()
+    x[:, cols - 1] = -127  # the codes are then the values themselves
+    codes, scales = moe.moe_quantize_rows(x)
+    assert bool((scales == 1).all())
+    for i in range(0, rows, 1 << 20):
+        assert torch.equal(codes[i:i + (1 << 20)].bfloat16(), x[i:i + (1 << 20)])
