@@ -3,8 +3,9 @@
     python examples/expert_products.py
 
 The layer is the library's (sigmoid router, top-K, SwiGLU experts, weighted combine), with the experts as plain
-tensors: ``GroupedProduct`` makes ``moe_grouped_matmul`` differentiable with ``moe_grouped_matmul_dx`` and
-``moe_grouped_matmul_dw``, and ``int8_experts`` runs the trained experts through ``moe_quantize_rows`` and
+tensors: ``moe_grouped_matmul`` is differentiable by itself; ``GroupedProduct`` is the same node written out with
+``moe_grouped_matmul_dx`` and ``moe_grouped_matmul_dw``, where the routing knows each token's rows and ``moe_combine``
+adds their gradients in one pass.  ``int8_experts`` runs the trained experts through ``moe_quantize_rows`` and
 ``moe_matmul_i8``.
 """
 import os

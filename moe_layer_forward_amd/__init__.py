@@ -446,12 +446,58 @@ def _matmul_ws(workspace, op, dtype, G, rows, N, K, dev):
     return ws, ws.data_ptr(), n
 
 
+_grouped_product = None
+
+
+def _differentiable_product(*args):
+    """moe_grouped_matmul as a node of torch's graph (its class is made at the first call: torch is imported late)."""
+    global _grouped_product
+    if _grouped_product is None:
+        import torch
+        from torch.autograd.function import once_differentiable
+
+        class GroupedProduct(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, w, group_offsets, row_index, y_dtype, workspace):
+                ctx.save_for_backward(x, w, group_offsets, row_index)
+                return moe_grouped_matmul(x, w, group_offsets, row_index, y_dtype, workspace)
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy):
+                x, w, group_offsets, row_index = ctx.saved_tensors
+                dy = dy.to(x.dtype).contiguous()  # a float32 y of bfloat16 operands: dy in their type, as torch's casts do
+                dx = dw = None
+                if ctx.needs_input_grad[0]:
+                    # zeros: rows past the last group have no gradient, and the product does not write them
+                    rows = torch.zeros((dy.shape[0], x.shape[1]), device=x.device,
+                                       dtype=x.dtype if row_index is None else torch.float32)
+                    dx = moe_grouped_matmul_dx(dy, w, group_offsets, out=rows)
+                    if row_index is not None:  # a row of x that was gathered several times: the sum, in float32
+                        at = row_index.clamp(0, max(x.shape[0] - 1, 0)).long()
+                        dx = torch.zeros(x.shape, device=x.device).index_put_((at,), rows, accumulate=True).to(x.dtype)
+                if ctx.needs_input_grad[1]:
+                    dw = moe_grouped_matmul_dw(dy, x, group_offsets, row_index=row_index)
+                return dx, dw, None, None, None, None
+
+        _grouped_product = GroupedProduct
+    return _grouped_product.apply(*args)
+
+
 def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, workspace=None, out=None):
     """Product of ragged row groups with their group's weight: y[r] = W[g(r)] x[row_index[r] or r].
 
     x [x_rows, K] and w [G, N, K] of one type (bfloat16 or float32), group_offsets [G + 1] int32 (None:
     one group of all rows), row_index [rows] int32 or None (then the rows are x's).  Returns y [rows, N] of
-    x's type, or of y_dtype (MOE_BF16, MOE_F32).  Rows past group_offsets[G] are not written."""
+    x's type, or of y_dtype (MOE_BF16, MOE_F32).  Rows past group_offsets[G] are not written.
+
+    Where x or w requires a gradient, y has one: moe_grouped_matmul_dx (summed over the rows that gathered a row of
+    x) and moe_grouped_matmul_dw, each once.  A y written to out has none, as have the results of the calls
+    below."""
+    import torch
+
+    if out is None and (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        return _differentiable_product(x, w, group_offsets, row_index, y_dtype, workspace)
     dt = _matmul_dtype(x, "x")
     if x.dim() != 2 or w.dim() != 3:
         raise ValueError("x must be [rows, K] and w [G, N, K]")
