@@ -574,13 +574,14 @@ def moe_quantize_rows(x, swiglu=False, codes=None, scales=None):
     return codes, scales
 
 
-def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_index=None, y_dtype=MOE_BF16,
+def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_index=None, y_dtype=None,
                   workspace=None, out=None):
     """Grouped product of 8-bit integers with scales for each row and output channel:
     y[r, n] = x_scales[i] w_scales[g, n] sum_k x_codes[i, k] w_codes[g, n, k], i = row_index[r] or r.
 
     x_codes [x_rows, K] int8, x_scales [x_rows] float32 (moe_quantize_rows), w_codes [G, N, K] int8,
-    w_scales [G, N] float32; group_offsets None: one group.  Returns y [rows, N] of y_dtype."""
+    w_scales [G, N] float32; group_offsets None: one group.  Returns y [rows, N] of y_dtype (MOE_BF16 by default, or
+    out's type)."""
     import torch
 
     if x_codes.dim() != 2 or w_codes.dim() != 3:
@@ -594,7 +595,7 @@ def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_
     _groups(group_offsets, row_index, G)
     rows = x_rows if row_index is None else row_index.shape[0]
     dev = _one_device(x_codes, x_scales, w_codes, w_scales, group_offsets, row_index, workspace, out)
-    y, ydt = _out(out, (rows, N), y_dtype if out is None else None, MOE_BF16, dev)
+    y, ydt = _out(out, (rows, N), y_dtype, MOE_BF16, dev)
     ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_I8, MOE_F32, G, rows, N, K, dev)
     _launch(dev, load_library().moe_matmul_i8, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
             x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,

@@ -306,3 +306,24 @@ def test_quantize_more_rows_than_a_grid_row(rows, cols):
     assert bool((scales == 1).all())
     for i in range(0, rows, 1 << 20):
         assert torch.equal(codes[i:i + (1 << 20)].bfloat16(), x[i:i + (1 << 20)])
+
+
+def test_output_types_that_contradict_each_other_are_refused():
+    torch = _torch()
+    x = torch.ones((4, 16), device="cuda").bfloat16()
+    w = torch.ones((1, 8, 16), device="cuda").bfloat16()
+    q, s = moe.moe_quantize_rows(x)
+    qw, sw = torch.ones((1, 8, 16), dtype=torch.int8, device="cuda"), torch.ones((1, 8), device="cuda")
+    for dtype, other in ((torch.float32, moe.MOE_BF16), (torch.bfloat16, moe.MOE_F32)):
+        y, dx = torch.zeros((4, 8), device="cuda", dtype=dtype), torch.zeros((4, 16), device="cuda", dtype=dtype)
+        dw = torch.zeros((1, 8, 16), device="cuda", dtype=dtype)
+        for bad in (lambda: moe.moe_matmul_i8(q, s, qw, sw, y_dtype=other, out=y),
+                    lambda: moe.moe_grouped_matmul(x, w, None, y_dtype=other, out=y),
+                    lambda: moe.moe_grouped_matmul_dx(w[0, :4, :8].contiguous(), w, None, dx_dtype=other, out=dx),
+                    lambda: moe.moe_grouped_matmul_dw(w[0, :4, :8].contiguous(), x, None, dw_dtype=other, out=dw)):
+            with pytest.raises(ValueError):
+                bad()
+        assert not bool(y.any()) and not bool(dx.any()) and not bool(dw.any())
+        assert moe.moe_matmul_i8(q, s, qw, sw, out=y) is y and bool((y == 16).all())
+    assert moe.moe_matmul_i8(q, s, qw, sw).dtype == torch.bfloat16
+    assert moe.moe_matmul_i8(q, s, qw, sw, y_dtype=moe.MOE_F32).dtype == torch.float32
