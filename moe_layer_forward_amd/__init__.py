@@ -538,6 +538,8 @@ def moe_grouped_matmul_dw(dy, x, group_offsets, row_index=None, dw_dtype=None, w
     dt = _matmul_dtype(dy, "dy")
     if dy.dim() != 2 or x.dim() != 2 or x.dtype != dy.dtype:
         raise ValueError("dy must be [rows, N] and x [x_rows, K] of one type")
+    if group_offsets is not None and (group_offsets.dim() != 1 or group_offsets.shape[0] < 1):
+        raise ValueError(f"group_offsets must be [G + 1], got {tuple(group_offsets.shape)}")
     G = 1 if group_offsets is None else group_offsets.shape[0] - 1
     _groups(group_offsets, row_index, G)
     (rows, N), (x_rows, K) = dy.shape, x.shape

@@ -38,3 +38,13 @@ def test_rows_of_the_quantizer(rows, status):
     """Accepted row counts get as far as the misaligned scales."""
     assert moe.load_library().moe_quantize_rows(moe.MOE_BF16, rows, 8, 0, FAKE, FAKE, ODD, None) == status
     assert ("scales" in moe.moe_last_error()) == (status == moe.MOE_ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("shape", [(), (0,), (2, 3)])
+def test_shapes_of_the_offsets(shape):
+    """The weight gradient takes its number of groups from the offsets: other shapes raise the binding's ValueError."""
+    import torch
+
+    t = torch.zeros((4, 8))
+    with pytest.raises(ValueError, match="group_offsets"):
+        moe.moe_grouped_matmul_dw(t, t, torch.zeros(shape, dtype=torch.int32))
