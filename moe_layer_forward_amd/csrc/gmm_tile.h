@@ -69,7 +69,7 @@ struct GmmLoadAlong {
   uint32_t records;
   uint32_t off[NL];    // lane's row and chunk of pieces w, w + W, ...
   uint32_t chunk;      // the lane's chunk, in bytes (the same in each of the wave's pieces)
-  uint32_t row_bytes;
+  uint32_t end;        // bytes of a row up to the end of this item's range
   int step0 = 0;       // first step of this item's range
 
   // stage row rl is matrix row row_of(rl), relative to base
@@ -79,7 +79,7 @@ struct GmmLoadAlong {
     const int lane = threadIdx.x & 63;
     base = gmm_uniform(b);
     records = (uint32_t)gmm_uniform((int)rec);
-    row_bytes = (uint32_t)ld;
+    end = (uint32_t)ld;
     chunk = (uint32_t)(((lane & 7) ^ L::swz(wave * 8 + (lane >> 3))) << 4);
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
@@ -87,12 +87,18 @@ struct GmmLoadAlong {
       off[j] = (uint32_t)(row_of(rl) * ld) + chunk;
     }
   }
+  // only the n steps from `first` on
+  __device__ __forceinline__ void range(int first, int n) {
+    step0 = first;
+    const uint32_t to = (uint32_t)(first + n) * kGmmStepBytes;
+    end = to < end ? to : end;
+  }
   __device__ __forceinline__ void prefetch(int) {}
   // the first n of them
   template <int n>
   __device__ __forceinline__ void issue(int step, char* stage, int wave) const {
     const uint32_t kb = (uint32_t)(step0 + step) * kGmmStepBytes;
-    const bool in = kb + chunk < row_bytes;
+    const bool in = kb + chunk < end;
     const GmmRsrc rs = gmm_rsrc(base, records);
 #pragma unroll
     for (int j = 0; j < n; ++j)
@@ -109,7 +115,7 @@ struct GmmLoadAcross {
   static constexpr int kRows = L::kRows, kRowsPer = 1024 / L::kRowBytes;  // rows of a step, of a piece
   const char* base;    // first contraction row (gathered: the matrix), uniform
   int64_t ld;          // bytes between rows
-  int depth;           // contraction rows
+  int depth;           // contraction rows up to the end of this item's range
   int step0 = 0;       // first step of this item's range
   uint32_t off[NL];    // lane's row of the stage and column (gathered: column only)
   const int32_t* index;
@@ -130,6 +136,12 @@ struct GmmLoadAcross {
       off[j] = (uint32_t)(col0 * T::kBytes + c * 16) + (kGather ? 0u : (uint32_t)(r * ld));
     }
     rows = next = 0;
+  }
+  // only the n steps from `first` on
+  __device__ __forceinline__ void range(int first, int n) {
+    step0 = first;
+    const int to = gmm_uniform((first + n) * kRows);
+    depth = to < depth ? to : depth;
   }
   // gathered: the 64 row numbers of a step, a lane each, read one step before its loads (issue(step - 1)
   // follows)
@@ -220,8 +232,8 @@ __device__ __forceinline__ void gmm_read_first(char* const (&p)[2], const char* 
 // meeting; a gathered Q reads its next row numbers before P0).  Counting what may still be in flight: in
 // the middle of step kt what follows P1(kt), at its end what follows P0(kt + 1).  Operations more in between
 // make a wait stricter, never laxer.  With one block (NB = 1) there is one half and one meeting.
-// Steps past the last are loaded too: they lie past the ends, read nothing and put zeros into arrays that
-// nobody multiplies, so that every step is the same code with the same waits.
+// Steps past an item's last are loaded too: they lie past the end of its range (range() of the loads), read nothing
+// and put zeros into arrays that nobody multiplies, so that every step is the same code with the same waits.
 // kMidWait, kEndWait: operations that may be in flight at the two meetings; mid(), end(): what is loaded there.
 template <class T, int W, int NB, int kMidWait, int kEndWait, class FP, class FQ, class Mid, class End>
 __device__ __forceinline__ void gmm_step(char* const (&ps)[2], const char* qs, char* const (&ps_next)[2],
@@ -517,9 +529,11 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
 #pragma unroll
     for (int s = 0; s < 4; ++s) acc[i][s] = typename T::Acc{0, 0, 0, 0};
   constexpr int kStep = kGmmStepBytes / T::kBytes;
-  int nk;
-  gmm_range((int)((depth + kStep - 1) / kStep), a.split, sp, lq.step0, nk);
-  lp[0].step0 = lp[1].step0 = lq.step0;
+  int first, nk;
+  gmm_range((int)((depth + kStep - 1) / kStep), a.split, sp, first, nk);
+  lp[0].range(first, nk);
+  lp[1].range(first, nk);
+  lq.range(first, nk);
   gmm_loop<T, W, NB>(lp, lq, nk, rings, fp, fq, wave, acc);
 
   GmmOut o;
