@@ -427,9 +427,13 @@ __global__ __launch_bounds__(256) void gmm_join_kernel(GmmArgs a) {
 
 // TN: the same for the groups of more than one range; one work-group per `share` elements of a group's matrix.
 // Where groups are more than further ranges can be, a group is found by its second range, and work-groups of
-// other ranges do nothing.  Many of those cost more than the fewer, longer joins of a larger share: 173 groups, 26129
-// rows, 86 x 2320 (7215 work-groups of 1024 elements): equal groups 92 us, 86 with 4096; 279 groups, 20499 skewed
-// rows, 448 x 110 (5194 of them): 100 us, 122 with 4096.
+// other ranges do nothing.  Very many of those cost equal groups more than longer joins cost skewed ones.  Shares of
+// 4096 elements against 1024, 60 sizes, groups equal and skewed by 1 / rank^1.1 (time of the whole call):
+//   8192 work-groups of 1024 elements or more: equal 0.89 to 1.00, skewed 0.98 to 1.04 (152 groups, 94200 rows,
+//     1152 x 184 in bf16: equal 93.5 us -> 83.9, skewed 134 -> 139)
+//   fewer: equal 0.90 to 1.01, skewed 1.00 to 2.0 (394 groups, 41681 rows, 40 x 96 in fp32: equal 18.4 us, skewed 42.0 ->
+//     85.4; 159 groups, 13065 rows, 408 x 240: equal 74.6 -> 68.5, skewed 83.9 -> 100.3)
+//   groups not searched for (no work-group idles): 1.04 to 2.8
 __global__ __launch_bounds__(256) void gmm_join_sums_kernel(GmmArgs a, int per_matrix, int share) {
   const int64_t range = a.range_rows;
   int g = (int)(blockIdx.x / (unsigned)per_matrix);
@@ -504,7 +508,7 @@ hipError_t launch_gmm_join(const GmmArgs& a, hipStream_t s) {
   if (a.form == GmmForm::kTN) {
     const int64_t further = a.max_rows / a.range_rows;
     const int64_t all = (int64_t)a.N * a.K, turns = std::min<int64_t>(a.G, further);
-    const int share = a.G > further && turns * all > 6144 * 1024 ? 4096 : 1024;
+    const int share = a.G > further && turns * all >= 8192 * 1024 ? 4096 : 1024;
     const int per_matrix = (int)((all + share - 1) / share);
     gmm_join_sums_kernel<<<dim3((unsigned)(turns * per_matrix)), block, 0, s>>>(a, per_matrix, share);
     return hipGetLastError();
