@@ -66,7 +66,6 @@ hipError_t launch_gmm_tile_i8(const GmmArgs& a, int waves, bool once, hipStream_
 hipError_t launch_gmm_tile_nn(const GmmArgs& a, int waves, bool once, hipStream_t s);
 hipError_t launch_gmm_tile_tn(const GmmArgs& a, int waves, hipStream_t s);
 int64_t gmm_tile_items(const GmmArgs& a, int waves);
-constexpr int64_t kGmmCacheBytes = 256 << 20;  // the last-level cache
 
 // codes[r] = rint(127 v / max|v|), scales[r] = max|v| / 127 of each row v (swiglu: v = SiLU(gate) * up of a
 // row gate | up of 2 cols values).

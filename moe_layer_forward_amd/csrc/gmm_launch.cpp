@@ -7,6 +7,7 @@ namespace moe {
 namespace {
 
 constexpr int64_t kCus = 256;
+constexpr int64_t kCacheBytes = 256 << 20;  // the last-level cache
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -126,7 +127,7 @@ int64_t tile_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, 32 * t
 // called again and again: 36 us with the default policy, 40 with this one).
 bool tile_once(const GmmArgs& a, int waves) {
   return a.form != GmmForm::kTN && a.max_rows <= (int64_t)a.G * 32 * waves &&
-         (int64_t)a.G * a.N * a.K * elem_bytes(a) > kGmmCacheBytes;
+         (int64_t)a.G * a.N * a.K * elem_bytes(a) > kCacheBytes;
 }
 
 size_t range_bytes(const GmmArgs& a, int64_t range) {

@@ -32,6 +32,7 @@
 // Tried and not kept for short sums: work-groups that stay and issue an item's first loads before storing the
 // last one's outputs (48 groups of 170 rows, 7168 x 2048: 530 us against 543, but 4 to 16% slower at 8 and
 // more steps, where it needs registers the loop does not have); stores straight from the registers (690 us).
+// Non-temporal stores of outputs of 256 MB and more: within 1% over 38 sizes; not kept.
 #pragma once
 #include "gmm_core.h"
 #include "tile_core.h"
@@ -346,7 +347,6 @@ struct GmmOut {
   int64_t ld;
   int rows, cols;
   bool bf16;
-  bool once;  // non-temporal stores: an output that no cache holds until its reader comes
 };
 
 // value(row block i, Q block s, element e, row, col) -> fp32
@@ -387,10 +387,7 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
         typedef gmm_u32x4 Unaligned __attribute__((aligned(2)));
         char* const to = o.out + (row * o.ld + 8 * c) * 2;
         if (8 * c + 8 <= o.cols) {
-          if (o.once)
-            __builtin_nontemporal_store(v, reinterpret_cast<Unaligned*>(to));
-          else
-            *reinterpret_cast<Unaligned*>(to) = v;
+          *reinterpret_cast<Unaligned*>(to) = v;
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -545,7 +542,6 @@ __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& 
   o.rows = rows;
   o.cols = (int)(q_len - q0 < S::kTile ? q_len - q0 : S::kTile);
   o.bf16 = e == 2;
-  o.once = a.max_rows * q_len * 2 >= kGmmCacheBytes;
   if constexpr (std::is_same_v<T, GmmI8>) {
     if (a.split > 1) {  // int32 partial sums, as they are
       gmm_store<W, NB>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return __int_as_float(acc[i][s][j]); });
@@ -650,7 +646,6 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   o.rows = (int)(a.N - p0 < S::kTile ? a.N - p0 : S::kTile);
   o.cols = (int)(a.K - q0 < S::kTile ? a.K - q0 : S::kTile);
   o.bf16 = e == 2;
-  o.once = (int64_t)a.G * a.N * a.K * 2 >= kGmmCacheBytes;
   gmm_store<W, W>(o, rings, wr, wc, [&](int i, int s, int j, int, int) { return acc[i][s][j]; });
 #else
   (void)rings;
