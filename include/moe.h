@@ -354,8 +354,8 @@ const char* moe_last_error(void);
  * launches.  moe_profile_count() and moe_profile_kernel(i) report what the last call on this
  * thread launched ("router_logits", "topk", "permute", "plan", "gateup_stream", "down_stream",
  * "gateup_tile", "down_tile", "combine", ...; a grouped product: "matmul_tile256" or
- * "matmul_tile128" by its output tiles, with "_nt" where the weights are read with the non-temporal
- * policy, "matmul_any128" or "matmul_any64" for fp32 and for rows that are not whole 16-byte pieces, and
+ * "matmul_tile128" by its output tiles, with "_nt" where weights that are read once come with the
+ * non-temporal policy, "matmul_any128" or "matmul_any64" for fp32 and for rows that are not whole 16-byte pieces, and
  * "matmul_join" after them where its sums were split). */
 int moe_profile_events(void* const* events, int32_t n_events);
 int32_t moe_profile_count(void);

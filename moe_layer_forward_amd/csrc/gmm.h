@@ -39,7 +39,7 @@ struct GmmPlan {
   GmmArgs args;      // with split, range_rows and part
   bool tile;         // the tile kernel, with work-groups of `waves`; or the plain one, with tiles of `edge`
   int waves, edge;
-  bool once;         // tile: weights read with the non-temporal policy
+  bool once;         // tile: weights that are read once come with the non-temporal policy
   bool join;         // launch_gmm_join follows
   const char* name;  // of the kernel
 };

@@ -238,8 +238,8 @@ struct GmmTiles {
     partial = __builtin_amdgcn_readlane(partial_to, 63);
   }
 
-  // Tile t (below full + partial): its group and rows.
-  __device__ __forceinline__ void find(const int32_t* off, int G, int64_t max_rows, int bm, int t, int& g,
+  // Tile t (below full + partial): its group and rows.  Returns the rows of the group.
+  __device__ __forceinline__ int find(const int32_t* off, int G, int64_t max_rows, int bm, int t, int& g,
                                        int64_t& beg, int64_t& end) const {
     const bool is_full = t < full;
     int rel = is_full ? t : t - full;
@@ -261,6 +261,7 @@ struct GmmTiles {
     end = is_full ? beg + bm : e;
     beg = __builtin_amdgcn_readfirstlane((int)beg);  // rows fit 31 bits
     end = __builtin_amdgcn_readfirstlane((int)end);
+    return __builtin_amdgcn_readfirstlane((int)rows);
   }
 };
 

@@ -121,11 +121,18 @@ int tile_waves(const GmmArgs& a) {
 int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a, tile_waves(a)), steps_of(a), kCus, 8); }
 int64_t tile_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, 32 * tile_waves(a)), kCus, 8); }
 
-// The weights are read with the non-temporal policy where nothing reads them twice: groups of about one row tile,
-// whose weights together exceed the 256 MB of last-level cache that a next call could find them in
-// (gm decode, 384 groups of 1.3 rows: 1.44 -> 1.32 ms; int8, 48 groups: 141 -> 127 us; a 132 MB int8 weight
-// called again and again: 36 us with the default policy, 40 with this one).
+// Whether the kernel reads the weights of groups of one row tile, which nothing reads again, with the non-temporal
+// policy: where tiles have room for the average group, where the weights exceed the 256 MB of last-level cache that
+// a next call could find them in, and where their rows are whole 128-byte lines (a line that two steps or tiles share
+// would be fetched twice).  Against the default policy, 18 to 20 sizes each, groups even, skewed by 1 / rank^1.1, and
+// all rows in one:
+//   as here: 0.88 to 0.96, 0.87 to 1.02, 1.00 to 1.01 (384 groups of 1.3 rows, 7168 x 2048: 1455 us -> 1306), but for
+//     weights just past the cache (300 MB, 32 rows of 32 groups: 27.9 us -> 29.9)
+//   rows of other lengths: 0.96 to 1.24 (61 groups, 3294 rows, 4560 x 2720 in int8: 200 us -> 248)
+//   groups of several row tiles as well: skewed 0.91 to 1.12, all rows in one up to 1.49 (55 us -> 82)
+//   132 MB of int8 weights, called again and again: 36 us -> 40
 bool tile_once(const GmmArgs& a, int waves) {
+  if ((int64_t)a.K * elem_bytes(a) % 128 || reinterpret_cast<uintptr_t>(a.w) % 128) return false;
   return a.form != GmmForm::kTN && a.max_rows <= (int64_t)a.G * 32 * waves &&
          (int64_t)a.G * a.N * a.K * elem_bytes(a) > kCacheBytes;
 }

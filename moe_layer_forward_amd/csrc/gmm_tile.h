@@ -479,7 +479,8 @@ inline int64_t gmm_weight_grid(int64_t items) {
       p11_[GmmShape<W>::kPStage], q0_[GmmShape<W>::kQStage], q1_[GmmShape<W>::kQStage], q2_[GmmShape<W>::kQStage];  \
   const GmmRings rings{{{p00_, p01_}, {p10_, p11_}}, {q0_, q1_, q2_}};
 
-// NT and NN: output rows are rows of a group.
+// NT and NN: output rows are rows of a group.  kOnce: weights that one row tile reads come with the non-temporal
+// policy.
 template <GmmForm F, class T, int W, bool kOnce, int NB>
 __device__ __forceinline__ void gmm_rows_body(const GmmArgs& a, const GmmRings& rings, int g, int64_t beg, int64_t end,
                                               int64_t q0, int sp) {
@@ -583,13 +584,18 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   GmmTiles tiles;
   tiles.count(a.group_offsets, a.G, a.max_rows, S::kTile);
   if (!gmm_row_item(gmm_block() / (unsigned)a.split, tiles, slabs, t, slab)) return;
-  tiles.find(a.group_offsets, a.G, a.max_rows, S::kTile, t, g, beg, end);
+  // the only row tile of its group: nothing else reads the group's weights
+  [[maybe_unused]] const bool alone = tiles.find(a.group_offsets, a.G, a.max_rows, S::kTile, t, g, beg, end) <= S::kTile;
 #if defined(__HIP_DEVICE_COMPILE__)
   const int64_t q0 = (int64_t)slab * S::kTile;
   const int nb = (int)(end - beg + 31) / 32;  // P blocks per wave
-#define MOE_GMM_CASE(N) \
-  if constexpr (N <= W) \
-    if (nb == N) return gmm_rows_body<F, T, W, kOnce, N>(a, rings, g, beg, end, q0, sp);
+#define MOE_GMM_CASE(N)                                                                                      \
+  if constexpr (N <= W)                                                                                      \
+    if (nb == N) {                                                                                           \
+      if constexpr (kOnce)                                                                                   \
+        if (alone) return gmm_rows_body<F, T, W, true, N>(a, rings, g, beg, end, q0, sp);                    \
+      return gmm_rows_body<F, T, W, false, N>(a, rings, g, beg, end, q0, sp);                                \
+    }
   MOE_GMM_CASE(8)
   MOE_GMM_CASE(7)
   MOE_GMM_CASE(6)

@@ -157,10 +157,30 @@ def test_rows_in_256_tiles(op, steps):
 @pytest.mark.parametrize("op", ["forward", "dx", "i8"])
 @pytest.mark.parametrize("rows,kernel", [("many", "matmul_tile256_nt"), ("few", "matmul_tile128_nt")])
 def test_streamed_weights(op, out_name, rows, kernel):
-    """More than 256 MB of weights, read once: groups of about a tile of rows (one has several tiles) and of few."""
+    """More than 256 MB of weights in whole lines: groups of one tile of rows, read once, beside one of several."""
     sizes = [60, 0, 250, 700, 33, 1] + [20] * 18 if rows == "many" else [8, 0, 1, 60, 131] + [0] * 19
-    K = 5616 if op == "i8" else 2808
+    K = 5632 if op == "i8" else 2816
     _check_rows(op, kernel, sizes, 2024, K, op != "dx" and out_name == "f32", out_name, 50)
+
+
+@pytest.mark.parametrize("K,start,kernel", [(2816, 0, "matmul_tile128_nt"), (2808, 0, "matmul_tile128"),
+                                            (2816, 8, "matmul_tile128"), (2816, 64, "matmul_tile128_nt")])
+def test_weights_are_streamed_in_whole_lines(K, start, kernel):
+    """Rows that are not whole 128-byte lines, or that start inside one, share lines: those keep the default policy
+    (streamed, they took up to a quarter longer)."""
+    torch = _torch()
+    sizes, N = [8, 0, 1, 60] + [0] * 20, 2024
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(53)
+    off, d_off = _offsets(sizes)
+    x, w = _ints(gen, int(off[-1]), K).bfloat16(), _ints(gen, len(sizes), N, K)
+    big = torch.zeros(w.numel() + start, dtype=torch.bfloat16, device="cuda")
+    big[start:] = w.view(-1)
+    y, names = _launched(lambda: moe.moe_grouped_matmul(x, big[start:].view(w.shape), d_off))
+    assert [k for k, _ in names] == [kernel]
+    for g in range(len(sizes)):
+        r = slice(int(off[g]), int(off[g + 1]))
+        assert torch.equal(y[r], _exact(x[r], w[g].T, torch.bfloat16))
 
 
 def _check_weights(sizes, N, K, gather, out_name, names, seed):
@@ -280,7 +300,7 @@ def test_gradients_against_differences_along_their_signs(size):
 
 # --------------------------------------------------------------------------- very many output tiles
 @pytest.mark.parametrize("op,depth,kernel", [
-    ("forward", 8, "matmul_tile128_nt"), ("dx", 8, "matmul_tile128_nt"), ("i8", 16, "matmul_tile128_nt"),
+    ("forward", 8, "matmul_tile128"), ("dx", 8, "matmul_tile128_nt"), ("i8", 16, "matmul_tile128"),
     ("forward", 1, "matmul_any128"), ("dx", 1, "matmul_any128"), ("i8", 1, "matmul_any128")])
 def test_rows_of_four_million_tiles(op, depth, kernel):
     """513 groups of 8192 tiles each: more work-groups than one row of the grid holds."""
