@@ -41,19 +41,21 @@ int split_of(int64_t items, int64_t steps, int64_t slots, int64_t min_steps) {
 // TN: rows of the ranges that a group's sum is cut into, 0: none cut.  One group's matrix is `tiles` output tiles;
 // `slots` work-groups run.  Group sizes are known on the device alone, so the rule goes by their number and all rows, and
 // a group that fits one range is written as if nothing was cut.  Ranges keep min_steps steps.
-//   * Groups that leave slots idle: as many ranges as fill them (with 1/32 to spare, so that nearly equal
-//     groups have equally many).  10 groups, 12688 skewed rows, 1088 x 120 in bf16: 19 us, 29 with as many ranges to
-//     every group.
+//   * Groups that leave slots idle: as many ranges as fill them, with 1/32 to spare, so that nearly equal groups have
+//     equally many (without: 0.96 to 1.23 of the time, 1.01 over 24 sizes), and as many on every XCD where that leaves
+//     out at most a quarter of them (rounded down always: up to 1.9, 3 groups, 48782 rows, 264 x 602 in bf16: 171 us
+//     against 90; never: up to 1.17, 55 groups, 57305 rows, 108 x 28 in fp32: 50 against 42; 120 sizes).
+//     10 groups, 12688 skewed rows, 1088 x 120 in bf16: 19 us, 29 with as many ranges to every group.
 //   * Groups that fill the slots: ranges of twice the average group, for the one that holds more than others, where a
 //     quarter of all rows in one sum would take half again as long as the rest and 8 steps more (an item's start
-//     and end counted as 6 steps).  fp32, skewed rows, not cut -> cut: 279 groups, 20499 rows, 448 x 110: 590 ->
-//     100 us; 194 groups, 5082 rows, 384 x 64: 103 -> 45.  The join's launch costs equal groups 3 to 4 us (218
-//     groups, 13206 rows, 128 x 256: 10 -> 13.6).  Without the condition: 130 groups, 8237 skewed rows, 1280 x 576:
-//     70 -> 80.
+//     and end counted as 6 steps).  30 sizes, uncut -> cut: skewed by 1 / rank^1.1 all gain, 1.06 to 7.6 times (105
+//     groups, 56522 rows, 118 x 134 in fp32: 935 -> 124 us); equal ones pay 2 to 5 us, the join's launch and its
+//     search (285 groups, 17372 rows, 32 x 56 in bf16: 5.3 -> 8.4).  Without the condition: 130 groups, 8237 skewed
+//     rows, 1280 x 576: 70 -> 80.
 int64_t range_of(const GmmArgs& a, int64_t tiles, int64_t slots, int64_t min_steps) {
   const int64_t step = 128 / elem_bytes(a), steps = (a.max_rows + step - 1) / step, mean = (a.max_rows + a.G - 1) / a.G;
   int64_t each = std::min(slots / (tiles * a.G), mean / (min_steps * step));
-  if (const int64_t e8 = each * a.G / 8 * 8 / a.G; e8 >= 2) each = e8;  // the same number on each XCD
+  if (const int64_t e8 = each * a.G / 8 * 8 / a.G; e8 >= 2 && e8 * 4 >= each * 3) each = e8;  // the same on each XCD
   int64_t rows;
   if (each >= 2) {
     rows = (mean + each - 1) / each;

@@ -48,3 +48,14 @@ def test_shapes_of_the_offsets(shape):
     t = torch.zeros((4, 8))
     with pytest.raises(ValueError, match="group_offsets"):
         moe.moe_grouped_matmul_dw(t, t, torch.zeros(shape, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("dtype,G,rows,N,K", [
+    (moe.MOE_BF16, 3, 48782, 264, 602), (moe.MOE_F32, 1, 5469, 152, 552), (moe.MOE_F32, 14, 222560, 28, 1087)])
+def test_ranges_of_the_weight_gradient_fill_the_chip(dtype, G, rows, N, K, tile=64, slots=768):
+    """Where groups leave work-groups idle, their ranges (two partial sums of N x K each in the workspace) take two
+    thirds of them or more, of three 64 x 64 tiles to a CU."""
+    n = moe.moe_matmul_workspace_size(DW, dtype, G, rows, N, K)
+    ranges = n // (2 * N * K * 4)
+    tiles = -(-N // tile) * -(-K // tile)
+    assert 2 / 3 * slots <= ranges * tiles <= slots * 1.05
