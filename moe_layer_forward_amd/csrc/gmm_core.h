@@ -84,10 +84,6 @@ struct GmmAlong {
     const int l = threadIdx.x & 63, x = l & 15, g = l >> 4;
     return Lane{{pos(x, g), pos(x, 4 + g)}};
   }
-  // Fragment of the 16-row block b for contraction half kk of the step.
-  __device__ static __forceinline__ gmm_u32x4 frag(const char* st, const Lane& ln, int b, int kk) {
-    return *reinterpret_cast<const gmm_u32x4*>(st + b * 16 * kGmmStepBytes + ln.off[kk]);
-  }
 };
 
 // LDS stage of an operand whose rows run across the contraction: one row per contraction index (64 bf16
@@ -130,9 +126,6 @@ struct GmmAcross {
     } else {
       return Lane{4 * g * kRowBytes + i * 4, swz(4 * g)};
     }
-  }
-  __device__ static __forceinline__ gmm_u32x4 frag(const char* st, const Lane& ln, int b, int kk) {
-    return read_at(st + ln.row + ((b ^ ln.s) * kUnit) + kk * (kRows / 2) * kRowBytes);
   }
   // the fragment whose first row (of this lane) is at p
   __device__ static __forceinline__ gmm_u32x4 read_at(const char* p) {

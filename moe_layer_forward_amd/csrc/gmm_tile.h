@@ -43,17 +43,14 @@ namespace {
 // A work-group of W waves, 2 x W / 2 of them (W = 8 or 4), and its tile of 32 W x 32 W outputs.
 template <int W>
 struct GmmShape {
-  static constexpr int kWaves = W, kThreads = 64 * W, kTile = 32 * W, kHalf = kTile / 2;  // kHalf: P rows per half
+  static constexpr int kThreads = 64 * W, kTile = 32 * W, kHalf = kTile / 2;  // kHalf: P rows per half
   static constexpr int kPStage = kHalf * kGmmStepBytes, kQStage = kTile * kGmmStepBytes;
-  static constexpr int kMaxNB = W;  // 16-row P blocks per wave
 };
 constexpr int kGmmPLoads = 2;       // 1 KiB loads per wave of a half of P
 constexpr int kGmmQLoads = 4;       // ... and of a step of Q
 constexpr int kGmmNonTemporal = 2;  // the loads' cache policy operand: nt
 constexpr uint32_t kGmmOutside = 0xfffffff0u;  // an offset past every record count
 constexpr int kGmmSuper = 4;        // row tiles that run side by side on one XCD
-
-#define MOE_GMM_INLINE __attribute__((always_inline))
 
 typedef __amdgpu_buffer_rsrc_t GmmRsrc;
 typedef __attribute__((address_space(3))) void* GmmLds;

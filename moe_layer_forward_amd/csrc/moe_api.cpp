@@ -535,7 +535,7 @@ int forward_quant(const char* name, const moe_config* cfg, int64_t T, const void
 constexpr int32_t kMaxMatmulSide = 1 << 20;
 constexpr int32_t kMaxI8Depth = 131071;  // 128 * 128 * K < 2^31
 
-// Checks that the product calls share.  need_x / need_w: the operands the form reads.
+// Checks that the product calls share: sizes, types and limits (pointers are the entries' own).
 int check_matmul(const char* fn, const moe::GmmArgs& a, int32_t out_dtype) {
   using moe::GmmForm;
   using moe::GmmType;
