@@ -118,7 +118,7 @@ int tile_waves(const GmmArgs& a) {
   const int64_t items = gmm_tile_items(a, 8);
   return items >= 512 || (items >= 160 && steps_of(a) >= 12) ? 8 : 4;
 }
-// One work-group to a CU, ranges of 8 steps (64 rows, 7168 x 7168: 39 us in one range, 25.5 in four, 30 in
+// One work-group to a CU, ranges of 8 steps (64 rows, 7168 x 7168: 37 us in one range, 24 in four, 27 in
 // eight; int8, 64 rows, 18432 x 7168, 144 tiles: 24.6 us in one range, 35.5 in two).
 int tile_split(const GmmArgs& a) { return split_of(gmm_tile_items(a, tile_waves(a)), steps_of(a), kCus, 8); }
 int64_t tile_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, 32 * tile_waves(a)), kCus, 8); }
