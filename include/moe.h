@@ -335,7 +335,8 @@ int moe_quantize_rows(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swigl
 
 /* The grouped product of 8-bit integers with scales for each row and each output channel:
  *     y[r, n] = x_scales[i] * w_scales[g(r), n] * sum_k x_codes[i, k] * w_codes[g(r), n, k],
- *     i = row_index ? row_index[r] : r, the sum exact in int32 (K <= 131071)
+ *     i = row_index ? row_index[r] : r, the sum exact in int32 (K <= 131071), then times x_scales and times
+ *     w_scales in fp32 (y overflows or underflows where the first of these products does)
  *   x_codes [x_rows, K] int8, x_scales [x_rows] fp32, w_codes [n_groups, N, K] int8,
  *   w_scales [n_groups, N] fp32, y [max_rows, N] of y_dtype out */
 int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets, int64_t max_rows,
