@@ -128,7 +128,7 @@ int64_t tile_range(const GmmArgs& a) { return range_of(a, matrix_tiles(a, 32 * t
 // a next call could find them in, and where their rows are whole 128-byte lines (a line that two steps or tiles share
 // would be fetched twice).  Against the default policy, 18 to 20 sizes each, groups even, skewed by 1 / rank^1.1, and
 // all rows in one:
-//   as here: 0.88 to 0.96, 0.87 to 1.02, 1.00 to 1.01 (384 groups of 1.3 rows, 7168 x 2048: 1455 us -> 1306), but for
+//   as here: 0.88 to 0.97, 0.87 to 1.02, 1.00 to 1.01 (384 groups of 1.3 rows, 7168 x 2048: 1455 us -> 1306), but for
 //     weights just past the cache (300 MB, 32 rows of 32 groups: 27.9 us -> 29.9)
 //   rows of other lengths: 0.96 to 1.24 (61 groups, 3294 rows, 4560 x 2720 in int8: 200 us -> 248)
 //   groups of several row tiles as well: skewed 0.91 to 1.12, all rows in one up to 1.49 (55 us -> 82)
