@@ -298,7 +298,8 @@ typedef enum {
   MOE_MATMUL_FORWARD = 0, /* moe_grouped_matmul    */
   MOE_MATMUL_DX = 1,      /* moe_grouped_matmul_dx */
   MOE_MATMUL_DW = 2,      /* moe_grouped_matmul_dw */
-  MOE_MATMUL_I8 = 3       /* moe_matmul_i8 (dtype ignored) */
+  MOE_MATMUL_I8 = 3,      /* moe_matmul_i8 (dtype ignored) */
+  MOE_MATMUL_MX4 = 4      /* moe_matmul_mx4 (dtype ignored) */
 } moe_matmul_op;
 size_t moe_matmul_workspace_size(int32_t op, int32_t dtype, int32_t n_groups, int64_t max_rows, int32_t N,
                                  int32_t K);
@@ -343,6 +344,73 @@ int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_o
                   const int8_t* x_codes, const float* x_scales, int64_t x_rows, const int32_t* row_index,
                   const int8_t* w_codes, const float* w_scales, void* y, int32_t y_dtype, void* workspace,
                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (the OCP MX format with E2M1 elements), which gfx950 multiplies natively: rows and
+ * weights of a grouped product in 4.25 bits a value.  The pages name no such format, so it is stated here.
+ * A row of K values, K a multiple of 32:
+ *   codes   K / 2 bytes: value k in bits 4 (k % 2) .. + 3 of byte k / 2; bit 3 the sign, bits 2..0 the magnitude
+ *           {0, 1/2, 1, 3/2, 2, 3, 4, 6}
+ *   scales  S = 16 ceil(K / 512) bytes: byte b is the power s of block b, values 32 b .. 32 b + 31:
+ *           value = magnitude * 2^(s - 127); s = 255: NaN.  Bytes from K / 32 on are padding (moe_quantize_mx4 writes 0;
+ *           the product reads no value from them).
+ * Codes and scales start on 16 bytes.
+ *
+ * Rows to this format: a = max |v| over a block, s = max(floor(log2 a) - 2, -127) + 127 (a = 0: 0), each code the
+ * nearest to v 2^(127 - s), ties to the even code, beyond 6 to 6.  A block with an infinity or NaN: s = 255, codes 0.
+ * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up, and v = SiLU(gate) * up in fp32.
+ *   x of x_dtype (MOE_BF16 or MOE_F32; any alignment); codes [rows, cols / 2], scales [rows, S] out
+ * cols a multiple of 32, at most 2^20, rows <= 2^31-1.  No workspace. */
+int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, uint8_t* codes,
+                     uint8_t* scales, void* stream);
+
+/* The values that codes stand for: y [rows, cols] of y_dtype out (exact but where bf16 or fp32 overflows or rounds a
+ * subnormal; a block of scale 255: NaN).  Sizes as above; y of any alignment.  No workspace. */
+int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* codes, const uint8_t* scales, void* y, int32_t y_dtype,
+                       void* stream);
+
+/* The grouped product: y[r, n] = sum_k x[i, k] * W[g(r), n, k], i = row_index ? row_index[r] : r, both in this format,
+ * with groups, gathers, sizes and limits as in moe_grouped_matmul above (K a multiple of 32).  Sums in fp32, each
+ * output rounded once; results are the same from call to call.  A NaN block makes its row's (its column's) outputs NaN.
+ *   x_codes [x_rows, K / 2], x_scales [x_rows, S], w_codes [n_groups, N, K / 2], w_scales [n_groups, N, S],
+ *   y [max_rows, N] of y_dtype out
+ * Workspace: moe_matmul_workspace_size(MOE_MATMUL_MX4, ...). */
+int moe_matmul_mx4(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets, int64_t max_rows,
+                   const uint8_t* x_codes, const uint8_t* x_scales, int64_t x_rows, const int32_t* row_index,
+                   const uint8_t* w_codes, const uint8_t* w_scales, void* y, int32_t y_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * The root-mean-square norm that stands before the layer, with the residual's addition:
+ *     h = x + residual, rounded to dtype (residual NULL: h = x and the argument h must be NULL)
+ *     y = h * w / sqrt(mean(h^2) + eps)
+ * Each row by itself, in fp32, y rounded once; mean(h^2) overflows (y = 0) where a row's squares do.
+ *   dtype     MOE_BF16 or MOE_F32: x, residual and h, [rows, cols]
+ *   weight    [cols] of w_dtype (MOE_BF16 or MOE_F32), or NULL: ones
+ *   eps       finite, >= 0
+ *   h         may be x or residual; y may be x, if it has its type
+ *   y         [rows, cols] of y_dtype out
+ * 1 <= cols <= 32768, rows <= 2^31-1.  Matrices need only start on a boundary of their element size.  No workspace. */
+int moe_rms_norm(int32_t dtype, int64_t rows, int32_t cols, const void* x, const void* residual, const void* weight,
+                 int32_t w_dtype, float eps, void* h, void* y, int32_t y_dtype, void* stream);
+
+/* The same with y, as fp32 holds it, in 8-bit integers: codes and scales as moe_quantize_rows makes them, for
+ * moe_matmul_i8.   codes [rows, cols] int8 out; scales [rows] fp32 out */
+int moe_rms_norm_i8(int32_t dtype, int64_t rows, int32_t cols, const void* x, const void* residual, const void* weight,
+                    int32_t w_dtype, float eps, void* h, int8_t* codes, float* scales, void* stream);
+
+/* Its gradients.  With m = 1 / sqrt(mean(h^2) + eps) and g = dy * w:
+ *     dx = m (g - h m^2 mean(g h)) + dh     the gradient for x and for residual alike
+ *     dw = sum over rows of dy h m          (zeros without rows; in a fixed order, no atomics)
+ *   dy, h      [rows, cols] dtype: the gradient of y, and the forward's h (x where it had no residual)
+ *   dh         [rows, cols] dtype: what reaches h past the norm, or NULL
+ *   dx         [rows, cols] dtype out; may be dy or dh
+ *   dw         [cols] of dw_dtype out, or NULL
+ * Sizes, types and alignment as moe_rms_norm.  Workspace (for dw): moe_rms_norm_workspace_size(rows, cols). */
+size_t moe_rms_norm_workspace_size(int64_t rows, int32_t cols);
+int moe_rms_norm_grad(int32_t dtype, int64_t rows, int32_t cols, const void* dy, const void* h, const void* weight,
+                      int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Message of the last failed call on this thread ("" if none); valid until the next call. */
 const char* moe_last_error(void);

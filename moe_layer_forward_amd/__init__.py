@@ -23,12 +23,13 @@ MOE_F32, MOE_BF16 = 0, 1
 (MOE_OP_ROUTE, MOE_OP_PERMUTE, MOE_OP_GROUPED_SWIGLU, MOE_OP_COMBINE, MOE_OP_FORWARD,
  MOE_OP_FORWARD_ROUTED, MOE_OP_FORWARD_Q4, MOE_OP_FORWARD_FP8) = range(8)
 
-MOE_MATMUL_FORWARD, MOE_MATMUL_DX, MOE_MATMUL_DW, MOE_MATMUL_I8 = range(4)
+MOE_MATMUL_FORWARD, MOE_MATMUL_DX, MOE_MATMUL_DW, MOE_MATMUL_I8, MOE_MATMUL_MX4 = range(5)
 
 EXPORTED = ("moe_workspace_size", "moe_route", "moe_permute", "moe_grouped_swiglu", "moe_combine", "moe_forward",
             "moe_forward_noalloc", "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8",
             "moe_matmul_workspace_size", "moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
-            "moe_quantize_rows", "moe_matmul_i8", "moe_last_error", "moe_profile_events",
+            "moe_quantize_rows", "moe_matmul_i8", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_matmul_mx4",
+            "moe_rms_norm", "moe_rms_norm_i8", "moe_rms_norm_workspace_size", "moe_rms_norm_grad", "moe_last_error", "moe_profile_events",
             "moe_profile_count", "moe_profile_kernel")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20  # the fixed scratch of moe_forward_noalloc (include/moe.h)
 
@@ -91,8 +92,18 @@ def load_library():
         lib.moe_grouped_matmul_dw.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, i32, vp, sz, vp]
         lib.moe_quantize_rows.argtypes = [i32, i64, i32, i32, vp, vp, vp, vp]
         lib.moe_matmul_i8.argtypes = [i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, i32, vp, sz, vp]
+        lib.moe_quantize_mx4.argtypes = [i32, i64, i32, i32, vp, vp, vp, vp]
+        lib.moe_dequantize_mx4.argtypes = [i64, i32, vp, vp, vp, i32, vp]
+        lib.moe_matmul_mx4.argtypes = [i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, i32, vp, sz, vp]
+        f32 = ctypes.c_float
+        lib.moe_rms_norm.argtypes = [i32, i64, i32, vp, vp, vp, i32, f32, vp, vp, i32, vp]
+        lib.moe_rms_norm_i8.argtypes = [i32, i64, i32, vp, vp, vp, i32, f32, vp, vp, vp, vp]
+        lib.moe_rms_norm_workspace_size.argtypes = [i64, i32]
+        lib.moe_rms_norm_workspace_size.restype = sz
+        lib.moe_rms_norm_grad.argtypes = [i32, i64, i32, vp, vp, vp, i32, f32, vp, vp, vp, i32, vp, sz, vp]
         for name in ("moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw", "moe_quantize_rows",
-                     "moe_matmul_i8"):
+                     "moe_matmul_i8", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_matmul_mx4", "moe_rms_norm",
+                     "moe_rms_norm_i8", "moe_rms_norm_grad"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("moe_route", "moe_permute", "moe_grouped_swiglu", "moe_combine", "moe_forward",
                      "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8"):
@@ -603,6 +614,237 @@ def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_
             x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
             nb)
     return y
+
+
+# --------------------------------------------------------------------------- microscaled 4 bits
+def mx4_scale_cols(K: int) -> int:
+    """Bytes of scales a row of K values has: one for every 32 of them, padded to whole 16 bytes."""
+    return (K + 511) // 512 * 16
+
+
+def _mx4_matrix(codes, scales, what):
+    """K of codes [.., K / 2] and their scales [.., mx4_scale_cols(K)], both uint8."""
+    import torch
+
+    if codes.dim() < 2 or codes.dtype != torch.uint8 or codes.shape[-1] % 16:
+        raise ValueError(f"{what}_codes must be uint8 [.., K / 2] with K a multiple of 32, got {tuple(codes.shape)} "
+                         f"{codes.dtype}")
+    K = codes.shape[-1] * 2
+    _want(scales, f"{what}_scales", (*codes.shape[:-1], mx4_scale_cols(K)), torch.uint8)
+    return K
+
+
+def moe_quantize_mx4(x, swiglu=False, codes=None, scales=None):
+    """Rows in microscaled 4-bit floating point: returns (codes uint8 [rows, cols / 2], scales uint8
+    [rows, mx4_scale_cols(cols)]), layouts and rounding as in include/moe.h; cols must be a multiple of 32.
+    swiglu: x is [rows, 2 cols], gate | up, and SiLU(gate) * up is quantized.  Weights [G, N, K] quantize as
+    [G * N, K]."""
+    import torch
+
+    dt = _matmul_dtype(x, "x")
+    if x.dim() != 2 or (swiglu and x.shape[1] % 2):
+        raise ValueError("x must be [rows, cols] (swiglu: [rows, 2 cols])")
+    rows, cols = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
+    if cols % 32:
+        raise ValueError(f"cols ({cols}) must be a multiple of 32")
+    dev = _one_device(x, codes, scales)
+    if codes is None:
+        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+    else:
+        _want(codes, "codes", (rows, cols // 2), torch.uint8)
+    if scales is None:
+        scales = torch.empty((rows, mx4_scale_cols(cols)), dtype=torch.uint8, device=dev)
+    else:
+        _want(scales, "scales", (rows, mx4_scale_cols(cols)), torch.uint8)
+    _launch(dev, load_library().moe_quantize_mx4, dt, rows, cols, 1 if swiglu else 0, x.data_ptr(), codes.data_ptr(),
+            scales.data_ptr())
+    return codes, scales
+
+
+def moe_dequantize_mx4(codes, scales, y_dtype=None, out=None):
+    """The values that codes [rows, K / 2] and scales stand for: y [rows, K] of y_dtype (MOE_BF16 by default, or out's
+    type)."""
+    if codes.dim() != 2:
+        raise ValueError("codes must be [rows, K / 2]")
+    rows, K = codes.shape[0], _mx4_matrix(codes, scales, "x")
+    dev = _one_device(codes, scales, out)
+    y, ydt = _out(out, (rows, K), y_dtype, MOE_BF16, dev)
+    _launch(dev, load_library().moe_dequantize_mx4, rows, K, codes.data_ptr(), scales.data_ptr(), y.data_ptr(), ydt)
+    return y
+
+
+def moe_matmul_mx4(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_index=None, y_dtype=None,
+                   workspace=None, out=None):
+    """Grouped product of microscaled 4-bit rows and weights: y[r] = W[g(r)] x[row_index[r] or r].
+
+    x_codes [x_rows, K / 2], x_scales [x_rows, mx4_scale_cols(K)] (moe_quantize_mx4), w_codes [G, N, K / 2], w_scales
+    [G, N, mx4_scale_cols(K)], all uint8; group_offsets [G + 1] int32 (None: one group), row_index [rows] int32 or
+    None.  Returns y [rows, N] of y_dtype (MOE_BF16 by default, or out's type); rows past group_offsets[G] are not
+    written."""
+    if x_codes.dim() != 2 or w_codes.dim() != 3:
+        raise ValueError("x_codes must be [rows, K / 2] and w_codes [G, N, K / 2]")
+    K = _mx4_matrix(x_codes, x_scales, "x")
+    if _mx4_matrix(w_codes, w_scales, "w") != K:
+        raise ValueError(f"x has rows of {K} values, w of {w_codes.shape[2] * 2}")
+    G, N, x_rows = w_codes.shape[0], w_codes.shape[1], x_codes.shape[0]
+    _groups(group_offsets, row_index, G)
+    rows = x_rows if row_index is None else row_index.shape[0]
+    dev = _one_device(x_codes, x_scales, w_codes, w_scales, group_offsets, row_index, workspace, out)
+    y, ydt = _out(out, (rows, N), y_dtype, MOE_BF16, dev)
+    ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_MX4, MOE_F32, G, rows, N, K, dev)
+    _launch(dev, load_library().moe_matmul_mx4, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
+            x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
+            nb)
+    return y
+
+
+# --------------------------------------------------------------------------- the norm before the layer
+def _norm_args(x, weight, residual, what="x"):
+    """(moe dtype of x, of the weight) of a norm's operands."""
+    dt = _matmul_dtype(x, what)
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be [rows, cols]")
+    wdt = dt
+    if weight is not None:
+        wdt = _matmul_dtype(weight, "weight")
+        _want(weight, "weight", (x.shape[1],))
+    if residual is not None:
+        _want(residual, "residual", x.shape, x.dtype)
+    return dt, wdt
+
+
+def _norm_h(x, residual, h_out):
+    """Where x + residual goes (None without a residual)."""
+    import torch
+
+    if residual is None:
+        if h_out is not None:
+            raise ValueError("h_out is for x + residual: there is no residual")
+        return None
+    if h_out is None:
+        return torch.empty_like(x)
+    _want(h_out, "h_out", x.shape, x.dtype)
+    return h_out
+
+
+_norm_node = None
+
+
+def _differentiable_norm(*args):
+    """moe_rms_norm as a node of torch's graph (its class is made at the first call: torch is imported late)."""
+    global _norm_node
+    if _norm_node is None:
+        import torch
+        from torch.autograd.function import once_differentiable
+
+        class RmsNorm(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, weight, residual, eps, y_dtype):
+                ctx.set_materialize_grads(False)
+                ctx.eps = eps
+                y = moe_rms_norm(x, weight, residual, eps, y_dtype)
+                y, h = (y, x) if residual is None else y
+                ctx.save_for_backward(h, weight)
+                return y if residual is None else (y, h)
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, dy, dh=None):
+                h, weight = ctx.saved_tensors
+                for_x, for_w, for_r = ctx.needs_input_grad[:3]
+                if dy is None:  # only h was used further
+                    return dh if for_x else None, None, dh if for_r else None, None, None
+                dy = dy.to(h.dtype).contiguous()  # a float32 y of bfloat16 rows: dy in their type, as torch's casts do
+                dx, dw = moe_rms_norm_grad(dy, h, weight, None if dh is None else dh.contiguous(), ctx.eps,
+                                           need_dw=for_w)
+                return dx if for_x else None, dw, dx if for_r else None, None, None
+
+        _norm_node = RmsNorm
+    return _norm_node.apply(*args)
+
+
+def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None, h_out=None):
+    """Root-mean-square norm of the rows of h = x + residual: y = h * weight / sqrt(mean(h^2) + eps).
+
+    x [rows, cols] and residual (or None: h = x) of one type (bfloat16 or float32), weight [cols] bfloat16 or float32
+    (None: ones).  Returns y of x's type, or of y_dtype (MOE_BF16, MOE_F32), and with a residual (y, h), h in x's type.
+    h_out may be x or residual, out may be x.
+
+    Where an input requires a gradient, y and h have one (moe_rms_norm_grad); what is written to out or h_out has none,
+    as have the results of the calls below."""
+    import torch
+
+    if out is None and h_out is None and torch.is_grad_enabled() and (
+            x.requires_grad or (weight is not None and weight.requires_grad)
+            or (residual is not None and residual.requires_grad)):
+        return _differentiable_norm(x, weight, residual, eps, y_dtype)
+    dt, wdt = _norm_args(x, weight, residual)
+    rows, cols = x.shape
+    dev = _one_device(x, weight, residual, out, h_out)
+    h = _norm_h(x, residual, h_out)
+    y, ydt = _out(out, (rows, cols), y_dtype, dt, dev)
+    _launch(dev, load_library().moe_rms_norm, dt, rows, cols, x.data_ptr(), _addr(residual), _addr(weight), wdt, eps,
+            _addr(h), y.data_ptr(), ydt)
+    return y if h is None else (y, h)
+
+
+def moe_rms_norm_i8(x, weight=None, residual=None, eps=1e-6, codes=None, scales=None, h_out=None):
+    """moe_rms_norm with y in 8-bit integers, one scale per row, for moe_matmul_i8: returns (codes int8 [rows, cols],
+    scales float32 [rows]), and with a residual (codes, scales, h)."""
+    import torch
+
+    dt, wdt = _norm_args(x, weight, residual)
+    rows, cols = x.shape
+    dev = _one_device(x, weight, residual, codes, scales, h_out)
+    h = _norm_h(x, residual, h_out)
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+    else:
+        _want(codes, "codes", (rows, cols), torch.int8)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _want(scales, "scales", (rows,), torch.float32)
+    _launch(dev, load_library().moe_rms_norm_i8, dt, rows, cols, x.data_ptr(), _addr(residual), _addr(weight), wdt, eps,
+            _addr(h), codes.data_ptr(), scales.data_ptr())
+    return (codes, scales) if h is None else (codes, scales, h)
+
+
+def moe_rms_norm_workspace_size(rows: int, cols: int) -> int:
+    n = load_library().moe_rms_norm_workspace_size(rows, cols)
+    if n == 0 and moe_last_error():
+        raise MoeError(MOE_ERR_INVALID_ARG, moe_last_error())
+    return int(n)
+
+
+def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dtype=None, workspace=None, out=None,
+                      dw_out=None):
+    """Gradients of moe_rms_norm: (dx, dw) from dy (y's gradient), h (what the norm was taken of) and dh (what reaches h
+    past the norm, or None).  dx is the gradient of x and of the residual alike; dw has the weight's type, or dw_dtype,
+    and is None without a weight or with need_dw=False.  out (for dx) may be dy or dh."""
+    import torch
+
+    dt, wdt = _norm_args(h, weight, None, "h")
+    rows, cols = h.shape
+    _want(dy, "dy", h.shape, h.dtype)
+    if dh is not None:
+        _want(dh, "dh", h.shape, h.dtype)
+    dev = _one_device(dy, h, weight, dh, workspace, out, dw_out)
+    if out is None:
+        out = torch.empty_like(h)
+    else:
+        _want(out, "out", h.shape, h.dtype)
+    dw, dwt, ws, nb = None, wdt, None, 0
+    if weight is not None and need_dw:
+        dw, dwt = _out(dw_out, (cols,), dw_dtype, wdt, dev)
+        if workspace is None:
+            workspace = torch.empty(moe_rms_norm_workspace_size(rows, cols), dtype=torch.uint8, device=dev)
+        ws, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif dw_out is not None or dw_dtype is not None:
+        raise ValueError("dw_out and dw_dtype are for the weight's gradient: none is asked for")
+    _launch(dev, load_library().moe_rms_norm_grad, dt, rows, cols, dy.data_ptr(), h.data_ptr(), _addr(weight), wdt, eps,
+            _addr(dh), out.data_ptr(), _addr(dw), dwt, ws, nb)
+    return out, dw
 
 
 def moe_profile_events(events_array, n_events: int):

@@ -34,7 +34,7 @@
 // more steps, where it needs registers the loop does not have); stores straight from the registers (690 us).
 // Non-temporal stores of outputs of 256 MB and more: within 1% over 38 sizes; not kept.
 #pragma once
-#include "gmm_core.h"
+#include "gmm_items.h"
 #include "tile_core.h"
 
 namespace moe {
@@ -50,7 +50,6 @@ constexpr int kGmmPLoads = 2;       // 1 KiB loads per wave of a half of P
 constexpr int kGmmQLoads = 4;       // ... and of a step of Q
 constexpr int kGmmNonTemporal = 2;  // the loads' cache policy operand: nt
 constexpr uint32_t kGmmOutside = 0xfffffff0u;  // an offset past every record count
-constexpr int kGmmSuper = 4;        // row tiles that run side by side on one XCD
 
 typedef __amdgpu_buffer_rsrc_t GmmRsrc;
 typedef __attribute__((address_space(3))) void* GmmLds;
@@ -417,45 +416,6 @@ __device__ __forceinline__ void gmm_store(const GmmOut& o, const GmmRings& r, in
   });
 }
 
-// Work items are tiles x slabs, numbered so that kGmmSuper tiles run slab by slab, side by side: 32
-// work-groups of an XCD then share kGmmSuper tiles' rows and 8 slabs in its L2.
-__device__ __forceinline__ void gmm_unnumber(int64_t item, int64_t tiles, int slabs, int64_t& tile, int& slab) {
-  const int64_t sup = item / ((int64_t)kGmmSuper * slabs), first = sup * kGmmSuper;
-  const int rem = (int)(item - first * slabs);
-  const int n = tiles - first < kGmmSuper ? (int)(tiles - first) : kGmmSuper;
-  tile = first + rem % n;
-  slab = rem / n;
-}
-
-// The hardware deals work-group b to XCD b % 8.  The items of the full tiles are cut into one contiguous range per
-// XCD, and after them those of the partial tiles: every XCD gets the same share of both (to within one
-// item), and the short items come last, where they fill the chip's last round.  False for padding.
-__device__ __forceinline__ bool gmm_row_item(int64_t b, const GmmTiles& t, int slabs, int& tile, int& slab) {
-  const int64_t xcd = b % kXcds;
-  int64_t local = b / kXcds, nf = (int64_t)t.full * slabs, np = (int64_t)t.partial * slabs, tt;
-  const int64_t per_f = (nf + kXcds - 1) / kXcds, per_p = (np + kXcds - 1) / kXcds;
-  if (local < per_f) {
-    const int64_t item = xcd * per_f + local;
-    if (item >= nf) return false;
-    gmm_unnumber(item, t.full, slabs, tt, slab);
-    tile = (int)tt;
-    return true;
-  }
-  local -= per_f;
-  const int64_t item = xcd * per_p + local;
-  if (local >= per_p || item >= np) return false;
-  gmm_unnumber(item, t.partial, slabs, tt, slab);
-  tile = t.full + (int)tt;
-  return true;
-}
-
-// Work-groups that cover the items of any grouping of max_rows rows.
-inline int64_t gmm_row_grid(const GmmArgs& a, int slabs, int tile) {
-  const int64_t full = a.max_rows / tile, partial = a.max_rows < a.G ? a.max_rows : a.G;
-  const auto per = [&](int64_t tiles) { return (tiles * slabs + kXcds - 1) / kXcds; };
-  return (per(full) + per(partial)) * kXcds;
-}
-
 // TN: sums x n tiles x slabs, dealt to the XCDs in chunks of consecutive items (groups differ in length, so
 // that long contiguous ranges could leave XCDs idle): 32 of them, what an XCD runs at once, when every
 // XCD gets 4 chunks or more, else 8.
@@ -660,7 +620,7 @@ hipError_t gmm_launch_rows(const GmmArgs& a, hipStream_t s) {
   using S = GmmShape<W>;
   const int slabs = ((F == GmmForm::kNT ? a.N : a.K) + S::kTile - 1) / S::kTile;
   gmm_rows_kernel<F, T, W, kOnce>
-      <<<gmm_grid(gmm_row_grid(a, slabs, S::kTile) * a.split), dim3(S::kThreads), 0, s>>>(a, slabs);
+      <<<gmm_grid(gmm_row_grid(a.max_rows, a.G, slabs, S::kTile) * a.split), dim3(S::kThreads), 0, s>>>(a, slabs);
   return hipGetLastError();
 }
 

@@ -3,6 +3,7 @@
 // every step of the layer runs in the kernels of this directory.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -13,6 +14,8 @@
 #include "gmm.h"
 #include "kernels.h"
 #include "moe.h"
+#include "mx4.h"
+#include "norm.h"
 
 namespace {
 
@@ -581,6 +584,98 @@ int run_matmul(const char* fn, const moe::GmmArgs& a, void* workspace, size_t wo
   return device_status(e, fn);
 }
 
+// ----------------------------------------------------------------------------- microscaled 4 bits, the norm
+constexpr int kMx4Block = 32;
+
+int check_mx4(const char* fn, const moe::Mx4Args& a, int32_t out_dtype) {
+  if (a.G < 1 || a.G > kMaxGroups) return fail(MOE_ERR_INVALID_ARG, "%s: n_groups must be in [1, %d]", fn, kMaxGroups);
+  if (a.N < 1 || a.K < 1) return fail(MOE_ERR_INVALID_ARG, "%s: N and K must be positive (N=%d K=%d)", fn, a.N, a.K);
+  if (a.K % kMx4Block) return fail(MOE_ERR_INVALID_ARG, "%s: K (%d) must be a multiple of %d", fn, a.K, kMx4Block);
+  if (a.max_rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative max_rows", fn);
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: output dtype %d", fn, out_dtype);
+  if (a.max_rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: max_rows exceeds 2^31-1", fn);
+  if (a.N > kMaxMatmulSide || a.K > kMaxMatmulSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: N and K must be at most %d", fn, kMaxMatmulSide);
+  constexpr int64_t kSpan = int64_t(1) << 32;  // 32-bit byte offsets
+  if ((int64_t)a.N * a.K / 2 >= kSpan) return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weight must stay below 4 GiB", fn);
+  if (!a.group_offsets && a.G != 1)
+    return fail(MOE_ERR_INVALID_ARG, "%s: group_offsets may be NULL for one group only", fn);
+  if (a.x_rows < 0 || (a.row_index ? a.x_rows == 0 && a.max_rows > 0 : a.x_rows < a.max_rows))
+    return fail(MOE_ERR_INVALID_ARG, "%s: x has too few rows (%lld)", fn, (long long)a.x_rows);
+  if (a.x_rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: x_rows exceeds 2^31-1", fn);
+  if (a.row_index && a.x_rows * a.K / 2 >= kSpan)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: a gathered x must stay below 4 GiB", fn);
+  if (!moe::mx4_grid_ok(a)) return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 output tiles", fn);
+  return MOE_OK;
+}
+
+// Sizes that the quantizers share.
+int check_rows(const char* fn, int64_t rows, int32_t cols, int32_t max_cols) {
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative rows", fn);
+  if (cols < 1) return fail(MOE_ERR_INVALID_ARG, "%s: cols must be positive", fn);
+  if (cols > max_cols) return fail(MOE_ERR_UNSUPPORTED, "%s: cols must be at most %d", fn, max_cols);
+  if (rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: rows exceeds 2^31-1", fn);
+  return MOE_OK;
+}
+int check_mx4_rows(const char* fn, int64_t rows, int32_t cols) {
+  const int st = check_rows(fn, rows, cols, kMaxMatmulSide);
+  if (st) return st;
+  if (cols % kMx4Block) return fail(MOE_ERR_INVALID_ARG, "%s: cols (%d) must be a multiple of %d", fn, cols, kMx4Block);
+  return MOE_OK;
+}
+
+int check_dtype(const char* fn, const char* what, int32_t dtype) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: %s %d", fn, what, dtype);
+  return MOE_OK;
+}
+
+int check_norm(const char* fn, int32_t dtype, int64_t rows, int32_t cols, int32_t w_dtype, float eps) {
+  int st;
+  if ((st = check_dtype(fn, "dtype", dtype)) || (st = check_dtype(fn, "w_dtype", w_dtype)) ||
+      (st = check_rows(fn, rows, cols, moe::kMaxNormCols)))
+    return st;
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  return MOE_OK;
+}
+
+int run_norm(const char* fn, const char* kernel, int32_t dtype, int64_t rows, int32_t cols, const void* x,
+             const void* residual, const void* weight, int32_t w_dtype, float eps, void* h, void* out, float* scales,
+             moe::NormOut kind, void* stream) {
+  prof_reset();
+  int st = check_norm(fn, dtype, rows, cols, w_dtype, eps);
+  if (st) return st;
+  if (rows == 0) return ok();
+  const bool i8 = kind == moe::NormOut::kI8;
+  if (!x || !out || (i8 && !scales))
+    return fail(MOE_ERR_INVALID_ARG, "%s: x and %s are required", fn, i8 ? "codes and scales" : "y");
+  if ((residual == nullptr) != (h == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: residual and h must both be given or both be NULL", fn);
+  const size_t e = elem_bytes(dtype);
+  if ((st = check_aligned(fn, {{x, e, "x"}, {residual, e, "residual"}, {weight, elem_bytes(w_dtype), "weight"}, {h, e, "h"},
+                               {out, i8 ? 1 : kind == moe::NormOut::kBf16 ? 2u : 4u, "y"}, {scales, 4, "scales"}})))
+    return st;
+  moe::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.w = weight;
+  a.h = h;
+  a.out = out;
+  a.scales = scales;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.bf16 = dtype == MOE_BF16;
+  a.w_bf16 = w_dtype == MOE_BF16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return device_status(timed(kernel, s, [&] { return moe::launch_rms_norm(a, kind, s); }), fn);
+}
+
+size_t norm_workspace(int64_t rows, int32_t cols) {
+  Carver cv(nullptr);
+  cv.take<float>(moe::norm_grad_parts(rows, cols) * moe::norm_grad_ld(cols));
+  return cv.used;
+}
+
 // ----------------------------------------------------------------------------- no-allocation forward
 // Scratch of moe_forward_noalloc: a file-scope device array that every GPU the library runs on holds
 // (its own copy, at its own address) until the process ends.  In host code `scratch` names a host
@@ -910,10 +1005,22 @@ int moe_forward_fp8(const moe_config* cfg, int64_t T, const void* x, const void*
 size_t moe_matmul_workspace_size(int32_t op, int32_t dtype, int32_t n_groups, int64_t max_rows, int32_t N,
                                  int32_t K) {
   const char* fn = "moe_matmul_workspace_size";
+  static const int32_t some_offsets[1] = {0};  // any grouping: never read here
   moe::GmmArgs a{};
-  if (op < MOE_MATMUL_FORWARD || op > MOE_MATMUL_I8) {
+  if (op < MOE_MATMUL_FORWARD || op > MOE_MATMUL_MX4) {
     fail(MOE_ERR_INVALID_ARG, "%s: unknown op %d", fn, op);
     return 0;
+  }
+  if (op == MOE_MATMUL_MX4) {
+    moe::Mx4Args m{};
+    m.G = n_groups;
+    m.N = N;
+    m.K = K;
+    m.max_rows = m.x_rows = max_rows;
+    m.group_offsets = some_offsets;
+    if (check_mx4(fn, m, MOE_F32)) return 0;
+    ok();
+    return moe::mx4_workspace(m);
   }
   a.form = op == MOE_MATMUL_DX ? moe::GmmForm::kNN : op == MOE_MATMUL_DW ? moe::GmmForm::kTN : moe::GmmForm::kNT;
   a.type = moe::GmmType::kI8;
@@ -922,7 +1029,6 @@ size_t moe_matmul_workspace_size(int32_t op, int32_t dtype, int32_t n_groups, in
   a.N = N;
   a.K = K;
   a.max_rows = a.x_rows = max_rows;
-  static const int32_t some_offsets[1] = {0};  // any grouping: never read here
   a.group_offsets = some_offsets;
   if (check_matmul(fn, a, MOE_F32)) return 0;
   ok();
@@ -1072,6 +1178,131 @@ int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_o
                                {y, elem_bytes(y_dtype), "y"}})))
     return st;
   return run_matmul(fn, a, workspace, workspace_bytes, stream);
+}
+
+int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, uint8_t* codes,
+                     uint8_t* scales, void* stream) {
+  prof_reset();
+  const char* fn = "moe_quantize_mx4";
+  int st;
+  if ((st = check_dtype(fn, "dtype", x_dtype)) || (st = check_mx4_rows(fn, rows, cols))) return st;
+  if (swiglu != 0 && swiglu != 1) return fail(MOE_ERR_INVALID_ARG, "%s: swiglu must be 0 or 1", fn);
+  if (rows == 0) return ok();
+  if (!x || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "%s: x, codes and scales are required", fn);
+  if ((st = check_aligned(fn, {{x, elem_bytes(x_dtype), "x"}, {codes, 16, "codes"}, {scales, 16, "scales"}}))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return device_status(timed("quantize_mx4", s, [&] {
+                         return moe::launch_quantize_mx4(x, x_dtype == MOE_BF16, rows, cols, swiglu == 1, codes, scales,
+                                                         s);
+                       }),
+                       fn);
+}
+
+int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* codes, const uint8_t* scales, void* y, int32_t y_dtype,
+                       void* stream) {
+  prof_reset();
+  const char* fn = "moe_dequantize_mx4";
+  int st;
+  if ((st = check_dtype(fn, "dtype", y_dtype)) || (st = check_mx4_rows(fn, rows, cols))) return st;
+  if (rows == 0) return ok();
+  if (!codes || !scales || !y) return fail(MOE_ERR_INVALID_ARG, "%s: codes, scales and y are required", fn);
+  if ((st = check_aligned(fn, {{codes, 16, "codes"}, {scales, 16, "scales"}, {y, elem_bytes(y_dtype), "y"}}))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return device_status(timed("dequantize_mx4", s, [&] {
+                         return moe::launch_dequantize_mx4(codes, scales, rows, cols, y, y_dtype == MOE_BF16, s);
+                       }),
+                       fn);
+}
+
+int moe_matmul_mx4(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_offsets, int64_t max_rows,
+                   const uint8_t* x_codes, const uint8_t* x_scales, int64_t x_rows, const int32_t* row_index,
+                   const uint8_t* w_codes, const uint8_t* w_scales, void* y, int32_t y_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  prof_reset();
+  const char* fn = "moe_matmul_mx4";
+  moe::Mx4Args a{};
+  a.G = n_groups;
+  a.N = N;
+  a.K = K;
+  a.group_offsets = group_offsets;
+  a.max_rows = max_rows;
+  a.x = x_codes;
+  a.xs = x_scales;
+  a.x_rows = x_rows;
+  a.row_index = row_index;
+  a.w = w_codes;
+  a.ws = w_scales;
+  a.out = y;
+  a.out_bf16 = y_dtype == MOE_BF16;
+  int st = check_mx4(fn, a, y_dtype);
+  if (st) return st;
+  if (max_rows == 0) return ok();
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !y)
+    return fail(MOE_ERR_INVALID_ARG, "%s: codes, scales and y are required", fn);
+  if ((st = check_aligned(fn, {{group_offsets, 4, "group_offsets"}, {row_index, 4, "row_index"},
+                               {x_codes, 16, "x_codes"}, {x_scales, 16, "x_scales"}, {w_codes, 16, "w_codes"},
+                               {w_scales, 16, "w_scales"}, {y, elem_bytes(y_dtype), "y"}})))
+    return st;
+  if ((st = check_ws(workspace, workspace_bytes, moe::mx4_workspace(a)))) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const moe::Mx4Plan p = moe::mx4_plan(a, workspace);
+  return device_status(timed(p.name, s, [&] { return moe::launch_mx4(p, s); }), fn);
+}
+
+int moe_rms_norm(int32_t dtype, int64_t rows, int32_t cols, const void* x, const void* residual, const void* weight,
+                 int32_t w_dtype, float eps, void* h, void* y, int32_t y_dtype, void* stream) {
+  const int st = check_dtype("moe_rms_norm", "y_dtype", y_dtype);
+  if (st) return st;
+  return run_norm("moe_rms_norm", "rms_norm", dtype, rows, cols, x, residual, weight, w_dtype, eps, h, y, nullptr,
+                  y_dtype == MOE_BF16 ? moe::NormOut::kBf16 : moe::NormOut::kF32, stream);
+}
+
+int moe_rms_norm_i8(int32_t dtype, int64_t rows, int32_t cols, const void* x, const void* residual, const void* weight,
+                    int32_t w_dtype, float eps, void* h, int8_t* codes, float* scales, void* stream) {
+  return run_norm("moe_rms_norm_i8", "rms_norm_i8", dtype, rows, cols, x, residual, weight, w_dtype, eps, h, codes,
+                  scales, moe::NormOut::kI8, stream);
+}
+
+size_t moe_rms_norm_workspace_size(int64_t rows, int32_t cols) {
+  if (check_rows("moe_rms_norm_workspace_size", rows, cols, moe::kMaxNormCols)) return 0;
+  ok();
+  return norm_workspace(rows, cols);
+}
+
+int moe_rms_norm_grad(int32_t dtype, int64_t rows, int32_t cols, const void* dy, const void* h, const void* weight,
+                      int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  prof_reset();
+  const char* fn = "moe_rms_norm_grad";
+  int st;
+  if ((st = check_norm(fn, dtype, rows, cols, w_dtype, eps)) || (st = check_dtype(fn, "dw_dtype", dw_dtype))) return st;
+  if (rows == 0 && !dw) return ok();
+  if (rows > 0 && (!dy || !h || !dx)) return fail(MOE_ERR_INVALID_ARG, "%s: dy, h and dx are required", fn);
+  const size_t e = elem_bytes(dtype);
+  if ((st = check_aligned(fn, {{dy, e, "dy"}, {h, e, "h"}, {weight, elem_bytes(w_dtype), "weight"}, {dh, e, "dh"},
+                               {dx, e, "dx"}, {dw, elem_bytes(dw_dtype), "dw"}})))
+    return st;
+  if (dw && (st = check_ws(workspace, workspace_bytes, norm_workspace(rows, cols)))) return st;
+  moe::NormGradArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.w = weight;
+  a.dh = dh;
+  a.dx = dx;
+  a.part = dw ? static_cast<float*>(workspace) : nullptr;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.bf16 = dtype == MOE_BF16;
+  a.w_bf16 = w_dtype == MOE_BF16;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t err = hipSuccess;
+  if (rows > 0) err = timed("rms_norm_grad", s, [&] { return moe::launch_norm_grad(a, s); });
+  if (err == hipSuccess && dw)
+    err = timed("rms_norm_grad_join", s, [&] {
+      return moe::launch_norm_grad_join(a.part, moe::norm_grad_parts(rows, cols), cols, dw, dw_dtype == MOE_BF16, s);
+    });
+  return device_status(err, fn);
 }
 
 const char* moe_last_error(void) { return g_last_error.c_str(); }
