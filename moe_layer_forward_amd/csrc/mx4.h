@@ -28,7 +28,8 @@ struct Mx4Args {
 // The kernel that a product's sizes call for.
 struct Mx4Plan {
   Mx4Args args;
-  int p_blocks;      // most 16-row blocks of an item
+  int waves;         // of the tile kernel's work-groups, 0: the stream kernel
+  int p_blocks;      // stream: most 16-row blocks of an item
   const char* name;
 };
 Mx4Plan mx4_plan(const Mx4Args& a, void* workspace);
@@ -39,6 +40,8 @@ bool mx4_grid_ok(const Mx4Args& a);
 hipError_t launch_mx4(const Mx4Plan& p, hipStream_t s);
 hipError_t launch_mx4_stream(const Mx4Args& a, int p_blocks, hipStream_t s);
 int64_t mx4_stream_grid(const Mx4Args& a, int p_blocks);
+hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s);
+int64_t mx4_tile_grid(const Mx4Args& a, int waves);
 
 hipError_t launch_quantize_mx4(const void* x, bool x_bf16, int64_t rows, int32_t cols, bool swiglu, uint8_t* codes,
                                uint8_t* scales, hipStream_t s);
