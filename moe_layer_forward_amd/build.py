@@ -36,7 +36,7 @@ MOE_SOURCES = ["moe_api.cpp", "route.hip", "permute.hip", "gemm_stream.hip", "ge
                "gemm_skinny.hip",
                "gemm_quant.hip", "gemm_simple.hip", "combine.hip", "gmm_launch.cpp", "gmm_any.hip",
                "gmm_tile_nt.hip", "gmm_tile_nn.hip", "gmm_tile_tn.hip", "gmm_tile_i8.hip", "quantize.hip",
-               "norm.hip", "mx4_launch.cpp", "mx4_quantize.hip", "mx4_stream.hip", "mx4_tile.hip"]
+               "norm.hip", "mx4_launch.cpp", "mx4_quantize.hip", "mx4_stream.hip", "mx4_tile.hip", "mx4_ring.hip"]
 
 
 def _run(cmd, verbose):

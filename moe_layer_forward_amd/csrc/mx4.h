@@ -25,11 +25,17 @@ struct Mx4Args {
   void* out;
   int32_t out_bf16;
 };
+// The stream kernel's items, 16 p_blocks rows x 16 q_blocks columns, and the waves that share a sum.
+struct Mx4Stream {
+  int p_blocks, q_blocks, waves;
+};
+enum class Mx4Kernel { kStream, kRing, kTile };
 // The kernel that a product's sizes call for.
 struct Mx4Plan {
   Mx4Args args;
-  int waves;         // of the tile kernel's work-groups, 0: the stream kernel
-  int p_blocks;      // stream: most 16-row blocks of an item
+  Mx4Kernel kernel;
+  Mx4Stream stream;  // kRing: its p_blocks
+  int tile_waves;    // kTile: of a work-group
   const char* name;
 };
 Mx4Plan mx4_plan(const Mx4Args& a, void* workspace);
@@ -38,8 +44,11 @@ size_t mx4_workspace(const Mx4Args& a);
 // Whether its work-groups number at most 2^31.
 bool mx4_grid_ok(const Mx4Args& a);
 hipError_t launch_mx4(const Mx4Plan& p, hipStream_t s);
-hipError_t launch_mx4_stream(const Mx4Args& a, int p_blocks, hipStream_t s);
-int64_t mx4_stream_grid(const Mx4Args& a, int p_blocks);
+hipError_t launch_mx4_stream(const Mx4Args& a, const Mx4Stream& c, hipStream_t s);
+int64_t mx4_stream_grid(const Mx4Args& a, const Mx4Stream& c);
+// Items of 16 p_blocks rows x 64 q_blocks columns; mx4_ring_items of them at most.
+hipError_t launch_mx4_ring(const Mx4Args& a, int p_blocks, int q_blocks, int per_cu, hipStream_t s);
+int64_t mx4_ring_items(const Mx4Args& a, int p_blocks, int q_blocks);
 hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s);
 int64_t mx4_tile_grid(const Mx4Args& a, int waves);
 

@@ -19,6 +19,93 @@ __device__ __forceinline__ gmm_u32x4 mx4_load128(Mx4Rsrc r, uint32_t off) {
 __device__ __forceinline__ uint32_t mx4_load32(Mx4Rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
 }
+__device__ __forceinline__ uint32_t mx4_load8(Mx4Rsrc r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, 0);
+}
+
+// The row tiles of the groups, `tile` rows each, as GmmTiles numbers them: the full ones first, then every group's last,
+// partial one.  GmmTiles walks a lane's groups one by one; here the lanes' loads go out together and a tile is found in
+// the registers, since with few rows the search is a good part of an item.
+struct Mx4Tiles {
+  static constexpr int kHeld = 8;  // groups of a lane whose rows stay in registers: 512 in all
+  GmmTiles t;
+  int n_full, n_part;  // of this lane's groups
+  int off[kHeld + 1];
+
+  __device__ __forceinline__ static int scan(int v) {  // inclusive sum over the lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1, 2, 4, 8: rows of 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 to rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 to rows 2 and 3
+    return v;
+  }
+  __device__ __forceinline__ static int clamp(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+  __device__ __forceinline__ static int per_lane(const Mx4Args& a) { return (a.G + 63) / 64; }
+
+  __device__ __forceinline__ void count(const Mx4Args& a, int tile) {
+    const int lane = threadIdx.x & 63, per = per_lane(a), most = (int)a.max_rows;
+    if (!a.group_offsets) {
+      t.full = most / tile;
+      t.partial = most % tile != 0;
+      return;
+    }
+    if (per > kHeld) return t.count(a.group_offsets, a.G, a.max_rows, tile);
+#pragma unroll
+    for (int j = 0; j <= kHeld; ++j) {  // as gmm_group_rows: inside [0, most], not decreasing
+      const int at = lane * per + j;
+      off[j] = j <= per ? a.group_offsets[at < a.G ? at : a.G] : 0;
+    }
+    n_full = n_part = 0;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int b = clamp(off[j], 0, most), rows = clamp(off[j + 1], b, most) - b;
+      const bool mine = j < per && lane * per + j < a.G;
+      n_full += mine ? rows / tile : 0;
+      n_part += mine ? rows % tile != 0 : 0;
+    }
+    t.full_to = scan(n_full);
+    t.partial_to = scan(n_part);
+    t.full = __builtin_amdgcn_readlane(t.full_to, 63);
+    t.partial = __builtin_amdgcn_readlane(t.partial_to, 63);
+  }
+
+  // Tile t0 (below full + partial): rows [beg, end) of group g.
+  __device__ __forceinline__ void find(const Mx4Args& a, int tile, int t0, int& g, int64_t& beg, int64_t& end) const {
+    const int lane = threadIdx.x & 63, per = per_lane(a), most = (int)a.max_rows;
+    if (!a.group_offsets) {
+      g = 0;
+      beg = (int64_t)t0 * tile;
+      end = beg + tile < most ? beg + tile : most;
+      return;
+    }
+    if (per > kHeld) {
+      t.find(a.group_offsets, a.G, a.max_rows, tile, t0, g, beg, end);
+      return;
+    }
+    const bool is_full = t0 < t.full;
+    const int rel = is_full ? t0 : t0 - t.full, to = is_full ? t.full_to : t.partial_to, n = is_full ? n_full : n_part;
+    const int owner = __ffsll((unsigned long long)__ballot(to > rel)) - 1;
+    int left = rel - (to - n), gj = 0, b = 0, e = 0;  // each lane among its own groups; the owner's are read
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int bj = clamp(off[j], 0, most), ej = clamp(off[j + 1], bj, most), rows = ej - bj;
+      const int k = j < per ? is_full ? rows / tile : rows % tile != 0 : 0;
+      if (!found && left < k) {
+        found = true;
+        gj = lane * per + j;
+        b = is_full ? bj + left * tile : bj + rows / tile * tile;
+        e = is_full ? b + tile : ej;
+      }
+      left -= k;
+    }
+    g = __builtin_amdgcn_readlane(gj, owner);
+    beg = __builtin_amdgcn_readlane(b, owner);
+    end = __builtin_amdgcn_readlane(e, owner);
+  }
+};
 
 // c += q p^T over 128 values: lane l holds 32 of row l % 16 of each and their scale, byte TQ (TP) of sq (sp); lane l,
 // element e of c is row l % 16 of p, row 4 (l / 16) + e of q.

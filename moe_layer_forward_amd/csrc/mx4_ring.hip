@@ -1,0 +1,262 @@
+// Microscaled 4-bit products for groups of few rows: a stream of weights.
+//
+// Work item = up to 16 NB rows of one group x 64 columns, 16 to each of four waves.  A step is a window of 512 values: 256
+// bytes of every row, whole lines, which go straight to LDS, four rows an instruction: the wave's own 16 rows of weights,
+// its quarter of the token rows, and in one more instruction the 16 bytes of scales of its weight rows and of one block
+// of token rows.  In v_mfma_scale_f32_16x16x128 number t of a step lane l multiplies block 4 (l / 16) + t of row
+// l % 16, so that one dword holds its scales, byte t for number t.  Row r keeps that block's 16 bytes at position
+// (4 t + l / 16) ^ r: the rows of one fragment read fall in different banks.
+//
+// Work-groups stay: each takes every 64th item of its XCD's share (neighbours read neighbouring weights), and the loads run
+// kDepth - 1 steps ahead of the products, across the ends of items, so that the stream never stops.  One barrier a step: a
+// stage is loaded again when every wave has passed the barrier of the step after it.
+#include "mx4_core.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRingWaves = 4;
+constexpr int kRingRow = 256;  // bytes of a row and step
+
+// QB 16-column blocks to a wave; as many stages as let `per` work-groups run on a CU.
+template <int NB, int QB, int per>
+struct RingShape {
+  static constexpr int kX = NB * 16 * kRingRow, kW = kRingWaves * QB * 16 * kRingRow, kS = kRingWaves * (QB + 1) * 256;
+  static constexpr int kFit = 160 * 1024 / per / (kX + kW + kS), kDepth = kFit < 6 ? kFit : 6;
+  static constexpr int kLoads = 4 * QB + NB + 1;  // of a wave and step
+  static_assert((kDepth - 2) * kLoads <= 63, "vmcnt");
+};
+
+struct RingStage {
+  char *x, *w, *s;
+};
+
+// Row rl of the item's rows in x: uniform (scalar loads of the index: a vector load's wait would drain the stream).
+__device__ __forceinline__ int ring_row(const Mx4Args& a, int64_t beg, int rows, int rl) {
+  rl = rl < rows ? rl : rows - 1;  // rows past the end read the last one
+  if (!a.row_index) return rl;
+  typedef const __attribute__((address_space(4))) int32_t* Const;
+  const int64_t i = ((Const)(uintptr_t)a.row_index)[beg + rl];
+  return (int)(i < 0 ? 0 : i >= a.x_rows ? a.x_rows - 1 : i);
+}
+
+// What a lane loads of an item.
+template <int NB, int QB>
+struct RingLoads {
+  const uint8_t *w, *x;  // uniform
+  const uint8_t* s;      // the lane's row of scales
+  uint32_t nw, nx;
+  uint32_t wo[4 * QB], xo[NB];
+
+  __device__ __forceinline__ static uint32_t chunk(int r) {  // which 16 bytes of a window of row r go where the lane's go
+    const int c = (threadIdx.x ^ r) & 15;
+    return (uint32_t)(4 * (c & 3) + (c >> 2)) * 16;
+  }
+  __device__ __forceinline__ void init(const Mx4Args& a, int g, int64_t beg, int64_t end, int slab, int wave) {
+    const int lane = threadIdx.x & 63, quarter = lane >> 4, q0 = (slab * kRingWaves + wave) * 16 * QB;
+    const int rows = (int)(end - beg), cols = a.N - q0 < 1 ? 1 : a.N - q0 < 16 * QB ? a.N - q0 : 16 * QB;
+    const uint32_t ld = (uint32_t)(a.K / 2), lds = (uint32_t)mx4_scale_cols(a.K);
+    const int64_t w0 = (int64_t)g * a.N + (q0 < a.N ? q0 : a.N - 1), x0 = a.row_index ? 0 : beg;
+    w = a.w + w0 * ld;
+    x = a.x + x0 * ld;
+    nw = (uint32_t)cols * ld;
+    nx = (uint32_t)((a.row_index ? a.x_rows : rows) * ld);
+#pragma unroll
+    for (int i = 0; i < 4 * QB; ++i) {
+      const int r = 4 * i + quarter;
+      wo[i] = (uint32_t)(r < cols ? r : cols - 1) * ld + chunk(r);
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      int row = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = ring_row(a, beg, rows, 16 * i + 4 * wave + k);
+        row = quarter == k ? at : row;
+      }
+      xo[i] = (uint32_t)row * ld + chunk(4 * wave + quarter);
+    }
+    const int r = lane & 15;
+    s = a.ws + (w0 + (lane < cols ? lane : cols - 1)) * lds;
+    if (wave < NB) {
+      int row = 0;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int at = ring_row(a, beg, rows, 16 * wave + k);
+        row = r == k ? at : row;
+      }
+      if (lane >= 16 * QB) s = a.xs + (x0 + row) * lds;
+    }
+  }
+  // window `win` of the rows, which have ld bytes
+  __device__ __forceinline__ void issue(const RingStage& st, int win, uint32_t ld, int wave) const {
+    typedef __attribute__((address_space(3))) void* Lds;
+    const int lane = threadIdx.x & 63, quarter = lane >> 4;
+    const uint32_t kb = (uint32_t)win * kRingRow, left = ld - kb;
+    const Mx4Rsrc rw = mx4_rsrc(w + kb, nw - kb), rx = mx4_rsrc(x + kb, nx - kb);
+    // chunks past the end of a row put zeros into LDS and read nothing
+#pragma unroll
+    for (int i = 0; i < 4 * QB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (Lds)(st.w + (wave * 4 * QB + i) * 1024), 16,
+                                               chunk(4 * i + quarter) < left ? wo[i] : kMx4Outside, 0, 0, 2);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (Lds)(st.x + (i * 4 + wave) * 1024), 16,
+                                               chunk(4 * wave + quarter) < left ? xo[i] : kMx4Outside, 0, 0, 0);
+    if (lane < 16 * QB + 16) __builtin_amdgcn_global_load_lds(s + kb / 16, (Lds)(st.s + wave * (QB + 1) * 256), 16, 0, 0);
+  }
+};
+
+// The share of a work-group: items first, first + stride, ... below end.
+struct RingShare {
+  int first, end, stride;
+  __device__ __forceinline__ RingShare(int items) {
+    const int xcd = blockIdx.x % kXcds, share = (items + kXcds - 1) / kXcds;
+    stride = gridDim.x / kXcds;
+    first = xcd * share + blockIdx.x / kXcds;
+    end = (xcd + 1) * share < items ? (xcd + 1) * share : items;
+  }
+  __device__ __forceinline__ int count() const { return first < end ? (end - first + stride - 1) / stride : 0; }
+};
+
+template <int NB, int QB, int per>
+__global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args a, int slabs) {
+  using S = RingShape<NB, QB, per>;
+  constexpr int D = S::kDepth;
+#define MOE_MX4_STAGE(i) \
+  __shared__ __align__(16) char x##i##_[i < D ? S::kX : 16], w##i##_[i < D ? S::kW : 16], s##i##_[i < D ? S::kS : 16]
+  MOE_MX4_STAGE(0);
+  MOE_MX4_STAGE(1);
+  MOE_MX4_STAGE(2);
+  MOE_MX4_STAGE(3);
+  MOE_MX4_STAGE(4);
+  MOE_MX4_STAGE(5);
+#undef MOE_MX4_STAGE
+  [[maybe_unused]] const auto stage = [&](auto dc) -> RingStage {
+    constexpr int d = decltype(dc)::value % D;
+    if constexpr (d == 0) return {x0_, w0_, s0_};
+    else if constexpr (d == 1) return {x1_, w1_, s1_};
+    else if constexpr (d == 2) return {x2_, w2_, s2_};
+    else if constexpr (d == 3) return {x3_, w3_, s3_};
+    else if constexpr (d == 4) return {x4_, w4_, s4_};
+    else return {x5_, w5_, s5_};
+  };
+#if defined(__HIP_DEVICE_COMPILE__)
+  Mx4Tiles tiles;
+  tiles.count(a, 16 * NB);
+  const RingShare share((tiles.t.full + tiles.t.partial) * slabs);
+  const int mine = share.count();
+  if (!mine) return;
+  const int wave = gmm_uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, part = lane >> 4;
+  const uint32_t ld = (uint32_t)(a.K / 2);
+  const int windows = (int)((ld + kRingRow - 1) / kRingRow);
+  RingLoads<NB, QB> loads;
+  int g, load_item = share.first, load_win = 0, item = share.first, win = 0, done = 0;
+  int64_t beg, end;
+  const auto next_load = [&](const RingStage& st) {
+    loads.issue(st, load_win, ld, wave);
+    if (++load_win == windows) {
+      load_win = 0;
+      load_item += share.stride;
+      if (load_item < share.end) {
+        tiles.find(a, 16 * NB, load_item / slabs, g, beg, end);
+        loads.init(a, g, beg, end, load_item % slabs, wave);
+      } else {
+        loads.nw = loads.nx = 0;  // past the last item: nothing is read, but the waits count the same
+      }
+    }
+  };
+  tiles.find(a, 16 * NB, load_item / slabs, g, beg, end);
+  loads.init(a, g, beg, end, load_item % slabs, wave);
+  static_for<D - 1>([&](auto dc) { next_load(stage(dc)); });
+  f32x4 acc[NB][QB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < QB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int turns = (mine * windows + D - 1) / D;
+  for (int turn = 0; turn < turns; ++turn)
+    static_for<D>([&](auto dc) {
+      constexpr int d = decltype(dc)::value;
+      wait_vmcnt<(D - 2) * S::kLoads>();
+      block_sync_lds();
+      next_load(stage(std::integral_constant<int, d + D - 1>{}));
+      __builtin_amdgcn_sched_barrier(0);
+      const RingStage st = stage(dc);
+      const uint32_t mask = mx4_scale_mask(a.K / 32 - 16 * win - 4 * part);  // no scales from the padding
+      const char* const scales = st.s + r * 16 + part * 4;
+      uint32_t sw[QB], sx[NB];
+#pragma unroll
+      for (int j = 0; j < QB; ++j)
+        sw[j] = *reinterpret_cast<const uint32_t*>(scales + (wave * (QB + 1) + j) * 256) & mask;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        sx[i] = *reinterpret_cast<const uint32_t*>(scales + (i * (QB + 1) + QB) * 256) & mask;
+      static_for<4>([&](auto tc) {
+        constexpr int t = decltype(tc)::value;
+        const int at = r * kRingRow + (((4 * t + part) ^ r) << 4);
+        gmm_u32x4 w[QB], x[NB];
+#pragma unroll
+        for (int j = 0; j < QB; ++j) w[j] = *reinterpret_cast<const gmm_u32x4*>(st.w + (wave * QB + j) * 4096 + at);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) x[i] = *reinterpret_cast<const gmm_u32x4*>(st.x + i * 4096 + at);
+#pragma unroll
+        for (int j = 0; j < QB; ++j)
+#pragma unroll
+          for (int i = 0; i < NB; ++i) acc[i][j] = mx4_mfma<t, t>(w[j], sw[j], x[i], sx[i], acc[i][j]);
+      });
+      if (++win == windows) {
+        if (done < mine) {
+          int gg;
+          int64_t b, e;
+          tiles.find(a, 16 * NB, item / slabs, gg, b, e);
+          const int q0 = (item % slabs * kRingWaves + wave) * 16 * QB;
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < QB; ++j) {
+              const int col = q0 + 16 * j + 4 * part;
+              if (b + 16 * i + r < e && col < a.N)
+                mx4_store4(a.out, a.out_bf16, (b + 16 * i + r) * a.N + col, a.N - col, acc[i][j]);
+              acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+        }
+        win = 0;
+        item += share.stride;
+        ++done;
+      }
+    });
+  wait_vmcnt<0>();  // no load may land in LDS that belongs to someone else
+#endif
+}
+
+template <int NB, int QB>
+void launch_ring(const Mx4Args& a, int per_cu, hipStream_t s) {
+  const int slabs = (a.N + 64 * QB - 1) / (64 * QB);
+  const int64_t items = (mx4_ring_items(a, NB, QB) + kXcds - 1) / kXcds * kXcds, most = 256 * per_cu;
+  const dim3 grid((unsigned)(items < most ? items : most)), block(64 * kRingWaves);
+  if (per_cu == 1) mx4_ring_kernel<NB, QB, 1><<<grid, block, 0, s>>>(a, slabs);
+  else if constexpr (RingShape<NB, QB, 2>::kFit >= 2) mx4_ring_kernel<NB, QB, 2><<<grid, block, 0, s>>>(a, slabs);
+}
+
+template <int NB>
+void launch_ring(const Mx4Args& a, int q_blocks, int per_cu, hipStream_t s) {
+  if (q_blocks == 1) launch_ring<NB, 1>(a, per_cu, s);
+  else launch_ring<NB, 2>(a, per_cu, s);
+}
+
+}  // namespace
+
+int64_t mx4_ring_items(const Mx4Args& a, int p_blocks, int q_blocks) {
+  return gmm_max_tiles(a.max_rows, a.G, 16 * p_blocks) * ((a.N + 64 * q_blocks - 1) / (64 * q_blocks));
+}
+
+hipError_t launch_mx4_ring(const Mx4Args& a, int p_blocks, int q_blocks, int per_cu, hipStream_t s) {
+  if (p_blocks == 1) launch_ring<1>(a, q_blocks, per_cu, s);
+  else if (p_blocks == 2) launch_ring<2>(a, q_blocks, per_cu, s);
+  else if (p_blocks == 3) launch_ring<3>(a, q_blocks, per_cu, s);
+  else launch_ring<4>(a, q_blocks, per_cu, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -58,11 +58,10 @@ struct Mx4LoadScales {
   uint32_t records, off, end;
   int win0;
 
-  template <class RowOf>
-  __device__ __forceinline__ void init(const uint8_t* b, uint32_t rec, uint32_t ld, int first, int n, RowOf row) {
+  __device__ __forceinline__ void init(const uint8_t* b, uint32_t rec, int64_t row, uint32_t ld, int first, int n) {
     base = gmm_uniform(reinterpret_cast<const char*>(b));
     records = (uint32_t)gmm_uniform((int)rec);
-    off = (uint32_t)row() * ld;
+    off = (uint32_t)row * ld;
     win0 = first;
     const uint32_t to = (uint32_t)(first + n) * 16;
     end = to < ld ? to : ld;
@@ -245,10 +244,9 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& a, const Mx4Rings& 
   Mx4Load<W, kGmmQLoads, kOnce> lq;
   lq.init(a.w + w0 * ld, (uint32_t)cols * ld, ld, 2 * first, 2 * n, wave, w_row);
   Mx4LoadScales ls;
-  if (wave < W / 2)
-    ls.init(a.xs + x0 * lds, (uint32_t)(xn * lds), lds, first, n, [&] { return x_row(64 * wave + lane); });
-  else
-    ls.init(a.ws + w0 * lds, (uint32_t)cols * lds, lds, first, n, [&] { return w_row(64 * (wave - W / 2) + lane); });
+  const bool of_x = wave < W / 2;
+  ls.init(of_x ? a.xs + x0 * lds : a.ws + w0 * lds, of_x ? (uint32_t)(xn * lds) : (uint32_t)cols * lds,
+          of_x ? x_row(64 * wave + lane) : w_row(64 * (wave - W / 2) + lane), lds, first, n);
   GmmFrags<GmmAlong<Mx4Type, S::kHalf>, 2> fp;
   fp.init(wr);
   GmmFrags<GmmAlong<Mx4Type, S::kTile>, 1> fq;
