@@ -355,14 +355,19 @@ def moe_forward_fp8(cfg, x, w_router, f8, ws_gate=None, ws_up=None, ws_down=None
 
 # --------------------------------------------------------------------------- grouped matrix products
 # These calls are short (a few microseconds of kernel at decode sizes), so the marshalling below is kept lean.
-def _matmul_dtype(t, what):
-    import torch
+_moe_dtypes = {}  # torch dtype -> moe dtype (filled at the first call: torch is imported late)
 
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_F32
-    raise ValueError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+
+def _matmul_dtype(t, what):
+    dt = _moe_dtypes.get(t.dtype)
+    if dt is None:
+        import torch
+
+        _moe_dtypes.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
+        dt = _moe_dtypes.get(t.dtype)
+        if dt is None:
+            raise ValueError(f"{what} must be bfloat16 or float32, got {t.dtype}")
+    return dt
 
 
 def _want(t, what, shape, dtype=None):
@@ -406,35 +411,44 @@ def _addr(t):
 
 def _one_device(*tensors):
     """The device of the tensors (all contiguous, on one GPU)."""
-    dev = None
+    index = first = None
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("moe: every tensor must live on the GPU")
+        i = t.get_device()  # -1: not on a GPU
+        if i != index:
+            if i < 0 or not t.is_cuda:
+                raise ValueError("moe: every tensor must live on the GPU")
+            if index is not None:
+                raise ValueError(f"moe: tensors on {t.device} and {first.device}")
+            index, first = i, t
         if not t.is_contiguous():
             raise ValueError("moe: tensors must be contiguous")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"moe: tensors on {t.device} and {dev}")
-    return dev
+    return None if first is None else first.device
+
+
+_current = None  # (the raw handle of a device's current stream, the current device), as functions
 
 
 def _launch(dev, entry, *args):
     """The C call on dev's current stream, with dev the current device (a stream belongs to its device)."""
-    import torch
+    global _current
+    if _current is None:
+        import torch
 
-    # the raw handle of the current stream, without building a Stream object around it
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    stream = raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        status = entry(*args, stream)
+        # the raw handle, without building a Stream object around it
+        _current = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                    or (lambda index: torch.cuda.current_stream(index).cuda_stream), torch.cuda.current_device)
+    index = dev.index
+    if index == _current[1]():
+        status = entry(*args, _current[0](index))
         if status != MOE_OK:
             _check(status)
     else:
+        import torch
+
         with torch.cuda.device(dev):
-            _check(entry(*args, stream))
+            _check(entry(*args, _current[0](index)))
 
 
 def moe_matmul_workspace_size(op: int, dtype: int, n_groups: int, max_rows: int, N: int, K: int) -> int:
@@ -644,16 +658,18 @@ def moe_quantize_mx4(x, swiglu=False, codes=None, scales=None):
     dt = _matmul_dtype(x, "x")
     if x.dim() != 2 or (swiglu and x.shape[1] % 2):
         raise ValueError("x must be [rows, cols] (swiglu: [rows, 2 cols])")
-    rows, cols = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
+    rows, cols = x.shape
+    if swiglu:
+        cols //= 2
     if cols % 32:
         raise ValueError(f"cols ({cols}) must be a multiple of 32")
     dev = _one_device(x, codes, scales)
     if codes is None:
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((rows, cols // 2), dtype=torch.uint8)
     else:
         _want(codes, "codes", (rows, cols // 2), torch.uint8)
     if scales is None:
-        scales = torch.empty((rows, mx4_scale_cols(cols)), dtype=torch.uint8, device=dev)
+        scales = x.new_empty((rows, mx4_scale_cols(cols)), dtype=torch.uint8)
     else:
         _want(scales, "scales", (rows, mx4_scale_cols(cols)), torch.uint8)
     _launch(dev, load_library().moe_quantize_mx4, dt, rows, cols, 1 if swiglu else 0, x.data_ptr(), codes.data_ptr(),
@@ -684,10 +700,12 @@ def moe_matmul_mx4(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row
     if x_codes.dim() != 2 or w_codes.dim() != 3:
         raise ValueError("x_codes must be [rows, K / 2] and w_codes [G, N, K / 2]")
     K = _mx4_matrix(x_codes, x_scales, "x")
-    if _mx4_matrix(w_codes, w_scales, "w") != K:
-        raise ValueError(f"x has rows of {K} values, w of {w_codes.shape[2] * 2}")
-    G, N, x_rows = w_codes.shape[0], w_codes.shape[1], x_codes.shape[0]
+    G, N, half = w_codes.shape
+    if half * 2 != K:
+        raise ValueError(f"x has rows of {K} values, w of {half * 2}")
+    _mx4_matrix(w_codes, w_scales, "w")
     _groups(group_offsets, row_index, G)
+    x_rows = x_codes.shape[0]
     rows = x_rows if row_index is None else row_index.shape[0]
     dev = _one_device(x_codes, x_scales, w_codes, w_scales, group_offsets, row_index, workspace, out)
     y, ydt = _out(out, (rows, N), y_dtype, MOE_BF16, dev)
@@ -701,27 +719,27 @@ def moe_matmul_mx4(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row
 # --------------------------------------------------------------------------- the norm before the layer
 def _norm_args(x, weight, residual, what="x"):
     """(moe dtype of x, of the weight) of a norm's operands."""
-    dt = _matmul_dtype(x, what)
-    if x.dim() != 2:
+    dt = wdt = _matmul_dtype(x, what)
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} must be [rows, cols]")
-    wdt = dt
     if weight is not None:
         wdt = _matmul_dtype(weight, "weight")
-        _want(weight, "weight", (x.shape[1],))
+        _want(weight, "weight", (shape[1],))
     if residual is not None:
-        _want(residual, "residual", x.shape, x.dtype)
+        _want(residual, "residual", shape, x.dtype)
     return dt, wdt
 
 
 def _norm_h(x, residual, h_out):
     """Where x + residual goes (None without a residual)."""
-    import torch
-
     if residual is None:
         if h_out is not None:
             raise ValueError("h_out is for x + residual: there is no residual")
         return None
     if h_out is None:
+        import torch
+
         return torch.empty_like(x)
     _want(h_out, "h_out", x.shape, x.dtype)
     return h_out
@@ -781,8 +799,11 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None
     dt, wdt = _norm_args(x, weight, residual)
     rows, cols = x.shape
     dev = _one_device(x, weight, residual, out, h_out)
-    h = _norm_h(x, residual, h_out)
-    y, ydt = _out(out, (rows, cols), y_dtype, dt, dev)
+    h = None if residual is None and h_out is None else _norm_h(x, residual, h_out)
+    if out is None and (y_dtype is None or y_dtype == dt):
+        y, ydt = torch.empty_like(x), dt
+    else:
+        y, ydt = _out(out, (rows, cols), y_dtype, dt, dev)
     _launch(dev, load_library().moe_rms_norm, dt, rows, cols, x.data_ptr(), _addr(residual), _addr(weight), wdt, eps,
             _addr(h), y.data_ptr(), ydt)
     return y if h is None else (y, h)
@@ -798,11 +819,11 @@ def moe_rms_norm_i8(x, weight=None, residual=None, eps=1e-6, codes=None, scales=
     dev = _one_device(x, weight, residual, codes, scales, h_out)
     h = _norm_h(x, residual, h_out)
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
+        codes = torch.empty_like(x, dtype=torch.int8)
     else:
         _want(codes, "codes", (rows, cols), torch.int8)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        scales = x.new_empty(rows, dtype=torch.float32)
     else:
         _want(scales, "scales", (rows,), torch.float32)
     _launch(dev, load_library().moe_rms_norm_i8, dt, rows, cols, x.data_ptr(), _addr(residual), _addr(weight), wdt, eps,
@@ -836,9 +857,12 @@ def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dt
         _want(out, "out", h.shape, h.dtype)
     dw, dwt, ws, nb = None, wdt, None, 0
     if weight is not None and need_dw:
-        dw, dwt = _out(dw_out, (cols,), dw_dtype, wdt, dev)
+        if dw_out is None and dw_dtype is None:
+            dw = torch.empty_like(weight)
+        else:
+            dw, dwt = _out(dw_out, (cols,), dw_dtype, wdt, dev)
         if workspace is None:
-            workspace = torch.empty(moe_rms_norm_workspace_size(rows, cols), dtype=torch.uint8, device=dev)
+            workspace = h.new_empty(moe_rms_norm_workspace_size(rows, cols), dtype=torch.uint8)
         ws, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif dw_out is not None or dw_dtype is not None:
         raise ValueError("dw_out and dw_dtype are for the weight's gradient: none is asked for")

@@ -3,31 +3,33 @@
 // +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} to v 2^-X, ties to the even code, beyond 6 to 6 (v_cvt_scalef32_pk_fp4_f32: exact,
 // since the scale is a power of two).  A block with an infinity or a NaN gets the scale 255 (NaN) and codes 0.
 //
-// Bound: HBM.  A wave takes 512 values of a row at a time, 8 a lane: four lanes share a block, and its codes and scales
-// leave as 256 and 16 consecutive bytes.
+// Bound: HBM.  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
+// leave as 256 and 16 consecutive bytes.  Large matrices: four windows to a wave, all loaded before the first is used
+// (one at a time: 32 KB in flight on a CU, 4.1 TB/s of reads and writes).
 #include "mx4.h"
 #include "row_core.h"
+#include "tile_core.h"
 
 namespace moe {
 namespace {
 
 constexpr int kMx4Threads = 256, kMx4Window = 512;
 
-// Windows of 512 values, numbered row by row; `turns` consecutive ones to a wave.
-struct Windows {
+// Window number n, counted row by row.
+struct Window {
   int64_t row;
   int win;
-  __device__ __forceinline__ Windows(int64_t first, int per_row) {
-    row = first / per_row;
-    win = (int)(first - row * per_row);
-  }
-  __device__ __forceinline__ void next(int per_row) {
-    if (++win == per_row) {
-      win = 0;
-      ++row;
-    }
-  }
 };
+__device__ __forceinline__ Window window_at(int64_t n, int per_row) {
+  Window w;
+  w.row = n >> 32 ? n / per_row : (uint32_t)n / (uint32_t)per_row;
+  w.win = (int)(n - w.row * per_row);
+  return w;
+}
+__device__ __forceinline__ int64_t first_window(int turns) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  return (((int64_t)blockIdx.y * kGmmGridX + blockIdx.x) * (kMx4Threads / 64) + wave) * turns;
+}
 
 // max over the four lanes of a block
 __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
@@ -37,107 +39,165 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   return o > m ? o : m;
 }
 
+// A lane's 8 values of a block (zeros where there are none): the bits of their largest magnitude, at or above those of
+// infinity for infinities and NaN, and their codes in units of `unit`.
 template <class In, bool kSwiglu>
+struct Block8 {
+  float v[8];
+  __device__ __forceinline__ Block8(const Raw8<In>& x, const Raw8<In>& up, bool some) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = !some ? 0.f : kSwiglu ? swiglu_f32(x[i], up[i]) : x[i];
+  }
+  __device__ __forceinline__ uint32_t top() const { return abs_bits_max(v, 0); }
+  __device__ __forceinline__ uint32_t codes(float unit) const {
+    uint32_t q = 0;
+    static_for<4>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2 * i], v[2 * i + 1], unit, i);
+    });
+    return q;
+  }
+};
+template <>  // bf16 as it is, two to a register
+struct Block8<uint16_t, false> {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  uint32_t u[4];
+  __device__ __forceinline__ Block8(const Raw8<uint16_t>& x, const Raw8<uint16_t>&, bool some) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = some ? x.u[i] : 0;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    u16x2 m = __builtin_bit_cast(u16x2, u[0] & 0x7fff7fffu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, u[i] & 0x7fff7fffu));
+    return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+  }
+  __device__ __forceinline__ uint32_t codes(float unit) const {
+    uint32_t q = 0;
+    static_for<4>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, u[i]), unit, i);
+    });
+    return q;
+  }
+};
+
+template <class In, bool kSwiglu, int kTurns, bool kNt>
 __global__ __launch_bounds__(kMx4Threads) void quantize_mx4_kernel(const In* x, int64_t rows, int cols, int per_row,
-                                                                   int turns, uint8_t* codes, uint8_t* scales) {
+                                                                   uint8_t* codes, uint8_t* scales) {
   const int lane = threadIdx.x & 63;
-  const int64_t wave = ((int64_t)blockIdx.y * kGmmGridX + blockIdx.x) * (kMx4Threads / 64) + (threadIdx.x >> 6);
-  Windows at(wave * turns, per_row);
-  for (int t = 0; t < turns; ++t, at.next(per_row)) {
-    if (at.row >= rows) return;
+  const int64_t n0 = first_window(kTurns), windows = rows * per_row;
+  Raw8<In> raw[kTurns], up[kSwiglu ? kTurns : 1];
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const Window at = window_at(n0 + t, per_row);
     const int c = at.win * kMx4Window + 8 * lane;
-    float v[8] = {};
-    if (c < cols) row_values<In, kSwiglu>(x + at.row * cols * (kSwiglu ? 2 : 1), c, cols, v);
-    const uint32_t m = quad_max(abs_bits_max(v, 0));
+    if (n0 + t < windows && c < cols) {
+      const In* p = x + at.row * cols * (kSwiglu ? 2 : 1) + c;
+      raw[t].template load<kNt>(p);
+      if constexpr (kSwiglu) up[t].template load<kNt>(p + cols);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    if (n0 + t >= windows) return;
+    const Window at = window_at(n0 + t, per_row);
+    const int c = at.win * kMx4Window + 8 * lane;
+    const Block8<In, kSwiglu> v(raw[t], up[kSwiglu ? t : 0], c < cols);
+    const uint32_t m = quad_max(v.top());
     const bool finite = m < 0x7f800000u;
     const uint32_t e = m >> 23, s = e > 2 ? e - 2 : 0;
-    const float unit = __uint_as_float(s ? s << 23 : 0x00400000u);
-    uint32_t q = 0;
-    if (finite) {
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], unit, 0);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], unit, 1);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], unit, 2);
-      q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], unit, 3);
-    }
+    const uint32_t q = finite ? v.codes(__uint_as_float(s ? s << 23 : 0x00400000u)) : 0;
     if (c < cols) __builtin_memcpy(codes + at.row * (cols / 2) + c / 2, &q, 4);
-    if ((lane & 3) == 0)
-      scales[(at.row * per_row + at.win) * 16 + lane / 4] = (uint8_t)(c >= cols ? 0 : finite ? s : 255);
+    if ((lane & 3) == 0) scales[(n0 + t) * 16 + lane / 4] = (uint8_t)(c >= cols ? 0 : finite ? s : 255);
   }
 }
 
-template <class Out>
+template <class Out, int kTurns, bool kNt>
 __global__ __launch_bounds__(kMx4Threads) void dequantize_mx4_kernel(const uint8_t* codes, const uint8_t* scales,
-                                                                     int64_t rows, int cols, int per_row, int turns,
-                                                                     Out* y) {
+                                                                     int64_t rows, int cols, int per_row, Out* y) {
   const int lane = threadIdx.x & 63;
-  const int64_t wave = ((int64_t)blockIdx.y * kGmmGridX + blockIdx.x) * (kMx4Threads / 64) + (threadIdx.x >> 6);
-  Windows at(wave * turns, per_row);
-  for (int t = 0; t < turns; ++t, at.next(per_row)) {
-    if (at.row >= rows) return;
+  const int64_t n0 = first_window(kTurns), windows = rows * per_row;
+  uint32_t codes8[kTurns], scale[kTurns];
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const Window at = window_at(n0 + t, per_row);
     const int c = at.win * kMx4Window + 8 * lane;
-    if (c >= cols) continue;
-    uint32_t q;
-    __builtin_memcpy(&q, codes + at.row * (cols / 2) + c / 2, 4);
-    const uint32_t s = scales[(at.row * per_row + at.win) * 16 + lane / 4];
+    if (n0 + t < windows && c < cols) {
+      __builtin_memcpy(&codes8[t], codes + at.row * (cols / 2) + c / 2, 4);
+      scale[t] = scales[(n0 + t) * 16 + lane / 4];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const Window at = window_at(n0 + t, per_row);
+    const int c = at.win * kMx4Window + 8 * lane;
+    if (n0 + t >= windows || c >= cols) continue;
+    const uint32_t q = codes8[t], s = scale[t];
     const float unit = __uint_as_float(s == 255 ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {  // e2m1 -> fp32: exponent field 0 is the value m / 2
-      const uint32_t code = q >> (4 * i) & 15, e = code >> 1 & 3, f = code & 1;
-      const float mag = e ? __uint_as_float((126 + e) << 23 | f << 22) : 0.5f * f;
-      v[i] = (code & 8 ? -mag : mag) * unit;
-    }
-    Out* to = y + at.row * cols + c;
-    if constexpr (sizeof(Out) == 2) {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
-      __builtin_memcpy(to, u, 16);
-    } else {
-      __builtin_memcpy(to, v, 32);
-    }
+    float v[8];  // magnitudes exact in fp32, then times the power of two
+    static_for<4>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      const auto two = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, i);
+      v[2 * i] = two[0] * unit;
+      v[2 * i + 1] = two[1] * unit;
+    });
+    Raw8<Out> o;
+    o.round(v);
+    o.template store<kNt>(y + at.row * cols + c);
   }
 }
 
+// Four windows to a wave where that leaves 16 waves for every SIMD.
 struct Mx4Grid {
-  int per_row, turns;
+  int per_row;
+  bool four, nt;
   dim3 grid;
-  Mx4Grid(int64_t rows, int32_t cols) {
+  Mx4Grid(int64_t rows, int32_t cols, int64_t bytes) {
+    nt = bytes >= kStreamBytes;
     per_row = mx4_scale_cols(cols) / 16;
     const int64_t windows = rows * per_row;
-    turns = windows >= (int64_t)1 << 17 ? 4 : 1;
-    const int64_t per = (int64_t)turns * (kMx4Threads / 64);
+    four = nt || windows >= (int64_t)1 << 16;
+    const int64_t per = (four ? 4 : 1) * (kMx4Threads / 64);
     grid = gmm_grid((windows + per - 1) / per);
   }
 };
 
-template <class In>
-void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, bool swiglu, uint8_t* codes, uint8_t* scales,
-              hipStream_t s) {
+template <class In, bool kSwiglu>
+void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
   const In* p = static_cast<const In*>(x);
-  if (swiglu) quantize_mx4_kernel<In, true><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, g.turns, codes, scales);
-  else quantize_mx4_kernel<In, false><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, g.turns, codes, scales);
+  if (g.nt) quantize_mx4_kernel<In, kSwiglu, 4, true><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, codes, scales);
+  else if (g.four) quantize_mx4_kernel<In, kSwiglu, 4, false><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, codes, scales);
+  else quantize_mx4_kernel<In, kSwiglu, 1, false><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, codes, scales);
+}
+
+template <class Out>
+void launch_d(const Mx4Grid& g, const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* y,
+              hipStream_t s) {
+  Out* p = static_cast<Out*>(y);
+  if (g.nt) dequantize_mx4_kernel<Out, 4, true><<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, p);
+  else if (g.four) dequantize_mx4_kernel<Out, 4, false><<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, p);
+  else dequantize_mx4_kernel<Out, 1, false><<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, p);
 }
 
 }  // namespace
 
 hipError_t launch_quantize_mx4(const void* x, bool x_bf16, int64_t rows, int32_t cols, bool swiglu, uint8_t* codes,
                                uint8_t* scales, hipStream_t s) {
-  const Mx4Grid g(rows, cols);
-  if (x_bf16) launch_q<uint16_t>(g, x, rows, cols, swiglu, codes, scales, s);
-  else launch_q<float>(g, x, rows, cols, swiglu, codes, scales, s);
+  const Mx4Grid g(rows, cols, rows * cols * (x_bf16 ? 2 : 4) * (swiglu ? 2 : 1));
+  if (x_bf16) swiglu ? launch_q<uint16_t, true>(g, x, rows, cols, codes, scales, s)
+                     : launch_q<uint16_t, false>(g, x, rows, cols, codes, scales, s);
+  else swiglu ? launch_q<float, true>(g, x, rows, cols, codes, scales, s)
+              : launch_q<float, false>(g, x, rows, cols, codes, scales, s);
   return hipGetLastError();
 }
 
 hipError_t launch_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* y,
                                  bool y_bf16, hipStream_t s) {
-  const Mx4Grid g(rows, cols);
-  if (y_bf16)
-    dequantize_mx4_kernel<<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, g.turns,
-                                                         static_cast<uint16_t*>(y));
-  else
-    dequantize_mx4_kernel<<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, g.turns,
-                                                         static_cast<float*>(y));
+  const Mx4Grid g(rows, cols, rows * cols * (y_bf16 ? 2 : 4));
+  if (y_bf16) launch_d<uint16_t>(g, codes, scales, rows, cols, y, s);
+  else launch_d<float>(g, codes, scales, rows, cols, y, s);
   return hipGetLastError();
 }
 

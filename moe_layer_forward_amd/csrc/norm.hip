@@ -13,30 +13,6 @@
 namespace moe {
 namespace {
 
-// 8 values as loaded; they are widened where they are used, so that nothing waits between the loads of a row.
-template <class T>
-struct Raw8 {
-  uint32_t u[2 * sizeof(T)];
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
-    return __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
-  }
-  __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(u, p, 8 * sizeof(T)); }
-  __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, u, 8 * sizeof(T)); }
-  // from fp32, rounded once
-  __device__ __forceinline__ void round(const float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v[i]);
-    } else {
-      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-      typedef float f32x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        u[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[2 * i], v[2 * i + 1]}, bf16x2));
-    }
-  }
-};
 __device__ __forceinline__ float widened(float v) { return v; }
 __device__ __forceinline__ float widened(uint16_t v) { return bf16_to_f32(v); }
 __device__ __forceinline__ void rounded(float v, float* to) { *to = v; }
@@ -84,7 +60,8 @@ __device__ __forceinline__ V join_lanes(V v, V* part, const Join& join) {
 
 // Lane l has columns 8 l .. 8 l + 7 of every 8 kLanes, and the l-th of the up to 7 that are left behind the row's last
 // whole chunk.
-template <class T, class Out, int kLanes, int kChunks>
+// kNt: 1: x, residual and h with the non-temporal policy, 2: y as well.
+template <class T, class Out, int kLanes, int kChunks, int kNt>
 __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs a) {
   constexpr int kRows = norm_threads(kLanes) / kLanes;  // rows of a work-group
   __shared__ float sums[kLanes / 64];
@@ -101,13 +78,13 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
 #pragma unroll
   for (int j = 0; j < kChunks; ++j) {
     const int c = 8 * (j * kLanes + lane);
-    if (c < whole) raw[j].load(x + c);
+    if (c < whole) raw[j].template load<(kNt > 0)>(x + c);
   }
   if (a.residual) {
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
       const int c = 8 * (j * kLanes + lane);
-      if (c < whole) add[j].load(res + c);
+      if (c < whole) add[j].template load<(kNt > 0)>(res + c);
     }
   }
 #pragma unroll
@@ -134,7 +111,7 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = raw[j][i] + add[j][i];
         raw[j].round(v);
-        raw[j].store(static_cast<T*>(a.h) + at + c);
+        raw[j].template store<(kNt > 0)>(static_cast<T*>(a.h) + at + c);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += raw[j][i] * raw[j][i];
@@ -156,7 +133,7 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
         for (int i = 0; i < 8; ++i) y[i] = raw[j][i] * m * w[j].v[i];
         Raw8<Out> o;
         o.round(y);
-        o.store(out + c);
+        o.template store<(kNt > 1)>(out + c);
       }
     }
     if (has_last) rounded(y_last, out + last);
@@ -197,7 +174,7 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
 // Rows r, r + gridDim.x * kRows, ... of a work-group (kLanes = 64: of each of its waves); dw of its rows stays in
 // registers and leaves once, as row blockIdx.x of part.  kHold: so do the weights, and dh is read ahead; without, both are
 // read where they are used (the weights twice a row, from the cache), for rows that leave no registers for them.
-template <class T, int kLanes, int kChunks, bool kHold>
+template <class T, int kLanes, int kChunks, bool kHold, bool kNt>
 __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(NormGradArgs a) {
   constexpr int kRows = norm_threads(kLanes) / kLanes;
   struct Two {
@@ -241,8 +218,8 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
     for (int j = 0; j < kChunks; ++j) {
       const int c = 8 * (j * kLanes + lane);
       if (c < whole) {
-        dy[j].load(pdy + c);
-        h[j].load(ph + c);
+        dy[j].template load<kNt>(pdy + c);
+        h[j].template load<kNt>(ph + c);
       }
     }
     if constexpr (kHold)
@@ -250,7 +227,7 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
 #pragma unroll
         for (int j = 0; j < kChunks; ++j) {
           const int c = 8 * (j * kLanes + lane);
-          if (c < whole) dh[j].load(pdh + c);
+          if (c < whole) dh[j].template load<kNt>(pdh + c);
         }
       }
     float h2 = 0.f, gh = 0.f, dy_last = 0.f, h_last = 0.f;
@@ -303,13 +280,13 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
         }
         if (a.dh) {
           Raw8<T>& d = dh[kHold ? j : 0];
-          if constexpr (!kHold) d.load(pdh + c);
+          if constexpr (!kHold) d.template load<kNt>(pdh + c);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] += d[i];
         }
         Raw8<T> o;
         o.round(v);
-        o.store(pdx + c);
+        o.template store<kNt>(pdx + c);
       }
     }
     if (has_last) {
@@ -375,24 +352,37 @@ __global__ __launch_bounds__(kJoinThreads) void norm_grad_join_kernel(const floa
 // its share.
 int norm_lanes(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
 
-template <class T, class Out>
+template <class T, class Out, int kNt>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   const int lanes = norm_lanes(a.cols), threads = norm_threads(lanes), per = threads / lanes;
   const dim3 grid = gmm_grid((a.rows + per - 1) / per);
-  if (lanes == 64) rms_norm_kernel<T, Out, 64, 4><<<grid, threads, 0, s>>>(a);
-  else if (lanes == 256) rms_norm_kernel<T, Out, 256, 4><<<grid, threads, 0, s>>>(a);
-  else rms_norm_kernel<T, Out, 1024, 4><<<grid, threads, 0, s>>>(a);
+  if (lanes == 64) rms_norm_kernel<T, Out, 64, 4, kNt><<<grid, threads, 0, s>>>(a);
+  else if (lanes == 256) rms_norm_kernel<T, Out, 256, 4, kNt><<<grid, threads, 0, s>>>(a);
+  else rms_norm_kernel<T, Out, 1024, 4, kNt><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <class T>
+// y with the non-temporal policy only where it could not stay in the cache for what follows.
+template <class T, class Out>
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  const int64_t n = a.rows * a.cols;
+  if constexpr (sizeof(Out) > 1)
+    if (n * (int64_t)sizeof(T) >= kStreamBytes && n * (int64_t)sizeof(Out) >= 2 * kStreamBytes) return launch_norm<T, Out, 2>(a, s);
+  return n * (int64_t)sizeof(T) >= kStreamBytes ? launch_norm<T, Out, 1>(a, s) : launch_norm<T, Out, 0>(a, s);
+}
+
+template <class T, bool kNt>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
   const int lanes = norm_lanes(a.cols), threads = norm_threads(lanes);
   const int grid = norm_grad_parts(a.rows, a.cols);
-  if (lanes == 64) norm_grad_kernel<T, 64, 4, true><<<grid, threads, 0, s>>>(a);
-  else if (lanes == 256) norm_grad_kernel<T, 256, 4, true><<<grid, threads, 0, s>>>(a);
-  else norm_grad_kernel<T, 1024, 4, false><<<grid, threads, 0, s>>>(a);
+  if (lanes == 64) norm_grad_kernel<T, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else if (lanes == 256) norm_grad_kernel<T, 256, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else norm_grad_kernel<T, 1024, 4, false, kNt><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
+}
+template <class T>
+hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
+  return a.rows * a.cols * (int64_t)sizeof(T) >= kStreamBytes ? launch_grad<T, true>(a, s) : launch_grad<T, false>(a, s);
 }
 
 }  // namespace
