@@ -336,7 +336,7 @@ struct GmmSum {
 __host__ __device__ inline int64_t gmm_max_sums(const GmmArgs& a) { return a.G + (a.range_rows ? a.max_rows / a.range_rows : 0); }
 
 // Most row tiles of bm rows that G groups over max_rows rows can have.
-inline int64_t gmm_max_tiles(int64_t max_rows, int G, int bm) {
+__host__ __device__ inline int64_t gmm_max_tiles(int64_t max_rows, int G, int bm) {
   const int64_t full = max_rows / bm + G;
   return full < max_rows ? full : max_rows;
 }

@@ -24,6 +24,7 @@ struct Mx4Args {
   const uint8_t* ws;             // [G, N, mx4_scale_cols(K)]
   void* out;
   int32_t out_bf16;
+  uint8_t* packed = nullptr;     // tile kernel: the scales in the order of its reads (launch_mx4_pack), or null
 };
 // The stream kernel's items, 16 p_blocks rows x 16 q_blocks columns, and the waves that share a sum.
 struct Mx4Stream {
@@ -36,7 +37,8 @@ struct Mx4Plan {
   Mx4Kernel kernel;
   Mx4Stream stream;  // kRing: its p_blocks
   int tile_waves;    // kTile: of a work-group
-  const char* name;
+  const char* name;  // of the kernel
+  bool pack = false; // launch_mx4_pack comes first
 };
 Mx4Plan mx4_plan(const Mx4Args& a, void* workspace);
 // The workspace bytes it needs (decided by sizes alone).
@@ -51,6 +53,9 @@ hipError_t launch_mx4_ring(const Mx4Args& a, int p_blocks, int q_blocks, int per
 int64_t mx4_ring_items(const Mx4Args& a, int p_blocks, int q_blocks);
 hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s);
 int64_t mx4_tile_grid(const Mx4Args& a, int waves);
+// Packs the scales of x and w into a.packed, mx4_packed_bytes of it.
+hipError_t launch_mx4_pack(const Mx4Args& a, int waves, hipStream_t s);
+size_t mx4_packed_bytes(const Mx4Args& a, int waves);
 
 hipError_t launch_quantize_mx4(const void* x, bool x_bf16, int64_t rows, int32_t cols, bool swiglu, uint8_t* codes,
                                uint8_t* scales, hipStream_t s);
