@@ -26,16 +26,16 @@ struct Mx4Args {
   int32_t out_bf16;
   uint8_t* packed = nullptr;     // tile kernel: the scales in the order of its reads (launch_mx4_pack), or null
 };
-// The stream kernel's items, 16 p_blocks rows x 16 q_blocks columns, and the waves that share a sum.
+// The stream kernel's items, 16 p_blocks (1 to 4) rows x 16 q_blocks (1 or 2) columns.
 struct Mx4Stream {
-  int p_blocks, q_blocks, waves;
+  int p_blocks, q_blocks;
 };
 enum class Mx4Kernel { kStream, kRing, kTile };
 // The kernel that a product's sizes call for.
 struct Mx4Plan {
   Mx4Args args;
   Mx4Kernel kernel;
-  Mx4Stream stream;  // kRing: its p_blocks
+  Mx4Stream stream;
   int tile_waves;    // kTile: of a work-group
   const char* name;  // of the kernel
   bool pack = false; // launch_mx4_pack comes first
@@ -48,9 +48,9 @@ bool mx4_grid_ok(const Mx4Args& a);
 hipError_t launch_mx4(const Mx4Plan& p, hipStream_t s);
 hipError_t launch_mx4_stream(const Mx4Args& a, const Mx4Stream& c, hipStream_t s);
 int64_t mx4_stream_grid(const Mx4Args& a, const Mx4Stream& c);
-// Items of 16 p_blocks rows x 64 q_blocks columns; mx4_ring_items of them at most.
-hipError_t launch_mx4_ring(const Mx4Args& a, int p_blocks, int q_blocks, int per_cu, hipStream_t s);
-int64_t mx4_ring_items(const Mx4Args& a, int p_blocks, int q_blocks);
+// Items of 16 rows x 128 columns; mx4_ring_items of them at most.
+hipError_t launch_mx4_ring(const Mx4Args& a, hipStream_t s);
+int64_t mx4_ring_items(const Mx4Args& a);
 hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s);
 int64_t mx4_tile_grid(const Mx4Args& a, int waves);
 // Packs the scales of x and w into a.packed, mx4_packed_bytes of it.

@@ -1,21 +1,26 @@
 // Microscaled 4-bit products for groups of few rows: a stream of weights.
 //
-// Work item = up to 16 NB rows of one group x 64 columns, 16 to each of four waves.  A step is a window of 512 values: 256
-// bytes of every row, whole lines, which go straight to LDS, four rows an instruction: the wave's own 16 rows of weights,
-// its quarter of the token rows, and in one more instruction the 16 bytes of scales of its weight rows and of one block
-// of token rows.  In v_mfma_scale_f32_16x16x128 number t of a step lane l multiplies block 4 (l / 16) + t of row
+// Work item = up to 16 NB rows of one group x 64 QB columns, 16 QB to each of four waves.  A step is a window of 512
+// values: 256 bytes of every row, whole lines, which go straight to LDS, four rows an instruction: the wave's own rows of
+// weights, its quarter of the token rows, and in one more instruction the 16 bytes of scales of its weight rows and of one
+// block of token rows.  In v_mfma_scale_f32_16x16x128 number t of a step lane l multiplies block 4 (l / 16) + t of row
 // l % 16, so that one dword holds its scales, byte t for number t.  Row r keeps that block's 16 bytes at position
 // (4 t + l / 16) ^ r: the rows of one fragment read fall in different banks.
 //
-// Work-groups stay: each takes every 64th item of its XCD's share (neighbours read neighbouring weights), and the loads run
-// kDepth - 1 steps ahead of the products, across the ends of items, so that the stream never stops.  One barrier a step: a
+// Work-groups stay, two to a CU: each takes every 64th item of its XCD's share (neighbours read neighbouring weights), and
+// the loads run ahead of the products, across the ends of items, so that the stream never stops.  One barrier a step: a
 // stage is loaded again when every wave has passed the barrier of the step after it.
+//
+// Bound: HBM.  384 groups, 512 rows, 7168 x 2048: 328 us, 6.8 TB/s of weights (16-row x 64-byte loads into
+// registers: 480, stopping at every item).  Two work-groups of 64 columns, three stages: 346; one of 128, four: 382; 32 or
+// more rows to an item: slower than tiles wherever there are so many.
 #include "mx4_core.h"
 
 namespace moe {
 namespace {
 
 constexpr int kRingWaves = 4;
+constexpr int kRingP = 1, kRingQ = 2, kRingPer = 2;  // NB, QB, work-groups to a CU
 constexpr int kRingRow = 256;  // bytes of a row and step
 
 // QB 16-column blocks to a wave; as many stages as let `per` work-groups run on a CU.
@@ -230,32 +235,16 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
 #endif
 }
 
-template <int NB, int QB>
-void launch_ring(const Mx4Args& a, int per_cu, hipStream_t s) {
-  const int slabs = (a.N + 64 * QB - 1) / (64 * QB);
-  const int64_t items = (mx4_ring_items(a, NB, QB) + kXcds - 1) / kXcds * kXcds, most = 256 * per_cu;
-  const dim3 grid((unsigned)(items < most ? items : most)), block(64 * kRingWaves);
-  if (per_cu == 1) mx4_ring_kernel<NB, QB, 1><<<grid, block, 0, s>>>(a, slabs);
-  else if constexpr (RingShape<NB, QB, 2>::kFit >= 2) mx4_ring_kernel<NB, QB, 2><<<grid, block, 0, s>>>(a, slabs);
-}
-
-template <int NB>
-void launch_ring(const Mx4Args& a, int q_blocks, int per_cu, hipStream_t s) {
-  if (q_blocks == 1) launch_ring<NB, 1>(a, per_cu, s);
-  else launch_ring<NB, 2>(a, per_cu, s);
-}
-
 }  // namespace
 
-int64_t mx4_ring_items(const Mx4Args& a, int p_blocks, int q_blocks) {
-  return gmm_max_tiles(a.max_rows, a.G, 16 * p_blocks) * ((a.N + 64 * q_blocks - 1) / (64 * q_blocks));
+int64_t mx4_ring_items(const Mx4Args& a) {
+  return gmm_max_tiles(a.max_rows, a.G, 16 * kRingP) * ((a.N + 64 * kRingQ - 1) / (64 * kRingQ));
 }
 
-hipError_t launch_mx4_ring(const Mx4Args& a, int p_blocks, int q_blocks, int per_cu, hipStream_t s) {
-  if (p_blocks == 1) launch_ring<1>(a, q_blocks, per_cu, s);
-  else if (p_blocks == 2) launch_ring<2>(a, q_blocks, per_cu, s);
-  else if (p_blocks == 3) launch_ring<3>(a, q_blocks, per_cu, s);
-  else launch_ring<4>(a, q_blocks, per_cu, s);
+hipError_t launch_mx4_ring(const Mx4Args& a, hipStream_t s) {
+  const int64_t items = (mx4_ring_items(a) + kXcds - 1) / kXcds * kXcds, most = 256 * kRingPer;
+  const dim3 grid((unsigned)(items < most ? items : most));
+  mx4_ring_kernel<kRingP, kRingQ, kRingPer><<<grid, 64 * kRingWaves, 0, s>>>(a, (a.N + 64 * kRingQ - 1) / (64 * kRingQ));
   return hipGetLastError();
 }
 

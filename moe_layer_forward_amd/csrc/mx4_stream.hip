@@ -110,18 +110,13 @@ __global__ __launch_bounds__(64 * W, PB * QB > 4 ? 2 : 4) void mx4_stream_kernel
 
 int stream_slabs(const Mx4Args& a, const Mx4Stream& c) { return (a.N + 16 * c.q_blocks - 1) / (16 * c.q_blocks); }
 
-template <int PB, int QB>
+// Eight waves to a sum of 16 columns, four to one of 32: as many registers, and the same time within 2% either way.
+template <int PB>
 void launch_stream(const Mx4Args& a, const Mx4Stream& c, hipStream_t s) {
   const int slabs = stream_slabs(a, c);
   const dim3 grid = gmm_grid(mx4_stream_grid(a, c));
-  if (c.waves == 4) mx4_stream_kernel<PB, QB, 4><<<grid, 64 * 4, 0, s>>>(a, slabs);
-  else mx4_stream_kernel<PB, QB, 8><<<grid, 64 * 8, 0, s>>>(a, slabs);
-}
-
-template <int PB>
-void launch_stream(const Mx4Args& a, const Mx4Stream& c, hipStream_t s) {
-  if (c.q_blocks == 1) launch_stream<PB, 1>(a, c, s);
-  else launch_stream<PB, 2>(a, c, s);
+  if (c.q_blocks == 1) mx4_stream_kernel<PB, 1, 8><<<grid, 64 * 8, 0, s>>>(a, slabs);
+  else mx4_stream_kernel<PB, 2, 4><<<grid, 64 * 4, 0, s>>>(a, slabs);
 }
 
 }  // namespace
