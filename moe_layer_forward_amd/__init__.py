@@ -13,6 +13,7 @@ always-on shared expert, weighted combine ("Kimi K2.5 模型架构深度拆解" 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -451,6 +452,7 @@ def _launch(dev, entry, *args):
             _check(entry(*args, _current[0](index)))
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone, asked before every call of the same sizes
 def moe_matmul_workspace_size(op: int, dtype: int, n_groups: int, max_rows: int, N: int, K: int) -> int:
     n = load_library().moe_matmul_workspace_size(op, dtype, n_groups, max_rows, N, K)
     if n == 0 and moe_last_error():
@@ -831,6 +833,7 @@ def moe_rms_norm_i8(x, weight=None, residual=None, eps=1e-6, codes=None, scales=
     return (codes, scales) if h is None else (codes, scales, h)
 
 
+@functools.lru_cache(maxsize=1024)
 def moe_rms_norm_workspace_size(rows: int, cols: int) -> int:
     n = load_library().moe_rms_norm_workspace_size(rows, cols)
     if n == 0 and moe_last_error():

@@ -349,12 +349,17 @@ __global__ __launch_bounds__(kJoinThreads) void norm_grad_join_kernel(const floa
 }
 
 // Lanes that share a row: few, so that a wave has many loads in flight and no barrier, but enough for a lane to hold
-// its share.
-int norm_lanes(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
+// its share.  The norm of few rows: more lanes, for a shorter way through each (64 rows of 2048: 4.3 us with 64
+// lanes, 3.3 with 256; of 7168: 4.5 with 256, 3.9 with 1024; 1024 rows of 7168: 10.8 and 14.3).
+int grad_lanes(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
+int norm_lanes(int64_t rows, int32_t cols) {
+  const int lanes = grad_lanes(cols);
+  return rows > 512 || cols <= 512 ? lanes : lanes == 64 ? 256 : 1024;
+}
 
 template <class T, class Out, int kNt>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  const int lanes = norm_lanes(a.cols), threads = norm_threads(lanes), per = threads / lanes;
+  const int lanes = norm_lanes(a.rows, a.cols), threads = norm_threads(lanes), per = threads / lanes;
   const dim3 grid = gmm_grid((a.rows + per - 1) / per);
   if (lanes == 64) rms_norm_kernel<T, Out, 64, 4, kNt><<<grid, threads, 0, s>>>(a);
   else if (lanes == 256) rms_norm_kernel<T, Out, 256, 4, kNt><<<grid, threads, 0, s>>>(a);
@@ -373,10 +378,11 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 
 template <class T, bool kNt>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
-  const int lanes = norm_lanes(a.cols), threads = norm_threads(lanes);
+  const int lanes = grad_lanes(a.cols), threads = norm_threads(lanes);
   const int grid = norm_grad_parts(a.rows, a.cols);
   if (lanes == 64) norm_grad_kernel<T, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
   else if (lanes == 256) norm_grad_kernel<T, 256, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else if (a.cols <= 1024 * 8 * 2) norm_grad_kernel<T, 1024, 2, true, kNt><<<grid, threads, 0, s>>>(a);
   else norm_grad_kernel<T, 1024, 4, false, kNt><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -397,9 +403,11 @@ hipError_t launch_rms_norm(const NormArgs& a, NormOut out, hipStream_t s) {
                                  : launch_norm<float, float>(a, s);
 }
 
+// As many work-groups as run at once, two on a CU or one of 1024 lanes: more write more sums and gain nothing (32768 rows of
+// 1024: 49 us with 512, 59 with 1024; 2048 of 16384: 79 with 256, 89 with 512).
 int norm_grad_parts(int64_t rows, int32_t cols) {
-  const int per = norm_threads(norm_lanes(cols)) / norm_lanes(cols);
-  const int64_t most = 512, groups = (rows + per - 1) / per;
+  const int lanes = grad_lanes(cols), per = norm_threads(lanes) / lanes;
+  const int64_t most = lanes == 1024 ? 256 : 512, groups = (rows + per - 1) / per;
   return (int)(groups < most ? groups : most);
 }
 
