@@ -1246,7 +1246,7 @@ int moe_matmul_mx4(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_
   if ((st = check_ws(workspace, workspace_bytes, moe::mx4_workspace(a)))) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const moe::Mx4Plan p = moe::mx4_plan(a, workspace);
-  hipError_t e = p.pack ? timed("matmul_mx4_pack", s, [&] { return moe::launch_mx4_pack(p.args, p.tile_waves, s); })
+  hipError_t e = p.pack ? timed("matmul_mx4_pack", s, [&] { return moe::launch_mx4_pack(p.args, s); })
                         : hipSuccess;
   if (e == hipSuccess) e = timed(p.name, s, [&] { return moe::launch_mx4(p, s); });
   return device_status(e, fn);

@@ -53,9 +53,9 @@ hipError_t launch_mx4_ring(const Mx4Args& a, hipStream_t s);
 int64_t mx4_ring_items(const Mx4Args& a);
 hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s);
 int64_t mx4_tile_grid(const Mx4Args& a, int waves);
-// Packs the scales of x and w into a.packed, mx4_packed_bytes of it.
-hipError_t launch_mx4_pack(const Mx4Args& a, int waves, hipStream_t s);
-size_t mx4_packed_bytes(const Mx4Args& a, int waves);
+// Packs the scales of x and w for work-groups of 8 waves into a.packed, mx4_packed_bytes of it.
+hipError_t launch_mx4_pack(const Mx4Args& a, hipStream_t s);
+size_t mx4_packed_bytes(const Mx4Args& a);
 
 hipError_t launch_quantize_mx4(const void* x, bool x_bf16, int64_t rows, int32_t cols, bool swiglu, uint8_t* codes,
                                uint8_t* scales, hipStream_t s);

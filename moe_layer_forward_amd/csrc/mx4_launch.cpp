@@ -20,11 +20,11 @@ int tile_waves(const Mx4Args& a) {
   return items >= 512 || (items >= 160 && a.K >= 12 * 256) ? 8 : 4;
 }
 
-// Whether the tile kernel's scales are packed first.  The product gains a tenth of its time (about 4 POP/s), the packing
-// takes 4 us and two passes over the scales at 2.5 TB/s: 8192 rows, 18432 x 7168: 565 -> 512 us; 3 groups of 16384 rows,
-// 4096 x 7168: 290 -> 262; 4096 x 4096 x 4096: 40.5 and 40.7; 48 groups of 8192 rows, 2048 x 7168: 133 -> 138.
-bool pack_scales(const Mx4Args& a, int waves) {
-  const double product = 2.0 * (double)a.max_rows * a.N * a.K / 4e15, bytes = 2.0 * (double)mx4_packed_bytes(a, waves);
+// Whether the scales are packed before the 256 x 256 tiles.  The product gains a tenth of its time (about 4 POP/s), the
+// packing takes 4 us and two passes over the scales at 2.5 TB/s: 8192 rows, 18432 x 7168: 565 -> 512 us; 3 groups of 16384
+// rows, 4096 x 7168: 290 -> 262; 4096 x 4096 x 4096: 40.5 and 40.7; 48 groups of 8192 rows, 2048 x 7168: 133 -> 138.
+bool pack_scales(const Mx4Args& a) {
+  const double product = 2.0 * (double)a.max_rows * a.N * a.K / 4e15, bytes = 2.0 * (double)mx4_packed_bytes(a);
   return 0.1 * product > 4e-6 + bytes / 2.5e12;
 }
 
@@ -57,7 +57,7 @@ Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
   if (p.kernel == Mx4Kernel::kTile) {
     p.tile_waves = tile_waves(a);
     p.name = p.tile_waves == 8 ? "matmul_mx4_tile256" : "matmul_mx4_tile128";
-    p.pack = pack_scales(a, p.tile_waves);
+    p.pack = p.tile_waves == 8 && pack_scales(a);
     p.args.packed = p.pack ? static_cast<uint8_t*>(workspace) : nullptr;
   }
   return p;
@@ -65,7 +65,7 @@ Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
 
 size_t mx4_workspace(const Mx4Args& a) {
   const Mx4Plan p = mx4_plan(a, nullptr);
-  return p.pack ? mx4_packed_bytes(a, p.tile_waves) : 0;
+  return p.pack ? mx4_packed_bytes(a) : 0;
 }
 
 bool mx4_grid_ok(const Mx4Args& a) {

@@ -154,8 +154,8 @@ struct Mx4Grid {
   int per_row;
   bool four, nt;
   dim3 grid;
-  Mx4Grid(int64_t rows, int32_t cols, int64_t bytes) {
-    nt = bytes >= kStreamBytes;
+  Mx4Grid(int64_t rows, int32_t cols, bool streams) {
+    nt = streams;
     per_row = mx4_scale_cols(cols) / 16;
     const int64_t windows = rows * per_row;
     four = nt || windows >= (int64_t)1 << 16;
@@ -166,26 +166,32 @@ struct Mx4Grid {
 
 template <class In, bool kSwiglu>
 void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
-  const In* p = static_cast<const In*>(x);
-  if (g.nt) quantize_mx4_kernel<In, kSwiglu, 4, true><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, codes, scales);
-  else if (g.four) quantize_mx4_kernel<In, kSwiglu, 4, false><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, codes, scales);
-  else quantize_mx4_kernel<In, kSwiglu, 1, false><<<g.grid, kMx4Threads, 0, s>>>(p, rows, cols, g.per_row, codes, scales);
+  const auto go = [&](auto kernel) {
+    kernel<<<g.grid, kMx4Threads, 0, s>>>(static_cast<const In*>(x), rows, cols, g.per_row, codes, scales);
+  };
+  if constexpr (sizeof(In) == 2)
+    if (g.nt) return go(quantize_mx4_kernel<In, kSwiglu, 4, true>);
+  if (g.four) go(quantize_mx4_kernel<In, kSwiglu, 4, false>);
+  else go(quantize_mx4_kernel<In, kSwiglu, 1, false>);
 }
 
 template <class Out>
 void launch_d(const Mx4Grid& g, const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* y,
               hipStream_t s) {
-  Out* p = static_cast<Out*>(y);
-  if (g.nt) dequantize_mx4_kernel<Out, 4, true><<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, p);
-  else if (g.four) dequantize_mx4_kernel<Out, 4, false><<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, p);
-  else dequantize_mx4_kernel<Out, 1, false><<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, p);
+  const auto go = [&](auto kernel) {
+    kernel<<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, static_cast<Out*>(y));
+  };
+  if constexpr (sizeof(Out) == 2)
+    if (g.nt) return go(dequantize_mx4_kernel<Out, 4, true>);
+  if (g.four) go(dequantize_mx4_kernel<Out, 4, false>);
+  else go(dequantize_mx4_kernel<Out, 1, false>);
 }
 
 }  // namespace
 
 hipError_t launch_quantize_mx4(const void* x, bool x_bf16, int64_t rows, int32_t cols, bool swiglu, uint8_t* codes,
                                uint8_t* scales, hipStream_t s) {
-  const Mx4Grid g(rows, cols, rows * cols * (x_bf16 ? 2 : 4) * (swiglu ? 2 : 1));
+  const Mx4Grid g(rows, cols, x_bf16 && row_streams<uint16_t>(rows * cols * (swiglu ? 2 : 1)));
   if (x_bf16) swiglu ? launch_q<uint16_t, true>(g, x, rows, cols, codes, scales, s)
                      : launch_q<uint16_t, false>(g, x, rows, cols, codes, scales, s);
   else swiglu ? launch_q<float, true>(g, x, rows, cols, codes, scales, s)
@@ -195,7 +201,7 @@ hipError_t launch_quantize_mx4(const void* x, bool x_bf16, int64_t rows, int32_t
 
 hipError_t launch_dequantize_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* y,
                                  bool y_bf16, hipStream_t s) {
-  const Mx4Grid g(rows, cols, rows * cols * (y_bf16 ? 2 : 4));
+  const Mx4Grid g(rows, cols, y_bf16 && row_streams<uint16_t>(rows * cols));
   if (y_bf16) launch_d<uint16_t>(g, codes, scales, rows, cols, y, s);
   else launch_d<float>(g, codes, scales, rows, cols, y, s);
   return hipGetLastError();

@@ -123,16 +123,8 @@ struct Mx4Scales {
       const u32x2 qs = *reinterpret_cast<const u32x2*>(at + q);
       c.sq[0] = qs[0];
       c.sq[1] = qs[1];
-      uint32_t ps[W / 2];
-      if constexpr (W == 8) {
-        const gmm_u32x4 v = *reinterpret_cast<const gmm_u32x4*>(at + p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ps[i] = v[i];
-      } else {
-        const u32x2 v = *reinterpret_cast<const u32x2*>(at + p);
-        ps[0] = v[0];
-        ps[1] = v[1];
-      }
+      static_assert(W == 8, "a lane's 16 bytes");
+      const gmm_u32x4 ps = *reinterpret_cast<const gmm_u32x4*>(at + p);
 #pragma unroll
       for (int i = 0; i < (NB + 1) / 2; ++i) c.sp[i] = ps[i];
     } else {
@@ -408,9 +400,7 @@ __global__ __launch_bounds__(32 * W) void mx4_pack_kernel(Mx4Args a, int slabs, 
 
 int tile_slabs(const Mx4Args& a, int waves) { return (a.N + 32 * waves - 1) / (32 * waves); }
 
-int64_t pack_places(const Mx4Args& a, int waves) {
-  return gmm_max_tiles(a.max_rows, a.G, 32 * waves) + (int64_t)a.G * tile_slabs(a, waves);
-}
+int64_t pack_places(const Mx4Args& a) { return gmm_max_tiles(a.max_rows, a.G, 256) + (int64_t)a.G * tile_slabs(a, 8); }
 
 }  // namespace
 
@@ -418,23 +408,23 @@ int64_t mx4_tile_grid(const Mx4Args& a, int waves) {
   return gmm_row_grid(a.max_rows, a.G, tile_slabs(a, waves), 32 * waves);
 }
 
-size_t mx4_packed_bytes(const Mx4Args& a, int waves) {
-  return (size_t)pack_places(a, waves) * (mx4_scale_cols(a.K) / 16) * (32 * waves * 16);
+size_t mx4_packed_bytes(const Mx4Args& a) {
+  return (size_t)pack_places(a) * (mx4_scale_cols(a.K) / 16) * kMx4WindowScales<8>;
 }
 
-hipError_t launch_mx4_pack(const Mx4Args& a, int waves, hipStream_t s) {
-  const int windows = mx4_scale_cols(a.K) / 16, slabs = tile_slabs(a, waves);
-  const dim3 grid((unsigned)pack_places(a, waves), (unsigned)((windows + kPackWindows - 1) / kPackWindows));
-  if (waves == 8) mx4_pack_kernel<8><<<grid, 256, 0, s>>>(a, slabs, a.packed);
-  else mx4_pack_kernel<4><<<grid, 128, 0, s>>>(a, slabs, a.packed);
+hipError_t launch_mx4_pack(const Mx4Args& a, hipStream_t s) {
+  const int windows = mx4_scale_cols(a.K) / 16;
+  const dim3 grid((unsigned)pack_places(a), (unsigned)((windows + kPackWindows - 1) / kPackWindows));
+  mx4_pack_kernel<8><<<grid, 256, 0, s>>>(a, tile_slabs(a, 8), a.packed);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s) {
   const dim3 grid = gmm_grid(mx4_tile_grid(a, waves)), block(64 * waves);
   const int slabs = tile_slabs(a, waves);
-  if (waves == 8) a.packed ? mx4_tile_kernel<8, true><<<grid, block, 0, s>>>(a, slabs) : mx4_tile_kernel<8, false><<<grid, block, 0, s>>>(a, slabs);
-  else a.packed ? mx4_tile_kernel<4, true><<<grid, block, 0, s>>>(a, slabs) : mx4_tile_kernel<4, false><<<grid, block, 0, s>>>(a, slabs);
+  if (waves == 4) mx4_tile_kernel<4, false><<<grid, block, 0, s>>>(a, slabs);
+  else if (a.packed) mx4_tile_kernel<8, true><<<grid, block, 0, s>>>(a, slabs);
+  else mx4_tile_kernel<8, false><<<grid, block, 0, s>>>(a, slabs);
   return hipGetLastError();
 }
 

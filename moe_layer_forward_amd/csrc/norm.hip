@@ -367,13 +367,16 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// y with the non-temporal policy only where it could not stay in the cache for what follows.
+// y, which what follows reads, with the non-temporal policy only where the cache could not keep most of it.
 template <class T, class Out>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   const int64_t n = a.rows * a.cols;
-  if constexpr (sizeof(Out) > 1)
-    if (n * (int64_t)sizeof(T) >= kStreamBytes && n * (int64_t)sizeof(Out) >= 2 * kStreamBytes) return launch_norm<T, Out, 2>(a, s);
-  return n * (int64_t)sizeof(T) >= kStreamBytes ? launch_norm<T, Out, 1>(a, s) : launch_norm<T, Out, 0>(a, s);
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(Out) == 2)
+      if (n >= (int64_t)100 << 20) return launch_norm<T, Out, 2>(a, s);
+    if (row_streams<T>(n)) return launch_norm<T, Out, 1>(a, s);
+  }
+  return launch_norm<T, Out, 0>(a, s);
 }
 
 template <class T, bool kNt>
@@ -388,7 +391,9 @@ hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
 }
 template <class T>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
-  return a.rows * a.cols * (int64_t)sizeof(T) >= kStreamBytes ? launch_grad<T, true>(a, s) : launch_grad<T, false>(a, s);
+  if constexpr (sizeof(T) == 2)
+    if (row_streams<T>(a.rows * a.cols)) return launch_grad<T, true>(a, s);
+  return launch_grad<T, false>(a, s);
 }
 
 }  // namespace

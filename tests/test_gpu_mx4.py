@@ -1,6 +1,8 @@
 """Microscaled 4-bit floating point: rows to codes and back, and the grouped product, against float64.
 
 The oracle is numpy on the CPU, written from include/moe.h."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -369,3 +371,105 @@ def test_refusals():
     odd = torch.zeros(4 * 32 + 8, dtype=torch.uint8, device="cuda")[8:].view(4, 32)
     with pytest.raises(moe.MoeError):
         moe.moe_matmul_mx4(odd, xs, wc, ws, off)
+
+
+def test_large_matrices_to_codes_and_back():
+    """Sizes that move with the non-temporal policy, four windows to a wave: the same codes as in parts."""
+    torch = _torch()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(2)
+    for rows, cols, swiglu in ((9001, 4640, False), (6000, 3520, True), (70001, 32, False)):
+        x = torch.randn((rows, cols * (2 if swiglu else 1)), generator=gen, device="cuda").bfloat16()
+        codes, scales = moe.moe_quantize_mx4(x, swiglu=swiglu)
+        for a in range(0, rows, 1000):
+            c, s = moe.moe_quantize_mx4(x[a:a + 1000], swiglu=swiglu)
+            assert torch.equal(codes[a:a + 1000], c) and torch.equal(scales[a:a + 1000], s)
+        if not swiglu:
+            c, s = _oracle_quantize(x[-300:].double().cpu().numpy())
+            assert (_unpack(codes[-300:]) == c).all() and (scales[-300:, :cols // 32].cpu().numpy() == s).all()
+        y = moe.moe_dequantize_mx4(codes, scales)
+        for a in range(0, rows, 1000):
+            assert torch.equal(y[a:a + 1000], moe.moe_dequantize_mx4(codes[a:a + 1000], scales[a:a + 1000]))
+        assert (y[-300:].double().cpu().numpy() == _values(codes[-300:], scales[-300:])).all()
+
+
+def _exact_product(sizes, N, K, index_rows=0, seed=1):
+    """Products of whole quarters: every sum is held by fp32, so that any kernel and order has to give it exactly."""
+    torch = _torch()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    rows, G = sum(sizes), len(sizes)
+    x_rows = index_rows or rows
+    xc = torch.randint(0, 256, (x_rows, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    wc = torch.randint(0, 256, (G, N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    xs = torch.randint(126, 129, (x_rows, moe.mx4_scale_cols(K)), generator=gen, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(126, 129, (G, N, moe.mx4_scale_cols(K)), generator=gen, device="cuda", dtype=torch.uint8)
+    index = torch.randint(0, x_rows, (rows,), generator=gen, device="cuda", dtype=torch.int32) if index_rows else None
+    out = torch.full((rows + 5, N), 9.0, device="cuda")
+    full = torch.cat([index, index[:5]]) if index_rows else None
+    if not index_rows:
+        xc, xs = torch.cat([xc, xc[:5]]), torch.cat([xs, xs[:5]])
+    y = moe.moe_matmul_mx4(xc, xs, wc, ws, _offsets(sizes), row_index=full, out=out)
+    assert bool((y[rows:] == 9).all())
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], device="cuda")
+    grid = torch.cat([grid, -grid])
+
+    def values(c, s):
+        v = grid[torch.stack([c & 15, c >> 4], dim=-1).int()].view(*c.shape[:-1], K // 32, 32)
+        return (v * (2.0 * s[..., :K // 32].eq(128) + s[..., :K // 32].eq(127) + 0.5 * s[..., :K // 32].eq(126))[..., None]).view(*c.shape[:-1], K)
+
+    x = values(xc, xs)
+    x = x[full.long()] if index_rows else x
+    at = 0
+    for g, n in enumerate(sizes):
+        if n:
+            ref = x[at:at + n].double() @ values(wc[g], ws[g]).double().T
+            assert torch.equal(y[at:at + n].double(), ref), g
+        at += n
+
+
+@pytest.mark.parametrize("sizes,N,K,index_rows", [
+    ([8192], 4608, 4096, 0),                       # 256 x 256 tiles, packed scales
+    ([6111], 5103, 6176, 700),                     # the same, gathered, odd sizes, the last window's padding
+    ([3000, 0, 2500, 2777], 5120, 6048, 0),        # several groups packed
+    ([2048], 8192, 7168, 0),
+    ([5000], 2048, 1056, 0),                       # 128 x 128 tiles, few of them
+    ([40000], 320, 1504, 0),                       # 128 x 128 tiles by the columns' padding, many row tiles
+    ([100] * 40, 1100, 992, 0),                    # 128 x 128 tiles of groups
+    ([200, 0, 300, 17, 1] * 9, 1000, 1024, 999),   # 256 x 256 tiles of groups, gathered
+    ([3, 0, 12, 1, 1, 7] * 40, 900, 1184, 0),      # the ring over groups of few rows
+    ([1] * 300 + [0] * 300 + [30] * 100, 520, 544, 50),  # more than 512 groups, gathered
+    ([5, 0, 2], 640, 6016, 0),                     # the stream kernel over groups
+    ([7], 1025, 9216, 0), ([33], 5125, 4096, 0), ([20], 8200, 2080, 31), ([64], 5120, 1024, 0), ([50], 130, 8192, 0),
+    ([64], 18432, 1024, 0),
+])
+def test_exact_sums_on_every_kernel(sizes, N, K, index_rows):
+    _exact_product(sizes, N, K, index_rows)
+
+
+def test_the_kernels_that_sizes_call_for():
+    """The names the profile reports (include/moe.h), so that the cases above reach every kernel."""
+    torch = _torch()
+    hip = ctypes.CDLL("libamdhip64.so")
+    events = (ctypes.c_void_p * 8)()
+    for i in range(8):
+        e = ctypes.c_void_p()
+        assert hip.hipEventCreate(ctypes.byref(e)) == 0
+        events[i] = e
+    try:
+        for sizes, N, K, want in (([8192], 4608, 4096, ["matmul_mx4_pack", "matmul_mx4_tile256"]), ([6111], 5103, 6176, ["matmul_mx4_pack", "matmul_mx4_tile256"]),
+                                  ([3000, 0, 2500, 2777], 5120, 6048, ["matmul_mx4_pack", "matmul_mx4_tile256"]), ([40000], 320, 1504, ["matmul_mx4_tile128"]),
+                                  ([300] * 50, 1300, 512, ["matmul_mx4_tile256"]), ([100] * 40, 1100, 992, ["matmul_mx4_tile128"]),
+                                  ([4] * 240, 900, 1184, ["matmul_mx4_ring"]), ([5, 0, 2], 640, 6016, ["matmul_mx4_stream"]),
+                                  ([64], 18432, 1024, ["matmul_mx4_tile128"]), ([64], 640, 1024, ["matmul_mx4_stream"])):
+            xc = torch.zeros((sum(sizes), K // 2), dtype=torch.uint8, device="cuda")
+            xs = torch.zeros((sum(sizes), moe.mx4_scale_cols(K)), dtype=torch.uint8, device="cuda")
+            wc = torch.zeros((len(sizes), N, K // 2), dtype=torch.uint8, device="cuda")
+            ws = torch.zeros((len(sizes), N, moe.mx4_scale_cols(K)), dtype=torch.uint8, device="cuda")
+            moe.moe_profile_events(events, 8)
+            moe.moe_matmul_mx4(xc, xs, wc, ws, _offsets(sizes))
+            torch.cuda.synchronize()
+            got = [moe.moe_profile_kernel(i) for i in range(moe.moe_profile_count())]
+            assert got == want, (sizes[:3], N, K, got)
+    finally:
+        moe.moe_profile_events(None, 0)

@@ -291,3 +291,20 @@ def test_refusals():
         with pytest.raises(moe.MoeError):
             bad()
     assert not np.any(x.cpu().numpy())
+
+
+@pytest.mark.parametrize("rows,cols", [(5300, 7168), (20000, 2048), (8000, 14336)])
+def test_large_matrices(rows, cols):
+    """Sizes that move with the non-temporal policy, y too in the last."""
+    torch = _torch()
+    x, r, w = _randn((rows, cols), "bf16", 1), _randn((rows, cols), "bf16", 2), _randn((cols,), "f32", 3)
+    y, h = moe.moe_rms_norm(x, w, residual=r)
+    assert torch.equal(h, (x.float() + r.float()).bfloat16())
+    ref = _reference(h, w, 1e-6)
+    _check_y(y, ref, "bf16")
+    q, s, h8 = moe.moe_rms_norm_i8(x, w, residual=r)
+    assert torch.equal(h, h8)
+    _check_codes(q, s, ref)
+    del ref, q, s, h8
+    dx, dw = moe.moe_rms_norm_grad(x, h, w, dh=r)
+    _check_grads(dx, dw, x, h, w, r, 1e-6, "bf16", "f32")
