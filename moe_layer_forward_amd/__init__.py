@@ -780,7 +780,27 @@ def _differentiable_norm(*args):
                 return dx if for_x else None, dw, dx if for_r else None, None, None
 
         _norm_node = RmsNorm
-    return _norm_node.apply(*args)
+    held = _graph_leaves(*args[:3])
+    out = _norm_node.apply(*args)
+    del held
+    return out
+
+
+def _graph_leaves(*tensors):
+    """The gradient accumulators of the leaves among the tensors, refused inside a capture where an eager graph that is
+    still alive made them on another stream: the captured backward pass would wait for that stream, which ends the
+    process."""
+    import torch
+
+    stream, nodes = torch.cuda.current_stream().cuda_stream, []
+    for t in tensors:
+        if t is not None and t.requires_grad and t.is_leaf:
+            node = torch.autograd.graph.get_gradient_edge(t).node
+            nodes.append(node)
+            if node.metadata.setdefault("moe_stream", stream) != stream and torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("moe: an eager graph of the same leaves is alive: drop its results before the capture, "
+                                   "or warm up on the capturing stream")
+    return nodes
 
 
 def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None, h_out=None):

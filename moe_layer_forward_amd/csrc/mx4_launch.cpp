@@ -43,7 +43,7 @@ Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
   Mx4Plan p{a, Mx4Kernel::kTile, {1, 1}, 0, "matmul_mx4_stream"};
   if (a.G > 1) {
     const int64_t items = mx4_ring_items(a);
-    if (a.max_rows <= (int64_t)a.G * 12 && items >= 800) {
+    if (a.max_rows <= (int64_t)a.G * 12 && items >= 800 && items <= (int64_t)1 << 30) {
       p.kernel = Mx4Kernel::kRing;
       p.name = "matmul_mx4_ring";
     } else if (a.max_rows <= (int64_t)a.G * 12 && items < 256 && a.K >= 2048) {

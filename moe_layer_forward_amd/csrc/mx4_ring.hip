@@ -179,8 +179,8 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < QB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int turns = (mine * windows + D - 1) / D;
-  for (int turn = 0; turn < turns; ++turn)
+  const int64_t turns = ((int64_t)mine * windows + D - 1) / D;
+  for (int64_t turn = 0; turn < turns; ++turn)
     static_for<D>([&](auto dc) {
       constexpr int d = decltype(dc)::value;
       wait_vmcnt<(D - 2) * S::kLoads>();

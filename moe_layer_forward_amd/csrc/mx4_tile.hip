@@ -327,6 +327,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   Mx4Tiles tiles;
   tiles.count(a, S::kTile);
   if (!gmm_row_item(gmm_block(), tiles.t, slabs, t, slab)) return;
+  if (kPacked && t >= gmm_max_tiles(a.max_rows, a.G, S::kTile)) return;  // offsets that overlap: no place among the packed
   tiles.find(a, S::kTile, t, g, beg, end);
   const int nb = (int)(end - beg + 31) / 32;  // P blocks per wave
 #define MOE_MX4_CASE(N) \
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(32 * W) void mx4_pack_kernel(Mx4Args a, int slabs, 
   if (at < places) {
     Mx4Tiles tiles;
     tiles.count(a, kTile);
-    if (at >= tiles.t.full + tiles.t.partial) return;
+    if (at >= tiles.t.full + tiles.t.partial) return;  // the whole work-group
     int g;
     int64_t beg, end;
     tiles.find(a, kTile, (int)at, g, beg, end);

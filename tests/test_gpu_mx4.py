@@ -473,3 +473,59 @@ def test_the_kernels_that_sizes_call_for():
             assert got == want, (sizes[:3], N, K, got)
     finally:
         moe.moe_profile_events(None, 0)
+
+
+@pytest.mark.parametrize("sizes,N,K", [([9, 1, 4] * 60, 700, 1056), ([6111], 5103, 6176), ([300] * 50, 1300, 544), ([5, 0, 2], 640, 6016)],
+                         ids=["ring", "packed", "tile256", "stream"])
+def test_nan_stays_in_its_row_and_column_on_every_kernel(sizes, N, K):
+    """NaN and padding of 255 in the scales; the other results keep their bits."""
+    torch = _torch()
+    rows, G, blocks = sum(sizes), len(sizes), K // 32
+    xc, xs = moe.moe_quantize_mx4(torch.randn((rows, K), device="cuda"))
+    wc, ws = _weights(G, N, K, 8)
+    want = moe.moe_matmul_mx4(xc, xs, wc, ws, _offsets(sizes))
+    xs[:, blocks:], ws[:, :, blocks:] = 255, 255
+    assert torch.equal(moe.moe_matmul_mx4(xc, xs, wc, ws, _offsets(sizes)), want)
+    last = max(g for g in range(G) if sizes[g])
+    xs[rows - 1, blocks - 1] = 255
+    ws[last, N - 3, blocks // 2] = 255
+    y = moe.moe_matmul_mx4(xc, xs, wc, ws, _offsets(sizes))
+    assert bool(y[rows - 1].isnan().all()) and bool(y[rows - sizes[last]:, N - 3].isnan().all())
+    want[rows - 1] = float("nan")
+    want[rows - sizes[last]:, N - 3] = float("nan")
+    assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.nan_to_num(), want.nan_to_num())
+
+
+def test_past_four_gib():
+    """Weights, rows and results beyond 4 GiB: the last parts are those of small calls."""
+    torch = _torch()
+    K = 4096
+    # 700 groups, 4.9 GB of codes; the last groups' rows
+    sizes = [1] * 700
+    xc, xs = moe.moe_quantize_mx4(torch.randn((700, K), device="cuda"))
+    wc, ws = _weights(700, 3400, K, 1)
+    assert wc.numel() > 1 << 32
+    y = moe.moe_matmul_mx4(xc, xs, wc, ws, _offsets(sizes))
+    part = moe.moe_matmul_mx4(xc[-2:], xs[-2:], wc[-2:], ws[-2:], _offsets([1, 1]), y_dtype=moe.MOE_F32)
+    assert bool(((y[-2:].double() - part.double()).abs() <= 2.0 ** -8 * part.double().abs() + 2.0 ** -18 * part.double().abs().max()).all())
+    del wc, ws, y
+    # 300000 rows of 32768 values: 4.9 GB of codes, 39 GB of bf16
+    x = torch.zeros((300000, 32768), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, 32768), device="cuda").bfloat16()
+    codes, scales = moe.moe_quantize_mx4(x)
+    c, s = moe.moe_quantize_mx4(x[-3:])
+    assert torch.equal(codes[-3:], c) and torch.equal(scales[-3:], s) and not bool(codes[:-3].any())
+    back = moe.moe_dequantize_mx4(codes, scales, out=x)
+    assert torch.equal(back[-3:], moe.moe_dequantize_mx4(c, s)) and not bool(back[:-3].any())
+    del x, back
+    wc, ws = _weights(1, 70, 32768, 3)
+    y = moe.moe_matmul_mx4(codes, scales, wc, ws, y_dtype=moe.MOE_F32)
+    part = moe.moe_matmul_mx4(c, s, wc, ws, y_dtype=moe.MOE_F32)
+    assert not bool(y[:-3].any()) and bool(((y[-3:] - part).abs() <= 2.0 ** -14 * part.abs().max()).all())
+    del codes, scales, y
+    # results of 5.6 GB
+    xc, xs = moe.moe_quantize_mx4(torch.randn((80000, 64), device="cuda"))
+    wc, ws = _weights(1, 17500, 64, 4)
+    y = moe.moe_matmul_mx4(xc, xs, wc, ws, y_dtype=moe.MOE_F32)
+    part = moe.moe_matmul_mx4(xc[-100:], xs[-100:], wc, ws, y_dtype=moe.MOE_F32)
+    assert bool(((y[-100:] - part).abs() <= 2.0 ** -20 * part.abs().max()).all())

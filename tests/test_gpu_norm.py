@@ -308,3 +308,60 @@ def test_large_matrices(rows, cols):
     del ref, q, s, h8
     dx, dw = moe.moe_rms_norm_grad(x, h, w, dh=r)
     _check_grads(dx, dw, x, h, w, r, 1e-6, "bf16", "f32")
+
+
+def test_a_captured_backward_pass():
+    """Forward and backward in one graph, against eager calls; refused while an eager graph of the same leaves lives."""
+    torch = _torch()
+    x, r, w = (_randn(s, t, i).requires_grad_() for i, (s, t) in enumerate((((40, 520), "bf16"), ((40, 520), "bf16"), ((520,), "f32"))))
+    cy, ch = _randn((40, 520), "bf16", 5), _randn((40, 520), "bf16", 6)
+
+    def step():
+        y, h = moe.moe_rms_norm(x, w, residual=r)
+        return torch.autograd.grad((y, h), (x, r, w), (cy, ch))
+
+    alive = moe.moe_rms_norm(x, w, residual=r)
+    with pytest.raises(RuntimeError, match="same leaves"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            torch.zeros(1, device="cuda")
+            moe.moe_rms_norm(x, w, residual=r)
+    del alive
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    for seed in range(4):
+        with torch.no_grad():
+            x.copy_(_randn(x.shape, "bf16", 30 + seed))
+            w.copy_(_randn(w.shape, "f32", 40 + seed))
+            cy.copy_(_randn(cy.shape, "bf16", 50 + seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        h = (x.detach().float() + r.detach().float()).bfloat16()
+        dx, dw = moe.moe_rms_norm_grad(cy, h, w.detach(), dh=ch)
+        assert torch.equal(out[0], dx) and torch.equal(out[1], dx) and torch.equal(out[2], dw)
+
+
+def test_past_four_gib():
+    """The last rows of matrices of 5.6 GB are those of small calls."""
+    torch = _torch()
+    rows, cols = 700000, 4000
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x[-4:] = _randn((4, cols), "bf16", 1)
+    w = _randn((cols,), "bf16", 2)
+    y, h = moe.moe_rms_norm(x, w, residual=x)
+    small_y, small_h = moe.moe_rms_norm(x[-4:], w, residual=x[-4:])
+    assert torch.equal(h[-4:], small_h) and not bool(y[:-4].any())
+    _check_y(y[-4:], _reference(small_h, w, 1e-6), "bf16")
+    _check_y(small_y, _reference(small_h, w, 1e-6), "bf16")
+    q, s = moe.moe_rms_norm_i8(x, w)
+    q2, s2 = moe.moe_rms_norm_i8(x[-4:], w)
+    assert bool((q[-4:].int() - q2.int()).abs().max() <= 1) and torch.allclose(s[-4:], s2, rtol=1e-5) and not bool(q[:-4].any())
+    dx, dw = moe.moe_rms_norm_grad(y, h, w, out=y)
+    small_dx, small_dw = moe.moe_rms_norm_grad(small_y.clone(), small_h, w)
+    assert bool(((dx[-4:].float() - small_dx.float()).abs() <= 0.02 * small_dx.float().abs().max()).all())
+    assert bool(((dw.float() - small_dw.float()).abs() <= 0.01 * small_dw.float().abs() + 1e-3 * small_dw.float().abs().max()).all())
