@@ -38,7 +38,8 @@ struct Mx4Plan {
   Mx4Stream stream;
   int tile_waves;    // kTile: of a work-group
   const char* name;  // of the kernel
-  bool pack = false; // launch_mx4_pack comes first
+  bool pack = false;    // launch_mx4_pack comes first
+  bool stream_w = false;  // kTile: the weights are read past the caches
 };
 Mx4Plan mx4_plan(const Mx4Args& a, void* workspace);
 // The workspace bytes it needs (decided by sizes alone).
@@ -51,7 +52,8 @@ int64_t mx4_stream_grid(const Mx4Args& a, const Mx4Stream& c);
 // Items of 16 rows x 128 columns; mx4_ring_items of them at most.
 hipError_t launch_mx4_ring(const Mx4Args& a, hipStream_t s);
 int64_t mx4_ring_items(const Mx4Args& a);
-hipError_t launch_mx4_tile(const Mx4Args& a, int waves, hipStream_t s);
+// stream: the weights are read past the caches (not with packed scales).
+hipError_t launch_mx4_tile(const Mx4Args& a, int waves, bool stream, hipStream_t s);
 int64_t mx4_tile_grid(const Mx4Args& a, int waves);
 // Packs the scales of x and w for work-groups of 8 waves into a.packed, mx4_packed_bytes of it.
 hipError_t launch_mx4_pack(const Mx4Args& a, hipStream_t s);

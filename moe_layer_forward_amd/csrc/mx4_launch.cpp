@@ -1,5 +1,6 @@
 // Which kernel a microscaled 4-bit product runs on.
 #include <algorithm>
+#include <cmath>
 
 #include "mx4.h"
 
@@ -9,15 +10,23 @@ namespace {
 int64_t padded(int64_t n, int64_t tile) { return (n + tile - 1) / tile * tile; }
 
 // Waves of the tile kernel's work-groups: 8 (256 x 256 tiles, one work-group to a CU) move half the bytes per product
-// through LDS, 4 (128 x 128, two to a CU) pad less and fill the chip with fewer tiles (rules as in gmm_launch.cpp; 8192 x
-// 18432 x 7168: 565 us with 8, 690 with 4; 64 x 18432 x 7168: 25 with 8, 17 with 4).  Groups that mostly fit one row tile
-// of 128 (343 groups of 96 rows, 2624 x 384: 137 us with 8, 126 with 4; 91 of 103, 712 x 4992: 72 and 64; 177 of 142, 1160 x
-// 2528: 117 and 161).
+// through LDS, 4 (128 x 128, two to a CU) pad less, and their rounds are shorter.
+//   * 4 where 256 columns would mostly pad, and for groups that mostly fit one row tile of 128 (343 groups of 96 rows, 2624
+//     x 384: 131 us with 4, 144 with 8; 48 of 64, 2048 x 7168: 73 and 81).
+//   * Otherwise by the rounds over the chip's 256 CUs.  A work-group of 8 takes 1.7 us a step and 5 around them, its last
+//     row tile from half of that; two of 4 on a CU 1.25 a step and 3, one 0.6 of that.  8's rounds are whole ones while there are few.
+//     Within 4% of the better of the two on 193 of 200 sizes drawn.  1024 rows, 18432 x 7168, 288 tiles of 256: 85 us with 4, 104
+//     with 8; 8192 rows: 690 and 500; 8 groups of 512 rows, 2048 x 7168: 39 and 52; 177 of 142, 1160 x 2528: 194 and 118.
 int tile_waves(const Mx4Args& a) {
-  if (padded(a.N, 256) * 100 > padded(a.N, 128) * 115) return 4;
-  if (a.G > 1 && a.max_rows <= (int64_t)a.G * 112) return 4;
-  const int64_t items = mx4_tile_grid(a, 8);
-  return items >= 512 || (items >= 160 && a.K >= 12 * 256) ? 8 : 4;
+  const double rows = (double)a.max_rows / a.G, steps = (a.K + 255) / 256;
+  if (rows <= 0 || padded(a.N, 256) * 100 > padded(a.N, 128) * 115 || (a.G > 1 && rows <= 112)) return 4;
+  const double full = std::floor(rows / 256), part = rows - 256 * full, tiles = part > 0 ? full + 1 : full;
+  const double each = (full + (part > 0 ? 0.5 + part / 512 : 0)) / tiles;
+  double r8 = a.G * tiles * (padded(a.N, 256) / 256) / 256;
+  r8 = r8 <= 3 ? std::ceil(r8) : r8 + 0.5;
+  const double r4 = a.G * std::ceil(rows / 128) * (padded(a.N, 128) / 128) / 512 + 0.15;
+  const double t4 = r4 <= 0.65 ? 0.6 : std::max(1.0, r4);  // one to a CU
+  return t4 * (1.25 * steps + 3) < r8 * each * (1.7 * steps + 5) ? 4 : 8;
 }
 
 // Whether the scales are packed before the 256 x 256 tiles.  The product gains a tenth of its time (about 4 POP/s), the
@@ -26,6 +35,14 @@ int tile_waves(const Mx4Args& a) {
 bool pack_scales(const Mx4Args& a) {
   const double product = 2.0 * (double)a.max_rows * a.N * a.K / 4e15, bytes = 2.0 * (double)mx4_packed_bytes(a);
   return 0.1 * product > 4e-6 + bytes / 2.5e12;
+}
+
+// Whether the tiles read the weights past the caches: more than the last level holds, 256 MB, and few row tiles read
+// each (64 groups of 32 rows, 2048 x 7168, 470 MB: 97 -> 85 us; of 128: 118 -> 102; of 256: 158 -> 147; 48 of 200: 125 ->
+// 115; 4 of 512, 18432 x 7168: 181 -> 177; of 2048: 526 -> 534).  Smaller weights may still be there from a call before
+// (one group of 64 rows, 18432 x 7168, 66 MB: 16.5 -> 20.1, and 22.4 -> 21.5 where they are not).
+bool stream_weights(const Mx4Args& a) {
+  return (int64_t)a.G * a.N * (a.K / 2) > 256000000 && a.max_rows <= (int64_t)a.G * 512;
 }
 
 }  // namespace
@@ -58,6 +75,7 @@ Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
     p.tile_waves = tile_waves(a);
     p.name = p.tile_waves == 8 ? "matmul_mx4_tile256" : "matmul_mx4_tile128";
     p.pack = p.tile_waves == 8 && pack_scales(a);
+    p.stream_w = !p.pack && stream_weights(a);
     p.args.packed = p.pack ? static_cast<uint8_t*>(workspace) : nullptr;
   }
   return p;
@@ -77,7 +95,7 @@ bool mx4_grid_ok(const Mx4Args& a) {
 }
 
 hipError_t launch_mx4(const Mx4Plan& p, hipStream_t s) {
-  if (p.kernel == Mx4Kernel::kTile) return launch_mx4_tile(p.args, p.tile_waves, s);
+  if (p.kernel == Mx4Kernel::kTile) return launch_mx4_tile(p.args, p.tile_waves, p.stream_w, s);
   if (p.kernel == Mx4Kernel::kRing) return launch_mx4_ring(p.args, s);
   return launch_mx4_stream(p.args, p.stream, s);
 }

@@ -436,7 +436,12 @@ def _exact_product(sizes, N, K, index_rows=0, seed=1):
     ([5000], 2048, 1056, 0),                       # 128 x 128 tiles, few of them
     ([40000], 320, 1504, 0),                       # 128 x 128 tiles by the columns' padding, many row tiles
     ([100] * 40, 1100, 992, 0),                    # 128 x 128 tiles of groups
-    ([200, 0, 300, 17, 1] * 9, 1000, 1024, 999),   # 256 x 256 tiles of groups, gathered
+    ([200, 0, 300, 17, 1] * 9, 1000, 1024, 999),   # the same, gathered
+    ([250, 0, 300, 17, 1, 400] * 12, 2048, 1056, 999),  # 256 x 256 tiles of groups, gathered
+    ([130, 0, 257, 300, 5] * 8, 2048, 7168, 0),    # the same, weights read past the caches
+    ([64, 0, 100, 1] * 10, 2048, 7168, 77),        # 128 x 128 tiles, the same
+    ([150, 200] * 300, 512, 544, 0),               # more groups than are sorted
+    ([5, 256, 31, 33, 0, 224, 255, 257, 511, 64, 1, 129] * 3, 1536, 2080, 0),  # every size of partial tile
     ([3, 0, 12, 1, 1, 7] * 40, 900, 1184, 0),      # the ring over groups of few rows
     ([1] * 300 + [0] * 300 + [30] * 100, 520, 544, 50),  # more than 512 groups, gathered
     ([5, 0, 2], 640, 6016, 0),                     # the stream kernel over groups
@@ -459,8 +464,10 @@ def test_the_kernels_that_sizes_call_for():
     try:
         for sizes, N, K, want in (([8192], 4608, 4096, ["matmul_mx4_pack", "matmul_mx4_tile256"]), ([6111], 5103, 6176, ["matmul_mx4_pack", "matmul_mx4_tile256"]),
                                   ([3000, 0, 2500, 2777], 5120, 6048, ["matmul_mx4_pack", "matmul_mx4_tile256"]), ([40000], 320, 1504, ["matmul_mx4_tile128"]),
-                                  ([300] * 50, 1300, 512, ["matmul_mx4_tile256"]), ([100] * 40, 1100, 992, ["matmul_mx4_tile128"]),
-                                  ([4] * 240, 900, 1184, ["matmul_mx4_ring"]), ([5, 0, 2], 640, 6016, ["matmul_mx4_stream"]),
+                                  ([300] * 50, 1300, 512, ["matmul_mx4_tile128"]), ([100] * 40, 1100, 992, ["matmul_mx4_tile128"]),
+                                  ([250, 0, 300, 17, 1, 400] * 12, 2048, 1056, ["matmul_mx4_tile256"]), ([130, 0, 257, 300, 5] * 8, 2048, 7168, ["matmul_mx4_tile256"]),
+                                  ([64, 0, 100, 1] * 10, 2048, 7168, ["matmul_mx4_tile128"]), ([150, 200] * 300, 512, 544, ["matmul_mx4_tile256"]),
+                                  ([1024], 18432, 1024, ["matmul_mx4_tile128"]), ([4] * 240, 900, 1184, ["matmul_mx4_ring"]), ([5, 0, 2], 640, 6016, ["matmul_mx4_stream"]),
                                   ([64], 18432, 1024, ["matmul_mx4_tile128"]), ([64], 640, 1024, ["matmul_mx4_stream"])):
             xc = torch.zeros((sum(sizes), K // 2), dtype=torch.uint8, device="cuda")
             xs = torch.zeros((sum(sizes), moe.mx4_scale_cols(K)), dtype=torch.uint8, device="cuda")
@@ -475,8 +482,8 @@ def test_the_kernels_that_sizes_call_for():
         moe.moe_profile_events(None, 0)
 
 
-@pytest.mark.parametrize("sizes,N,K", [([9, 1, 4] * 60, 700, 1056), ([6111], 5103, 6176), ([300] * 50, 1300, 544), ([5, 0, 2], 640, 6016)],
-                         ids=["ring", "packed", "tile256", "stream"])
+@pytest.mark.parametrize("sizes,N,K", [([9, 1, 4] * 60, 700, 1056), ([6111], 5103, 6176), ([300] * 50, 1300, 544), ([250, 0, 300, 17, 1, 400] * 12, 2048, 1056), ([5, 0, 2], 640, 6016)],
+                         ids=["ring", "packed", "tile128", "tile256", "stream"])
 def test_nan_stays_in_its_row_and_column_on_every_kernel(sizes, N, K):
     """NaN and padding of 255 in the scales; the other results keep their bits."""
     torch = _torch()
