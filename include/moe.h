@@ -425,7 +425,9 @@ const char* moe_last_error(void);
  * "gateup_tile", "down_tile", "combine", ...; a grouped product: "matmul_tile256" or
  * "matmul_tile128" by its output tiles, with "_nt" where weights that are read once come with the
  * non-temporal policy, "matmul_any128" or "matmul_any64" for fp32 and for rows that are not whole 16-byte pieces, and
- * "matmul_join" after them where its sums were split). */
+ * "matmul_join" after them where its sums were split; a microscaled one: "matmul_mx4_stream", "matmul_mx4_ring",
+ * "matmul_mx4_tile128" or "matmul_mx4_tile256", before the last "matmul_mx4_pack" where scales are packed;
+ * "quantize_mx4", "dequantize_mx4"; "rms_norm", "rms_norm_i8", "rms_norm_grad" and, with dw, "rms_norm_grad_join"). */
 int moe_profile_events(void* const* events, int32_t n_events);
 int32_t moe_profile_count(void);
 const char* moe_profile_kernel(int32_t i);

@@ -5,7 +5,8 @@
 //
 // Bound: HBM.  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
 // leave as 256 and 16 consecutive bytes.  Large matrices: four windows to a wave, all loaded before the first is used
-// (one at a time: 32 KB in flight on a CU, 4.1 TB/s of reads and writes).
+// (one at a time: 32 KB in flight on a CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3
+// at 18432 x 7168, 53 us; back 22.8 and 48.7).
 #include "mx4.h"
 #include "row_core.h"
 #include "tile_core.h"

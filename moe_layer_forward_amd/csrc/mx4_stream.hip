@@ -7,6 +7,10 @@
 //
 // Work item = up to 16 PB rows of one group x 16 QB columns; the W waves of a work-group take every W-th window each
 // and join their sums in LDS, in a fixed order.
+//
+// Bound: the way of weights through registers: a wave holds one window of both operands and asks for the next when it
+// has multiplied this one, and many waves on a CU cover that.  8 rows, 18432 x 7168 (70 MB with scales): 16.4 us where
+// the weights come from the last-level cache, 18.5 from HBM; 32 rows, 7168 x 18432: 21.5 and 24.2.
 #include "mx4_core.h"
 
 namespace moe {
