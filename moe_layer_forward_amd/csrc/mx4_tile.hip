@@ -176,13 +176,13 @@ __device__ __forceinline__ void mx4_read_first(char* const (&p)[2], const char* 
 }
 
 // Step kt (kt % 4 == D), as gmm_step with these loads:
-//   in the middle: P0(kt + 2) and Q(kt + 2), before them, in every window's last step, the scales of window
-//     (kt + 5) / 4, whose slot the step's own scales have left
-//   at its end: P1(kt + 2)
-// The middle waits for P1(kt), behind which P0(kt + 1), Q(kt + 1) and P1(kt + 1) may be in flight, and in a window's
-// first step the scales that came before them; the end for P0(kt + 1) and Q(kt + 1), behind which P1(kt + 1), P0(kt + 2)
-// and Q(kt + 2) may be, and in a window's last step the scales.  They are read three steps later.  With one block the
-// only meeting waits for everything.  `next`: the window of step kt + 1.
+//   in the middle: P0(kt + 2) and Q(kt + 2)
+//   at its end: P1(kt + 2), and in a window's last step, when the next one's first scales have been read (the compiler
+//     lets no read of the scales' array pass while a load into it is in flight), the scales of window (kt + 5) / 4,
+//     whose slot the step's own scales have left
+// The middle waits for P1(kt), behind which P0(kt + 1), Q(kt + 1) and P1(kt + 1) may be in flight; the end for P0(kt + 1)
+// and Q(kt + 1), behind which P1(kt + 1), P0(kt + 2) and Q(kt + 2) may be; in a window's first step the scales, too.
+// With one block the only meeting waits for everything.  `next`: the window of step kt + 1.
 template <int W, int NB, int D, class LoadP, class LoadQ, class LoadS, class FP, class FQ, class Scales>
 __device__ __forceinline__ void mx4_step(const LoadP (&lp)[2], const LoadQ& lq, const LoadS& ls, int kt,
                                          const Mx4Rings& r, char* next, const FP& fp, const FQ& fq, const Scales& sc, int wave,
@@ -208,19 +208,19 @@ __device__ __forceinline__ void mx4_step(const LoadP (&lp)[2], const LoadQ& lq, 
     if (f == kMid) {
       wait_vmcnt<NB == 1 ? 0 : kGmmQLoads + n0 + n1 + (D == 0 ? kMx4ScaleLoads : 0)>();
       block_sync_lds();
-      if (D == 3) ls.issue((kt + 5) / 4, r.s + (kt / 4 & 1) * kMx4WindowScales<W>, wave);
       lp[0].template issue<n0>(kt + 2, r.p[D % 2][0], wave);
       lq.template issue<kGmmQLoads>(kt + 2, r.q[D % 2], wave);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (f == NF - 2) {
       if (NB > 1) {
-        wait_vmcnt<kGmmQLoads + n0 + n1 + (D == 3 ? kMx4ScaleLoads : 0)>();
+        wait_vmcnt<kGmmQLoads + n0 + n1 + (D == 0 ? kMx4ScaleLoads : 0)>();
         block_sync_lds();
         lp[1].template issue<n1>(kt + 2, r.p[D % 2][1], wave);
         __builtin_amdgcn_sched_barrier(0);
       }
       mx4_read_first<W, NB, (D + 1) % 4>(r.p[(D + 1) % 2], r.q[(D + 1) % 2], next, kt + 1, fp, fq, sc, c);
+      if (D == 3) ls.issue((kt + 5) / 4, r.s + (kt / 4 & 1) * kMx4WindowScales<W>, wave);
     }
     if constexpr (f + 2 < NF) p[f + 2] = gmm_read_p<W, NB>(ps, fp, f + 2);
     constexpr int kk = O::kk(f), i = O::acc(f);
@@ -247,18 +247,18 @@ __device__ __forceinline__ void mx4_loop(const LoadP (&lp)[2], const LoadQ& lq, 
   __builtin_amdgcn_sched_barrier(0);
   lp[1].template issue<n1>(0, r.p[0][1], wave);
   __builtin_amdgcn_sched_barrier(0);
-  ls.issue(1, r.s + kMx4WindowScales<W>, wave);
-  __builtin_amdgcn_sched_barrier(0);
   lp[0].template issue<n0>(1, r.p[1][0], wave);
   __builtin_amdgcn_sched_barrier(0);
   lq.template issue<kGmmQLoads>(1, r.q[1], wave);
   __builtin_amdgcn_sched_barrier(0);
-  wait_vmcnt<kGmmQLoads + n0 + n1 + kMx4ScaleLoads>();
+  wait_vmcnt<kGmmQLoads + n0 + n1>();
   block_sync_lds();
   lp[1].template issue<n1>(1, r.p[1][1], wave);
   __builtin_amdgcn_sched_barrier(0);
   Mx4Carry<NB> c;
   mx4_read_first<W, NB, 0>(r.p[0], r.q[0], r.s, 0, fp, fq, sc, c);
+  ls.issue(1, r.s + kMx4WindowScales<W>, wave);
+  __builtin_amdgcn_sched_barrier(0);
   mx4_step<W, NB, 0>(lp, lq, ls, 0, r, r.s, fp, fq, sc, wave, c, acc);
   const auto window = [&](int step) { return r.s + (step / 4 & 1) * kMx4WindowScales<W>; };
   int kt = 1;
