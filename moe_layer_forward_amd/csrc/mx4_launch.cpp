@@ -47,29 +47,32 @@ bool stream_weights(const Mx4Args& a) {
 
 }  // namespace
 
-// Groups of up to 12 rows on average: the ring, one pass over the weights (340 groups of 12 rows, 1264 x 928: 62 us, tiles
-// 71; 120 of 9, 1736 x 4480: 106 and 117; with 15 rows: 358 groups, 960 x 3008: 178 and 135), where it has 800 items, three
-// for every two of its work-groups (31 groups, 31 rows, 3904 x 1344: 17.7 and 17.0; 19 groups of 12 rows, 2176 x 3520, 561
-// items: 30 and 19).  Few items of long sums: the stream kernel, whose waves share a sum (24 groups of 2 rows, 896 x 5632:
-// 19 us on the ring, 15 on tiles, 13.5).  Otherwise tiles.
-// One group of up to 64 rows: the stream kernel, with 32-column items where 16-column ones would read the rows of x too
-// often and enough of them remain (32 rows, 7168 x 18432: 32 us with 16, 24 with 32; 4096 x 14336: 13.5 and 17.3); from 33
-// rows on tiles where 128 columns still make 72 of them (64 rows, 18432 x 7168: 38 us, 24 on tiles; 7168 x 18432: 34 and
-// 48).
+// Groups of few rows: the ring, one pass over the weights, up to 12 rows on average (340 groups of 12 rows, 1264 x 928: 59 us,
+// tiles 74; 384 of 8, 7168 x 2048: 511 and 585; 120 of 9, 1736 x 4480: 106 and 107; with 15 rows: 358 groups, 960 x 3008: 178
+// and 135), of long sums up to 6 (384 of 4, 2048 x 7168: 443 and 440; of 12: 494 and 461), where it has 800 items, three for
+// every two of its work-groups (31 groups, 31 rows, 3904 x 1344: 17.7 and 17.0; 19 groups of 12 rows, 2176 x 3520, 561 items:
+// 29 and 21).  Long sums and at most 128 tiles: the stream kernel, whose waves share a sum (8 groups of 4 rows, 2048 x 7168:
+// 14.7, tiles 17.4; 24 of 8, 896 x 5632, 168 tiles: 19.7 and 15.7).  Otherwise tiles.
+// One group: the stream kernel up to 8 rows (18432 x 7168: 16.3 us, tiles 15.0 with the weights in the cache, 18.7 and 20.0
+// without; one row 13.9 and 15.0); up to 16 unless 128 columns make 128 tiles (16 rows, 18432 x 7168: 18.0 and 15.1; 12288 x
+// 5120: 10.0 and 11.3); up to 64 unless they make 72 (32 rows, 18432 x 7168: 23.6 and 15.3; 9216 x 4096: 11.7 and 9.4; 8192 x
+// 8192: 12.2 and 16.1; 64 rows, 7168 x 18432: 31 and 33), with 32-column items where 16-column ones would read the rows of x
+// too often and enough of them remain (32 rows, 7168 x 18432: 30 us with 16, 21.5 with 32; 4096 x 14336: 13.5 and 17.3).
 Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
   Mx4Plan p{a, Mx4Kernel::kTile, {1, 1}, 0, "matmul_mx4_stream"};
+  const int64_t rows = a.max_rows, columns = padded(a.N, 128) / 128;
   if (a.G > 1) {
     const int64_t items = mx4_ring_items(a);
-    if (a.max_rows <= (int64_t)a.G * 12 && items >= 800 && items <= (int64_t)1 << 30) {
+    if (rows <= (int64_t)a.G * (a.K < 6144 ? 12 : 6) && items >= 800 && items <= (int64_t)1 << 30) {
       p.kernel = Mx4Kernel::kRing;
       p.name = "matmul_mx4_ring";
-    } else if (a.max_rows <= (int64_t)a.G * 12 && items < 256 && a.K >= 2048) {
+    } else if (rows <= (int64_t)a.G * 12 && a.G * columns <= 128 && a.K >= 2048) {
       p.kernel = Mx4Kernel::kStream;
     }
-  } else if (a.max_rows <= 32 || (a.max_rows <= 64 && a.N < 72 * 128)) {
+  } else if (rows <= 8 || (rows <= 16 && columns < 128) || (rows <= 64 && columns < 72)) {
     p.kernel = Mx4Kernel::kStream;
-    p.stream.p_blocks = (int)std::max<int64_t>(1, (a.max_rows + 15) / 16);
-    p.stream.q_blocks = a.max_rows > 8 && a.N >= 5120 ? 2 : 1;
+    p.stream.p_blocks = (int)std::max<int64_t>(1, (rows + 15) / 16);
+    p.stream.q_blocks = rows > 8 && a.N >= 5120 ? 2 : 1;
   }
   if (p.kernel == Mx4Kernel::kTile) {
     p.tile_waves = tile_waves(a);
