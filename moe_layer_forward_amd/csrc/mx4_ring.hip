@@ -149,7 +149,9 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
 #if defined(__HIP_DEVICE_COMPILE__)
   Mx4Tiles tiles;
   tiles.count(a, 16 * NB);
-  const RingShare share((tiles.t.full + tiles.t.partial) * slabs);
+  constexpr int64_t kMost = (int64_t)1 << 30;  // only offsets that overlap make more
+  const int64_t items = (int64_t)(tiles.t.full + tiles.t.partial) * slabs;
+  const RingShare share((int)(items < kMost ? items : kMost));
   const int mine = share.count();
   if (!mine) return;
   const int wave = gmm_uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, part = lane >> 4;

@@ -26,6 +26,7 @@ __global__ __launch_bounds__(64 * W, PB * QB > 4 ? 2 : 4) void mx4_stream_kernel
   if (!gmm_row_item(gmm_block(), tiles.t, slabs, t0, slab)) return;
   int64_t beg, end;
   tiles.find(a, 16 * PB, t0, g, beg, end);
+  if (beg >= end) return;  // offsets that overlap: more tiles than were counted
   const int wave = gmm_uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, part = lane >> 4;
   const int q0 = slab * 16 * QB, rows = (int)(end - beg), cols = a.N - q0 < 16 * QB ? a.N - q0 : 16 * QB;
   const uint32_t ld = (uint32_t)(a.K / 2), lds = (uint32_t)mx4_scale_cols(a.K);

@@ -373,6 +373,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   if (!mx4_row_item(gmm_block(), tiles.t, slabs, t, slab)) return;
   if (kPacked && t >= gmm_max_tiles(a.max_rows, a.G, S::kTile)) return;  // offsets that overlap: no place among the packed
   tiles.find(a, S::kTile, t, g, beg, end);
+  if (beg >= end) return;  // the same: more tiles than were counted
   // P blocks per wave.  Two at least: with one the loop has one meeting a step, which waits for all that is in flight (32
   // rows, 18432 x 7168: 17.9 us, with two 15.3).
   const int nb = end - beg > 32 ? (int)(end - beg + 31) / 32 : 2;
@@ -412,6 +413,7 @@ __global__ __launch_bounds__(32 * W) void mx4_pack_kernel(Mx4Args a, int slabs, 
     int g;
     int64_t beg, end;
     tiles.find(a, kTile, (int)at, g, beg, end);
+    if (beg >= end) return;
     const int64_t i = beg + (beg + rl < end ? rl : end - beg - 1);
     row = a.xs + (a.row_index ? mx4_gathered(a, i) : i) * lds;
     per = W;  // row 16 (wr + 2 i) + r: scale i of lane r of wave row wr

@@ -312,6 +312,36 @@ def test_another_stream_and_a_captured_graph(rows):
         assert torch.equal(out.isnan(), want.isnan()) and torch.equal(out.nan_to_num(), want.nan_to_num())
 
 
+def test_two_streams_and_two_graphs_of_one_workspace():
+    """Products with packed scales: at once on two streams, and captured twice with the same workspace, replayed in turn."""
+    torch = _torch()
+    x = [moe.moe_quantize_mx4(_rows(8192, 4096, 31 + i)) for i in range(2)]
+    w = [_weights(1, 4608, 4096, 33 + i) for i in range(2)]
+    want = [moe.moe_matmul_mx4(*x[i], *w[i]) for i in range(2)]
+    nbytes = moe.moe_matmul_workspace_size(moe.MOE_MATMUL_MX4, moe.MOE_F32, 1, 8192, 4608, 4096)
+    assert nbytes > 0
+    side = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(3):
+        for i in range(2):
+            with torch.cuda.stream(side[i]):
+                got[i].append(moe.moe_matmul_mx4(*x[i], *w[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    graphs, out = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            out.append(moe.moe_matmul_mx4(*x[i], *w[i], workspace=ws))
+    for _ in range(3):
+        for i in range(2):
+            out[i].fill_(7)
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[i], want[i]) for i in range(2))
+
+
 def test_norm_experts_and_combine_together():
     """A layer as it would be served: residual and norm, routing, experts in this format, combine.  Every stage against
     float64 on the stage before, so that no code depends on a rounding that came earlier."""
