@@ -11,7 +11,7 @@
 //     of steps in the order of the reads, so that a load is 1 KiB of consecutive bytes and one 16-byte and one 8-byte
 //     read bring a lane all scales of a step.
 //   * LDS holds two steps of both operands and two windows of scales: 160 KiB (80 KiB, two work-groups to a CU).
-// What bounds it: 8192 x 18432 x 7168 takes 470 us, 1.6 a step of a work-group: the matrix instructions 1.3 (6.4 POP/s, what
+// What bounds it: 8192 x 18432 x 7168 takes 470 to 490 us, 1.6 a step of a work-group: the matrix instructions 1.3 (6.4 POP/s, what
 // they reach from registers on random data, by power; 0.85 by their clocks), LDS about 1.4 (64 KiB written at 64 bytes a
 // clock, 192 read at 128), the loads alone 0.7.  The same step with weights of its own for every work-group, 64 groups of
 // 256 rows: 2.6.
