@@ -57,7 +57,8 @@ bool stream_weights(const Mx4Args& a) {
 // without; one row 13.9 and 15.0); up to 16 unless 128 columns make 128 tiles (16 rows, 18432 x 7168: 18.0 and 15.1; 12288 x
 // 5120: 10.0 and 11.3); up to 64 unless they make 72 (32 rows, 18432 x 7168: 23.6 and 15.3; 9216 x 4096: 11.7 and 9.4; 8192 x
 // 8192: 12.2 and 16.1; 64 rows, 7168 x 18432: 31 and 33), with 32-column items where 16-column ones would read the rows of x
-// too often and enough of them remain (32 rows, 7168 x 18432: 30 us with 16, 21.5 with 32; 4096 x 14336: 13.5 and 17.3).
+// too often and enough of them remain (32 rows, 7168 x 18432: 30 us with 16, 21.4 with 32; 8 rows: 17.5 and 15.7, one: 14.5 and
+// 14.9; 32 rows, 4096 x 14336: 13.4 and 17.0).
 Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
   Mx4Plan p{a, Mx4Kernel::kTile, {1, 1}, 0, "matmul_mx4_stream"};
   const int64_t rows = a.max_rows, columns = padded(a.N, 128) / 128;
@@ -72,7 +73,7 @@ Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
   } else if (rows <= 8 || (rows <= 16 && columns < 128) || (rows <= 64 && columns < 72)) {
     p.kernel = Mx4Kernel::kStream;
     p.stream.p_blocks = (int)std::max<int64_t>(1, (rows + 15) / 16);
-    p.stream.q_blocks = rows > 8 && a.N >= 5120 ? 2 : 1;
+    p.stream.q_blocks = rows > 4 && a.N >= 5120 ? 2 : 1;
   }
   if (p.kernel == Mx4Kernel::kTile) {
     p.tile_waves = tile_waves(a);

@@ -6,19 +6,22 @@
 // the window's 16 bytes.
 //
 // Work item = up to 16 PB rows of one group x 16 QB columns; the W waves of a work-group take every W-th window each
-// and join their sums in LDS, in a fixed order.
+// and join their sums in LDS, in a fixed order.  (4 or 16 waves: within 2%, and up to 30% slower.)
 //
 // Bound: the way of weights through registers: a wave holds one window of both operands and asks for the next when it
-// has multiplied this one, and many waves on a CU cover that.  8 rows, 18432 x 7168 (70 MB with scales): 16.4 us where
-// the weights come from the last-level cache, 18.5 from HBM; 32 rows, 7168 x 18432: 21.5 and 24.2.
+// has multiplied this one, and many waves on a CU cover that (asking earlier takes registers from other waves: 17.3 us
+// against 13.7 with one row).  18432 x 7168 (70 MB with scales), one row: 13.7 us where the weights come from the last-level
+// cache, 16.3 from HBM; 32 rows, 7168 x 18432: 21.4 and 23.7.
 #include "mx4_core.h"
 
 namespace moe {
 namespace {
 
-template <int PB, int QB, int W>
-__global__ __launch_bounds__(64 * W, PB * QB > 4 ? 2 : 4) void mx4_stream_kernel(Mx4Args a, int slabs) {
-  __shared__ f32x4 sums[W / 2 * PB * QB * 64];
+constexpr int W = 8;  // waves of a work-group
+
+template <int PB, int QB>
+__global__ __launch_bounds__(64 * W, PB * QB >= 4 ? 2 : 4) void mx4_stream_kernel(Mx4Args a, int slabs) {
+  __shared__ f32x4 sums[W * PB * QB * 64];
 #if defined(__HIP_DEVICE_COMPILE__)
   Mx4Tiles tiles;
   tiles.count(a, 16 * PB);
@@ -77,37 +80,17 @@ __global__ __launch_bounds__(64 * W, PB * QB > 4 ? 2 : 4) void mx4_stream_kernel
         for (int i = 0; i < PB; ++i) acc[i][j] = mx4_mfma<0, 0>(w[j][t], qs[j], x[i][t], ps[i], acc[i][j]);
     }
   }
-  // the upper half of the waves to the lower, and again
+  // every block's sums joined by one of the waves, in their order
 #pragma unroll
-  for (int half = W / 2; half > 0; half /= 2) {
-    f32x4* const to = sums + wave % half * PB * QB * 64 + lane;
-    if (wave >= half && wave < 2 * half) {
+  for (int b = 0; b < PB * QB; ++b) sums[(wave * PB * QB + b) * 64 + lane] = acc[b / QB][b % QB];
+  __syncthreads();
+  static_assert(PB * QB <= W, "a block to a wave");
+  if (wave >= PB * QB) return;
+  f32x4 v = sums[wave * 64 + lane];
 #pragma unroll
-      for (int i = 0; i < PB; ++i)
-#pragma unroll
-        for (int j = 0; j < QB; ++j) to[(i * QB + j) * 64] = acc[i][j];
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int i = 0; i < PB; ++i)
-#pragma unroll
-        for (int j = 0; j < QB; ++j) acc[i][j] += to[(i * QB + j) * 64];
-    }
-    __syncthreads();
-  }
-  if (wave) return;
-#pragma unroll
-  for (int i = 0; i < PB; ++i) {
-    const int row = 16 * i + r;
-    if (row < rows) {
-#pragma unroll
-      for (int j = 0; j < QB; ++j) {
-        const int col = 16 * j + 4 * part;
-        if (col < cols) mx4_store4(a.out, a.out_bf16, (beg + row) * a.N + q0 + col, cols - col, acc[i][j]);
-      }
-    }
-  }
+  for (int k = 1; k < W; ++k) v += sums[(k * PB * QB + wave) * 64 + lane];
+  const int row = 16 * (wave / QB) + r, col = 16 * (wave % QB) + 4 * part;
+  if (row < rows && col < cols) mx4_store4(a.out, a.out_bf16, (beg + row) * a.N + q0 + col, cols - col, v);
 #else
   (void)sums;
 #endif
@@ -115,13 +98,12 @@ __global__ __launch_bounds__(64 * W, PB * QB > 4 ? 2 : 4) void mx4_stream_kernel
 
 int stream_slabs(const Mx4Args& a, const Mx4Stream& c) { return (a.N + 16 * c.q_blocks - 1) / (16 * c.q_blocks); }
 
-// Eight waves to a sum of 16 columns, four to one of 32: as many registers, and the same time within 2% either way.
 template <int PB>
 void launch_stream(const Mx4Args& a, const Mx4Stream& c, hipStream_t s) {
   const int slabs = stream_slabs(a, c);
   const dim3 grid = gmm_grid(mx4_stream_grid(a, c));
-  if (c.q_blocks == 1) mx4_stream_kernel<PB, 1, 8><<<grid, 64 * 8, 0, s>>>(a, slabs);
-  else mx4_stream_kernel<PB, 2, 4><<<grid, 64 * 4, 0, s>>>(a, slabs);
+  if (c.q_blocks == 1) mx4_stream_kernel<PB, 1><<<grid, 64 * W, 0, s>>>(a, slabs);
+  else mx4_stream_kernel<PB, 2><<<grid, 64 * W, 0, s>>>(a, slabs);
 }
 
 }  // namespace
