@@ -811,7 +811,8 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None
     h_out may be x or residual, out may be x.
 
     Where an input requires a gradient, y and h have one (moe_rms_norm_grad); what is written to out or h_out has none,
-    as have the results of the calls below."""
+    as have the results of the calls below.  A backward pass can be captured into a graph; torch ends the process where
+    results of eager calls on the same leaves are alive meanwhile, which is refused where they are this function's."""
     import torch
 
     if out is None and h_out is None and torch.is_grad_enabled() and (

@@ -54,7 +54,9 @@ bool stream_weights(const Mx4Args& a) {
 // 29 and 21).  Long sums and at most 128 tiles: the stream kernel, whose waves share a sum (8 groups of 4 rows, 2048 x 7168:
 // 14.7, tiles 17.4; 24 of 8, 896 x 5632, 168 tiles: 19.7 and 15.7).  Otherwise tiles.
 // One group: the stream kernel up to 8 rows (18432 x 7168: 16.3 us, tiles 15.0 with the weights in the cache, 18.7 and 20.0
-// without; one row 13.9 and 15.0); up to 16 unless 128 columns make 128 tiles (16 rows, 18432 x 7168: 18.0 and 15.1; 12288 x
+// without; one row 13.9 and 15.0), or 2 where 128 columns make tiles for 0.7 of the CUs or more, in whole rounds (4 rows,
+// 28672 x 4096, 224 tiles: 13.9 and 11.4, 14.9 and 13.9; 65536 x 4096, 512: 29.2 and 24.1, 31.8 and 27.2; one row 25.9 and
+// 24.1, 28672 x 4096 13.3 and 13.8); up to 16 unless 128 columns make 128 tiles (16 rows, 18432 x 7168: 18.0 and 15.1; 12288 x
 // 5120: 10.0 and 11.3); up to 64 unless they make 72 (32 rows, 18432 x 7168: 23.6 and 15.3; 9216 x 4096: 11.7 and 9.4; 8192 x
 // 8192: 12.2 and 16.1; 64 rows, 7168 x 18432: 31 and 33), with 32-column items where 16-column ones would read the rows of x
 // too often and enough of them remain (32 rows, 7168 x 18432: 30 us with 16, 21.4 with 32; 8 rows: 17.5 and 15.7, one: 14.5 and
@@ -70,7 +72,8 @@ Mx4Plan mx4_plan(const Mx4Args& a, void* workspace) {
     } else if (rows <= (int64_t)a.G * 12 && a.G * columns <= 128 && a.K >= 2048) {
       p.kernel = Mx4Kernel::kStream;
     }
-  } else if (rows <= 8 || (rows <= 16 && columns < 128) || (rows <= 64 && columns < 72)) {
+  } else if (const bool fill = columns * 10 >= padded(columns, 256) * 7;
+             rows <= (fill ? 2 : 8) || (rows <= 16 && columns < 128) || (rows <= 64 && columns < 72)) {
     p.kernel = Mx4Kernel::kStream;
     p.stream.p_blocks = (int)std::max<int64_t>(1, (rows + 15) / 16);
     p.stream.q_blocks = rows > 4 && a.N >= 5120 ? 2 : 1;

@@ -478,7 +478,7 @@ def _exact_product(sizes, N, K, index_rows=0, seed=1):
     ([7], 1025, 9216, 0), ([33], 5125, 4096, 0), ([20], 8200, 2080, 31), ([64], 5120, 1024, 0), ([50], 130, 8192, 0),
     ([64], 18432, 1024, 0),
     ([61], 18432, 2080, 0), ([128], 2048, 7168, 90), ([5, 0, 100, 64, 1], 700, 2336, 0), ([33], 9300, 2272, 0),
-    ([128] * 7, 1100, 2048, 0), ([300], 1500, 2560, 0), ([129, 17, 128], 1024, 16416, 11),
+    ([128] * 7, 1100, 2048, 0), ([5], 28672, 512, 0), ([300], 1500, 2560, 0), ([129, 17, 128], 1024, 16416, 11),
 ])
 def test_exact_sums_on_every_kernel(sizes, N, K, index_rows):
     _exact_product(sizes, N, K, index_rows)
