@@ -5,7 +5,7 @@
 // moe_quantize_rows (row_core.h).
 //
 // Bound: HBM, each value moved once.  A row stays in the registers of the lanes that share it (64, 256 or 1024 of
-// them, chunks of 8 values a lane), from its one load to its last use; every load of a row is issued before the first is
+// them, chunks of 8 values a lane; 16 where rows are short), from its one load to its last use; every load of a row is issued before the first is
 // waited for.  bf16, 7168 columns, with a residual: 8192 rows 77 us (470 MB, 6.1 TB/s; a copy reaches 5.2, reads alone
 // 7.0), in 8 bits 72 (5.7), the gradients of 16384 rows 155 and the join 7 (940 MB, 6.1).  Few rows: the latency of a
 // load, two joins over the lanes and a store, 2.8 us for one row, 3.9 for 64.
@@ -49,7 +49,7 @@ constexpr int norm_threads(int lanes) { return lanes < 256 ? 256 : lanes; }
 template <int kLanes, class V, class Join>
 __device__ __forceinline__ V join_lanes(V v, V* part, const Join& join) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v = join(v, __shfl_xor(v, d, 64));
+  for (int d = (kLanes < 64 ? kLanes : 64) / 2; d > 0; d >>= 1) v = join(v, __shfl_xor(v, d, 64));
   if constexpr (kLanes > 64) {
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -66,11 +66,11 @@ __device__ __forceinline__ V join_lanes(V v, V* part, const Join& join) {
 template <class T, class Out, int kLanes, int kChunks, int kNt>
 __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs a) {
   constexpr int kRows = norm_threads(kLanes) / kLanes;  // rows of a work-group
-  __shared__ float sums[kLanes / 64];
-  [[maybe_unused]] __shared__ int tops[kLanes / 64];
+  __shared__ float sums[(kLanes + 63) / 64];
+  [[maybe_unused]] __shared__ int tops[(kLanes + 63) / 64];
   const int lane = threadIdx.x % kLanes, whole = a.cols / 8 * 8, last = whole + lane;
   const int64_t r = ((int64_t)blockIdx.y * kGmmGridX + blockIdx.x) * kRows + threadIdx.x / kLanes;
-  if (r >= a.rows) return;  // a whole wave or work-group
+  if (r >= a.rows) return;  // all lanes of a row
   const int64_t at = r * a.cols;
   const T* x = static_cast<const T*>(a.x) + at;
   const T* res = static_cast<const T*>(a.residual) + at;
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
   }
 }
 
-// Rows r, r + gridDim.x * kRows, ... of a work-group (kLanes = 64: of each of its waves); dw of its rows stays in
+// Rows r, r + gridDim.x * kRows, ... of a work-group's kRows sets of kLanes lanes; dw of its rows stays in
 // registers and leaves once, as row blockIdx.x of part.  kHold: so do the weights, and dh is read ahead; without, both are
 // read where they are used (the weights twice a row, from the cache), for rows that leave no registers for them.
 template <class T, int kLanes, int kChunks, bool kHold, bool kNt>
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
   struct Two {
     float h2, gh;
   };
-  __shared__ Two sums[2][kLanes / 64];  // of even and odd turns
+  __shared__ Two sums[2][(kLanes + 63) / 64];  // of even and odd turns
   const int lane = threadIdx.x % kLanes, whole = a.cols / 8 * 8, last = whole + lane;
   const bool has_last = last < a.cols;
   RawWeight w[kHold ? kChunks : 1];
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
       }
     }
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
+    for (int d = (kLanes < 64 ? kLanes : 64) / 2; d > 0; d >>= 1) {
       h2 += __shfl_xor(h2, d, 64);
       gh += __shfl_xor(gh, d, 64);
     }
@@ -300,12 +300,12 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
   }
   if (!a.part) return;
   float* part = a.part + (int64_t)blockIdx.x * norm_grad_ld(a.cols);
-  if constexpr (kLanes == 64) {  // the waves' sums, in their order
-    __shared__ float all[kRows][kChunks * 512 + 8];
-    float* mine = all[threadIdx.x / 64];
+  if constexpr (kRows > 1) {  // the sets' sums, in their order
+    __shared__ float all[kRows][kChunks * kLanes * 8 + 8];
+    float* mine = all[threadIdx.x / kLanes];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-      const int c = 8 * (j * 64 + lane);
+      const int c = 8 * (j * kLanes + lane);
       if (c < whole) __builtin_memcpy(mine + c, dw[j], 32);
     }
     if (has_last) mine[last] = dw_last;
@@ -353,9 +353,16 @@ __global__ __launch_bounds__(kJoinThreads) void norm_grad_join_kernel(const floa
 // Lanes that share a row: few, so that a wave has many loads in flight and no barrier, but enough for a lane to hold
 // its share.  The norm of few rows: more lanes, for a shorter way through each (64 rows of 2048: 4.3 us with 64
 // lanes, 3.3 with 256; of 7168: 4.5 with 256, 3.9 with 1024; 1024 rows of 7168: 10.8 and 14.3).
-int grad_lanes(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
+int lanes_of(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
+// Short rows (those of heads, say): 16 lanes, four rows to a wave, where there are many of them (bf16, 262144 rows of 128,
+// 16 and 64 lanes: 23.6 us and 64.8, with 8-bit output 27 and 92, gradients 46 and 148; of 512: 85 and 111, 66 and 110, 134
+// and 192; fp32 of 512: 183 and 183, 118 and 150, 305 and 292; 600 rows of 512: 3.5 and 3.1; 4096 of 512 with a residual: 5.6
+// and 4.8, of 256 4.2 and 4.2).
+bool short_rows(int64_t rows, int32_t cols) { return cols <= 512 && rows > (cols <= 256 ? 512 : 8192); }
+int grad_lanes(int64_t rows, int32_t cols) { return cols <= 512 && rows > 512 ? 16 : lanes_of(cols); }
 int norm_lanes(int64_t rows, int32_t cols) {
-  const int lanes = grad_lanes(cols);
+  const int lanes = lanes_of(cols);
+  if (short_rows(rows, cols)) return 16;
   return rows > 512 || cols <= 512 ? lanes : lanes == 64 ? 256 : 1024;
 }
 
@@ -363,7 +370,8 @@ template <class T, class Out, int kNt>
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   const int lanes = norm_lanes(a.rows, a.cols), threads = norm_threads(lanes), per = threads / lanes;
   const dim3 grid = gmm_grid((a.rows + per - 1) / per);
-  if (lanes == 64) rms_norm_kernel<T, Out, 64, 4, kNt><<<grid, threads, 0, s>>>(a);
+  if (lanes == 16) rms_norm_kernel<T, Out, 16, 4, kNt><<<grid, threads, 0, s>>>(a);
+  else if (lanes == 64) rms_norm_kernel<T, Out, 64, 4, kNt><<<grid, threads, 0, s>>>(a);
   else if (lanes == 256) rms_norm_kernel<T, Out, 256, 4, kNt><<<grid, threads, 0, s>>>(a);
   else rms_norm_kernel<T, Out, 1024, 4, kNt><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
@@ -383,9 +391,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 
 template <class T, bool kNt>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
-  const int lanes = grad_lanes(a.cols), threads = norm_threads(lanes);
+  const int lanes = grad_lanes(a.rows, a.cols), threads = norm_threads(lanes);
   const int grid = norm_grad_parts(a.rows, a.cols);
-  if (lanes == 64) norm_grad_kernel<T, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  if (lanes == 16) norm_grad_kernel<T, 16, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else if (lanes == 64) norm_grad_kernel<T, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
   else if (lanes == 256) norm_grad_kernel<T, 256, 4, true, kNt><<<grid, threads, 0, s>>>(a);
   else if (a.cols <= 1024 * 8 * 2) norm_grad_kernel<T, 1024, 2, true, kNt><<<grid, threads, 0, s>>>(a);
   else norm_grad_kernel<T, 1024, 4, false, kNt><<<grid, threads, 0, s>>>(a);
@@ -413,7 +422,7 @@ hipError_t launch_rms_norm(const NormArgs& a, NormOut out, hipStream_t s) {
 // As many work-groups as run at once, two on a CU or one of 1024 lanes: more write more sums and gain nothing (32768 rows of
 // 1024: 49 us with 512, 59 with 1024; 2048 of 16384: 79 with 256, 89 with 512).
 int norm_grad_parts(int64_t rows, int32_t cols) {
-  const int lanes = grad_lanes(cols), per = norm_threads(lanes) / lanes;
+  const int lanes = grad_lanes(rows, cols), per = norm_threads(lanes) / lanes;
   const int64_t most = lanes == 1024 ? 256 : 512, groups = (rows + per - 1) / per;
   return (int)(groups < most ? groups : most);
 }

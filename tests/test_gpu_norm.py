@@ -71,7 +71,8 @@ def _check_codes(q, s, ref):
     assert bool(((q.double() - t).abs() <= 0.5 + 1e-3).all())
 
 
-@pytest.mark.parametrize("rows,cols", [(2, 300), (1, 7168), (300, 7168), (64, 7168), (4097, 1024), (20000, 136), (3, 20000)])
+@pytest.mark.parametrize("rows,cols", [(2, 300), (1, 7168), (300, 7168), (64, 7168), (4097, 1024), (20000, 136), (3, 20000),
+                                       (9001, 511), (8193, 257), (513, 5), (1111, 128), (700, 256)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_without_residual_or_weight(rows, cols, dt):
     x, w = _randn((rows, cols), dt, rows), _randn((cols,), dt, 7)
@@ -114,6 +115,24 @@ def test_zeros_infinities_and_nan_stay_in_their_row():
     assert not bool(y[1].any()) and not bool(q[1].any()) and float(s[1]) == 0
     assert bool(y[3].isnan().all()) and bool(y[4, 2].isnan()) and not bool(y[4, 3:].any())
     assert bool(s[3:5].isnan().all()) and not bool(q[3:5].any())
+
+
+@pytest.mark.parametrize("rows,cols", [(9001, 511), (515, 200), (1111, 128), (8200, 320), (600, 7)])
+@pytest.mark.parametrize("dt,wdt", [("bf16", "f32"), ("f32", "bf16")])
+def test_many_short_rows(rows, cols, dt, wdt):
+    """With a residual, at any alignment, in place: h and y of a few rows more and of the rows themselves."""
+    torch = _torch()
+    flat = [_randn((rows * cols + 1,), dt, i) for i in range(2)]
+    x, r = (f[1:].view(rows, cols) for f in flat)
+    w = _randn((cols,), wdt, 3)
+    want_h = (x.float() + r.float()).to(x.dtype)
+    ref = _reference(want_h, w, 1e-5)
+    q, s, h = moe.moe_rms_norm_i8(x, w, residual=r, eps=1e-5)
+    assert torch.equal(h, want_h)
+    _check_codes(q, s, ref)
+    y, h = moe.moe_rms_norm(x, w, residual=r, eps=1e-5, out=x, h_out=r)
+    assert y is x and h is r and torch.equal(r, want_h) and float(flat[1][0]) == float(_randn((rows * cols + 1,), dt, 1)[0])
+    _check_y(y, ref, dt)
 
 
 def test_no_rows_and_a_row_of_one():
@@ -165,7 +184,7 @@ def test_gradients(cols, dt, wdt):
         _check_grads(dx, dw, dy, h, w, dh, 1e-5, dt, wdt)
 
 
-@pytest.mark.parametrize("rows,cols", [(5000, 72), (3001, 2048), (2500, 4104), (1500, 10000)])
+@pytest.mark.parametrize("rows,cols", [(5000, 72), (515, 9), (9003, 511), (777, 128), (3001, 2048), (2500, 4104), (1500, 10000)])
 def test_gradients_of_many_rows_are_the_same_every_time(rows, cols):
     torch = _torch()
     dy, h, w = _randn((rows, cols), "bf16", 1), _randn((rows, cols), "bf16", 2), _randn((cols,), "f32", 3)
