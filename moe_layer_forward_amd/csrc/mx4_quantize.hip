@@ -3,7 +3,7 @@
 // +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} to v 2^-X, ties to the even code, beyond 6 to 6 (v_cvt_scalef32_pk_fp4_f32: exact,
 // since the scale is a power of two).  A block with an infinity or a NaN gets the scale 255 (NaN) and codes 0.
 //
-// Bound: HBM.  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
+// Bound: HBM, with SwiGLU its exponential and division (8192 x 7168: 60 us).  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
 // leave as 256 and 16 consecutive bytes.  Large matrices: four windows to a wave, all loaded before the first is used
 // (one at a time: 32 KB in flight on a CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3
 // at 18432 x 7168, 53 us; back 22.8 and 48.7).
@@ -115,6 +115,20 @@ __global__ __launch_bounds__(kMx4Threads) void quantize_mx4_kernel(const In* x, 
   }
 }
 
+// The values of 8 codes of a block with scale s.
+template <class Out>
+__device__ __forceinline__ void decode8(uint32_t q, uint32_t s, Raw8<Out>& o) {
+  const float unit = __uint_as_float(s == 255 ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
+  float v[8];  // magnitudes exact in fp32, then times the power of two
+  static_for<4>([&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    const auto two = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, i);
+    v[2 * i] = two[0] * unit;
+    v[2 * i + 1] = two[1] * unit;
+  });
+  o.round(v);
+}
+
 template <class Out, int kTurns, bool kNt>
 __global__ __launch_bounds__(kMx4Threads) void dequantize_mx4_kernel(const uint8_t* codes, const uint8_t* scales,
                                                                      int64_t rows, int cols, int per_row, Out* y) {
@@ -135,19 +149,57 @@ __global__ __launch_bounds__(kMx4Threads) void dequantize_mx4_kernel(const uint8
     const Window at = window_at(n0 + t, per_row);
     const int c = at.win * kMx4Window + 8 * lane;
     if (n0 + t >= windows || c >= cols) continue;
-    const uint32_t q = codes8[t], s = scale[t];
-    const float unit = __uint_as_float(s == 255 ? 0x7fc00000u : s ? s << 23 : 0x00400000u);
-    float v[8];  // magnitudes exact in fp32, then times the power of two
-    static_for<4>([&](auto ic) {
-      constexpr int i = decltype(ic)::value;
-      const auto two = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, i);
-      v[2 * i] = two[0] * unit;
-      v[2 * i + 1] = two[1] * unit;
-    });
     Raw8<Out> o;
-    o.round(v);
+    decode8(codes8[t], scale[t], o);
     o.template store<kNt>(y + at.row * cols + c);
   }
+}
+
+// Rows of up to 8 L values: L lanes to a row, 64 / L rows to a wave.
+template <class In, bool kSwiglu, int L>
+__global__ __launch_bounds__(kMx4Threads) void quantize_mx4_short_kernel(const In* x, int64_t rows, int cols,
+                                                                         uint8_t* codes, uint8_t* scales) {
+  const int lane = threadIdx.x & 63, part = lane % L, c = 8 * part;
+  const int64_t r = first_window(64 / L) + lane / L;
+  const bool some = r < rows && c < cols;
+  Raw8<In> raw, up;
+  if (some) {
+    const In* p = x + r * cols * (kSwiglu ? 2 : 1) + c;
+    raw.load(p);
+    if constexpr (kSwiglu) up.load(p + cols);
+  }
+  const Block8<In, kSwiglu> v(raw, up, some);
+  const uint32_t m = quad_max(v.top());
+  const bool finite = m < 0x7f800000u;
+  const uint32_t e = m >> 23, s = e > 2 ? e - 2 : 0;
+  const uint32_t q = finite ? v.codes(__uint_as_float(s ? s << 23 : 0x00400000u)) : 0;
+  if (some) __builtin_memcpy(codes + r * (cols / 2) + c / 2, &q, 4);
+  // the row's scales, up to 8 of its 16 bytes, in its first lane
+  const uint32_t byte = !some ? 0 : finite ? s : 255;
+  uint32_t all[2] = {part < 16 ? byte << part / 4 * 8 : 0, part < 16 ? 0 : byte << (part / 4 - 4) * 8};
+#pragma unroll
+  for (int d = 4; d < L; d <<= 1) {
+    all[0] |= __shfl_xor(all[0], d, 64);
+    if constexpr (L > 16) all[1] |= __shfl_xor(all[1], d, 64);
+  }
+  if (part == 0 && r < rows) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<u32x4*>(scales + r * 16) = u32x4{all[0], all[1], 0, 0};
+  }
+}
+
+template <class Out, int L>
+__global__ __launch_bounds__(kMx4Threads) void dequantize_mx4_short_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                           int64_t rows, int cols, Out* y) {
+  const int lane = threadIdx.x & 63, part = lane % L, c = 8 * part;
+  const int64_t r = first_window(64 / L) + lane / L;
+  if (r >= rows || c >= cols) return;
+  uint32_t q;
+  __builtin_memcpy(&q, codes + r * (cols / 2) + c / 2, 4);
+  const uint32_t s = scales[r * 16 + part / 4];
+  Raw8<Out> o;
+  decode8(q, s, o);
+  o.template store<false>(y + r * cols + c);
 }
 
 // Four windows to a wave where that leaves 16 waves for every SIMD.
@@ -165,8 +217,26 @@ struct Mx4Grid {
   }
 };
 
+// Rows of up to 256 values: several to a wave (bf16, 65536 rows of 64: 12.4 -> 3.6 us, back 11.8 -> 3.9; of 256: 12.4 -> 9.1,
+// 13.0 -> 8.4; 262144 of 128: 37.6 -> 15.4; with SwiGLU 65536 of 64: 31.5 -> 6.6).
+constexpr int kMx4Short = 256;
+int short_lanes(int32_t cols) { return cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
+dim3 short_grid(int64_t rows, int lanes) {
+  const int64_t per = kMx4Threads / lanes;
+  return gmm_grid((rows + per - 1) / per);
+}
+
 template <class In, bool kSwiglu>
 void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  if (cols <= kMx4Short) {
+    const int lanes = short_lanes(cols);
+    const auto go = [&](auto kernel) {
+      kernel<<<short_grid(rows, lanes), kMx4Threads, 0, s>>>(static_cast<const In*>(x), rows, cols, codes, scales);
+    };
+    return lanes == 8    ? go(quantize_mx4_short_kernel<In, kSwiglu, 8>)
+           : lanes == 16 ? go(quantize_mx4_short_kernel<In, kSwiglu, 16>)
+                         : go(quantize_mx4_short_kernel<In, kSwiglu, 32>);
+  }
   const auto go = [&](auto kernel) {
     kernel<<<g.grid, kMx4Threads, 0, s>>>(static_cast<const In*>(x), rows, cols, g.per_row, codes, scales);
   };
@@ -179,6 +249,15 @@ void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, uint8
 template <class Out>
 void launch_d(const Mx4Grid& g, const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, void* y,
               hipStream_t s) {
+  if (cols <= kMx4Short) {
+    const int lanes = short_lanes(cols);
+    const auto go = [&](auto kernel) {
+      kernel<<<short_grid(rows, lanes), kMx4Threads, 0, s>>>(codes, scales, rows, cols, static_cast<Out*>(y));
+    };
+    return lanes == 8    ? go(dequantize_mx4_short_kernel<Out, 8>)
+           : lanes == 16 ? go(dequantize_mx4_short_kernel<Out, 16>)
+                         : go(dequantize_mx4_short_kernel<Out, 32>);
+  }
   const auto go = [&](auto kernel) {
     kernel<<<g.grid, kMx4Threads, 0, s>>>(codes, scales, rows, cols, g.per_row, static_cast<Out*>(y));
   };

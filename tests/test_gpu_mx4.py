@@ -57,7 +57,7 @@ def _rows(rows, K, seed, dt="bf16"):
     return torch.from_numpy(x).to("cuda", {"bf16": torch.bfloat16, "f32": torch.float32}[dt])
 
 
-@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (5, 480), (2, 512), (7, 544), (65, 7168), (700, 2048), (40000, 64)])
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 96), (5, 480), (2, 512), (7, 544), (65, 7168), (700, 2048), (40000, 64), (9, 64), (13, 128), (31, 160), (1001, 256), (17, 224), (4099, 32)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_codes_are_those_of_the_formula(rows, K, dt):
     x = _rows(rows, K, rows, dt)
@@ -115,7 +115,7 @@ def test_blocks_with_infinities_nan_and_zeros():
     assert (y[1, 0::2] == 2.0 ** 126).all() and np.isinf(y[1, 1::2]).all()
 
 
-@pytest.mark.parametrize("rows,cols", [(3, 32), (50, 2048), (9, 992)])
+@pytest.mark.parametrize("rows,cols", [(3, 32), (50, 2048), (9, 992), (37, 64), (21, 96), (19, 256)])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_swiglu_before_the_codes(rows, cols, dt):
     """v = SiLU(g) u in fp32 (expf, a sum, a division, two products: 2^-20 relative); a code is the nearest value's but
