@@ -3,7 +3,7 @@
 // +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} to v 2^-X, ties to the even code, beyond 6 to 6 (v_cvt_scalef32_pk_fp4_f32: exact,
 // since the scale is a power of two).  A block with an infinity or a NaN gets the scale 255 (NaN) and codes 0.
 //
-// Bound: HBM, with SwiGLU its exponential and division (8192 x 7168: 60 us).  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
+// Bound: HBM (with SwiGLU 8192 x 7168: 47.7 us, 5.6 TB/s; with expf and a full division 59.8).  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
 // leave as 256 and 16 consecutive bytes.  Large matrices: four windows to a wave, all loaded before the first is used
 // (one at a time: 32 KB in flight on a CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3
 // at 18432 x 7168, 53 us; back 22.8 and 48.7).
@@ -40,6 +40,17 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   return o > m ? o : m;
 }
 
+// g u / (1 + 2^(-g log2 e)) within 8 units of 2^-24: the hardware's power (one unit) of the product's upper part t, times 1 +
+// ln 2 times its lower part, and the hardware's reciprocal (one), scaled so that it stays a normal number.  An infinite power
+// gives 0; infinities and NaN in g or u make the block's largest value one of them.
+__device__ __forceinline__ float swiglu_quick(float g, float u) {
+  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+  const float t = -g * kLog2e, low = __builtin_fmaf(-g, kLog2eLow, __builtin_fmaf(-g, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, kLn2, 1.f);
+  const float r = __builtin_amdgcn_rcpf((1.f + e) * 0x1p-32f) * 0x1p-32f;
+  return g * r * u;
+}
+
 // A lane's 8 values of a block (zeros where there are none): the bits of their largest magnitude, at or above those of
 // infinity for infinities and NaN, and their codes in units of `unit`.
 template <class In, bool kSwiglu>
@@ -47,7 +58,7 @@ struct Block8 {
   float v[8];
   __device__ __forceinline__ Block8(const Raw8<In>& x, const Raw8<In>& up, bool some) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = !some ? 0.f : kSwiglu ? swiglu_f32(x[i], up[i]) : x[i];
+    for (int i = 0; i < 8; ++i) v[i] = !some ? 0.f : kSwiglu ? swiglu_quick(x[i], up[i]) : x[i];
   }
   __device__ __forceinline__ uint32_t top() const { return abs_bits_max(v, 0); }
   __device__ __forceinline__ uint32_t codes(float unit) const {
@@ -218,7 +229,7 @@ struct Mx4Grid {
 };
 
 // Rows of up to 256 values: several to a wave (bf16, 65536 rows of 64: 12.4 -> 3.6 us, back 11.8 -> 3.9; of 256: 12.4 -> 9.1,
-// 13.0 -> 8.4; 262144 of 128: 37.6 -> 15.4; with SwiGLU 65536 of 64: 31.5 -> 6.6).
+// 13.0 -> 8.4; 262144 of 128: 37.6 -> 15.4; with SwiGLU 65536 of 64: 31.5 -> 5.0).
 constexpr int kMx4Short = 256;
 int short_lanes(int32_t cols) { return cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 dim3 short_grid(int64_t rows, int lanes) {

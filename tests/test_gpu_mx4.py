@@ -134,6 +134,31 @@ def test_swiglu_before_the_codes(rows, cols, dt):
     assert ((c == lo[0]) | (c == hi[0]) | ~same).all()
 
 
+def test_swiglu_of_far_gates():
+    """SiLU where its exponential is tiny, huge and past the type's range; infinities and NaN; tiny and huge factors."""
+    torch = _torch()
+    g = np.array([-88.5, -80.25, -64.0, -44.5, -20.0, -1e-3, -1e-30, 1e-30, 0.5, 17.0, 88.0, 89.5, 120.0, 1e4, 1e30])
+    for factor in (1.0, 2.0 ** 60, 2.0 ** -20):
+        x = np.concatenate([np.repeat(g[:, None], 32, axis=1), np.full((len(g), 32), factor)], axis=1).astype(np.float32)
+        codes, scales = moe.moe_quantize_mx4(torch.from_numpy(x).cuda(), swiglu=True)
+        v = x[:, :32].astype(np.float64)
+        v = v / (1 + np.exp(-v)) * factor
+        some = (np.abs(v[:, 0]) < 2.0 ** 127) & (np.abs(v[:, 0]) > 2.0 ** -125)
+        got = _values(codes, scales)
+        # the nearest code of a block of one value in [4, 8) units: within a unit of it below 6, two above
+        assert (np.abs(got - v)[some] <= np.abs(v)[some] * (0.25 + 2.0 ** -20)).all()
+        lo, hi = _oracle_quantize(v * (1 - 2.0 ** -20)), _oracle_quantize(v * (1 + 2.0 ** -20))
+        c, s = _unpack(codes), scales.cpu().numpy()[:, :1]
+        same = lo[1] == hi[1]
+        assert (((c == lo[0]) | (c == hi[0]))[(same & some[:, None])[:, 0]]).all() and ((s == lo[1]) | (s == hi[1]))[some].all()
+    for gate, up, nan in ((-1e4, 1.0, False), (-200.0, -3.0, False), (float("inf"), 1.0, True), (float("nan"), 1.0, True), (1.0, float("inf"), True),
+                          (0.0, float("nan"), True), (0.0, 5.0, False)):
+        x = torch.zeros((1, 64), device="cuda")
+        x[0, 3], x[0, 35] = gate, up
+        codes, scales = moe.moe_quantize_mx4(x, swiglu=True)
+        assert int(scales[0, 0]) == (255 if nan else 0) and not bool((_unpack(codes) & 7).any())
+
+
 def test_rows_that_start_anywhere():
     torch = _torch()
     for t in (torch.bfloat16, torch.float32):
