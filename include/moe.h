@@ -358,7 +358,8 @@ int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_o
  *
  * Rows to this format: a = max |v| over a block, s = max(floor(log2 a) - 2, -127) + 127 (a = 0: 0), each code the
  * nearest to v 2^(127 - s), ties to the even code, beyond 6 to 6.  A block with an infinity or NaN: s = 255, codes 0.
- * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up, and v = SiLU(gate) * up in fp32.
+ * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up, and v = SiLU(gate) * up in fp32, the same
+ * value as in moe_quantize_rows and in the layer's experts.
  *   x of x_dtype (MOE_BF16 or MOE_F32; any alignment); codes [rows, cols / 2], scales [rows, S] out
  * cols a multiple of 32, at most 2^20, rows <= 2^31-1.  No workspace. */
 int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, uint8_t* codes,

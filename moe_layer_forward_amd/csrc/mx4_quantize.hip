@@ -3,10 +3,11 @@
 // +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} to v 2^-X, ties to the even code, beyond 6 to 6 (v_cvt_scalef32_pk_fp4_f32: exact,
 // since the scale is a power of two).  A block with an infinity or a NaN gets the scale 255 (NaN) and codes 0.
 //
-// Bound: HBM (with SwiGLU 8192 x 7168: 47.7 us, 5.6 TB/s; with expf and a full division 59.8).  A wave takes windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales
-// leave as 256 and 16 consecutive bytes.  Large matrices: four windows to a wave, all loaded before the first is used
-// (one at a time: 32 KB in flight on a CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3
-// at 18432 x 7168, 53 us; back 22.8 and 48.7).
+// Bound: HBM (with SwiGLU of bf16 rows the vector unit as well: 8192 x 7168 in 55 us, 4.8 TB/s).  A wave takes windows of
+// 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales leave as 256 and 16 consecutive
+// bytes.  Large matrices: four windows to a wave, all loaded before the first is used (one at a time: 32 KB in flight on a
+// CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3 at 18432 x 7168, 53 us; back 22.8 and
+// 48.7).
 #include "mx4.h"
 #include "row_core.h"
 #include "tile_core.h"
@@ -40,15 +41,27 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   return o > m ? o : m;
 }
 
-// g u / (1 + 2^(-g log2 e)) within 8 units of 2^-24: the hardware's power (one unit) of the product's upper part t, times 1 +
-// ln 2 times its lower part, and the hardware's reciprocal (one), scaled so that it stays a normal number.  An infinite power
-// gives 0; infinities and NaN in g or u make the block's largest value one of them.
-__device__ __forceinline__ float swiglu_quick(float g, float u) {
-  constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
-  const float t = -g * kLog2e, low = __builtin_fmaf(-g, kLog2eLow, __builtin_fmaf(-g, kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(low, kLn2, 1.f);
-  const float r = __builtin_amdgcn_rcpf((1.f + e) * 0x1p-32f) * 0x1p-32f;
-  return g * r * u;
+// v = swiglu_f32(gate, up) bit for bit, with a reciprocal in place of its division: the hardware's is off by a unit at
+// most, and a step of Newton's method in fused multiply-adds rounds it correctly (compared with the division for every
+// fp32 number of [1, 2^126)).  From 2^126 on (gates below -87.3), where it is subnormal, the division itself.  bf16, 8192 x
+// 7168: 55 us, with the division everywhere 66; 8192 x 2048: 16.8 and 20.5.
+template <class In>
+__device__ __forceinline__ void swiglu8(const Raw8<In>& gate, const Raw8<In>& up, float (&v)[8]) {
+  float d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = 1.f + expf(-gate[i]);
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r[i] = __builtin_amdgcn_rcpf(d[i]);
+    r[i] = __builtin_fmaf(__builtin_fmaf(-d[i], r[i], 1.f), r[i], r[i]);
+  }
+  if (__builtin_expect(abs_bits_max(d, 0) >= 0x7e800000u, 0)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = 1.f / d[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = gate[i] * r[i] * up[i];
 }
 
 // A lane's 8 values of a block (zeros where there are none): the bits of their largest magnitude, at or above those of
@@ -57,8 +70,14 @@ template <class In, bool kSwiglu>
 struct Block8 {
   float v[8];
   __device__ __forceinline__ Block8(const Raw8<In>& x, const Raw8<In>& up, bool some) {
+    if constexpr (kSwiglu) {
+      swiglu8(x, up, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = !some ? 0.f : kSwiglu ? swiglu_quick(x[i], up[i]) : x[i];
+      for (int i = 0; i < 8; ++i) v[i] = x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = some ? v[i] : 0.f;
   }
   __device__ __forceinline__ uint32_t top() const { return abs_bits_max(v, 0); }
   __device__ __forceinline__ uint32_t codes(float unit) const {
