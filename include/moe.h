@@ -413,6 +413,12 @@ int moe_rms_norm_grad(int32_t dtype, int64_t rows, int32_t cols, const void* dy,
                       int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/* The same with dy in fp32 whatever dtype is: the gradient of a y that left in fp32, unrounded.  dx may be dy where dtype
+ * is MOE_F32, and dh. */
+int moe_rms_norm_grad_f32(int32_t dtype, int64_t rows, int32_t cols, const float* dy, const void* h, const void* weight,
+                          int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message of the last failed call on this thread ("" if none); valid until the next call. */
 const char* moe_last_error(void);
 

@@ -30,8 +30,8 @@ EXPORTED = ("moe_workspace_size", "moe_route", "moe_permute", "moe_grouped_swigl
             "moe_forward_noalloc", "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8",
             "moe_matmul_workspace_size", "moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw",
             "moe_quantize_rows", "moe_matmul_i8", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_matmul_mx4",
-            "moe_rms_norm", "moe_rms_norm_i8", "moe_rms_norm_workspace_size", "moe_rms_norm_grad", "moe_last_error", "moe_profile_events",
-            "moe_profile_count", "moe_profile_kernel")
+            "moe_rms_norm", "moe_rms_norm_i8", "moe_rms_norm_workspace_size", "moe_rms_norm_grad",
+            "moe_rms_norm_grad_f32", "moe_last_error", "moe_profile_events", "moe_profile_count", "moe_profile_kernel")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20  # the fixed scratch of moe_forward_noalloc (include/moe.h)
 
 
@@ -101,10 +101,11 @@ def load_library():
         lib.moe_rms_norm_i8.argtypes = [i32, i64, i32, vp, vp, vp, i32, f32, vp, vp, vp, vp]
         lib.moe_rms_norm_workspace_size.argtypes = [i64, i32]
         lib.moe_rms_norm_workspace_size.restype = sz
-        lib.moe_rms_norm_grad.argtypes = [i32, i64, i32, vp, vp, vp, i32, f32, vp, vp, vp, i32, vp, sz, vp]
+        for name in ("moe_rms_norm_grad", "moe_rms_norm_grad_f32"):
+            getattr(lib, name).argtypes = [i32, i64, i32, vp, vp, vp, i32, f32, vp, vp, vp, i32, vp, sz, vp]
         for name in ("moe_grouped_matmul", "moe_grouped_matmul_dx", "moe_grouped_matmul_dw", "moe_quantize_rows",
                      "moe_matmul_i8", "moe_quantize_mx4", "moe_dequantize_mx4", "moe_matmul_mx4", "moe_rms_norm",
-                     "moe_rms_norm_i8", "moe_rms_norm_grad"):
+                     "moe_rms_norm_i8", "moe_rms_norm_grad", "moe_rms_norm_grad_f32"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("moe_route", "moe_permute", "moe_grouped_swiglu", "moe_combine", "moe_forward",
                      "moe_forward_routed", "moe_forward_q4", "moe_forward_fp8"):
@@ -774,8 +775,9 @@ def _differentiable_norm(*args):
                 for_x, for_w, for_r = ctx.needs_input_grad[:3]
                 if dy is None:  # only h was used further
                     return dh if for_x else None, None, dh if for_r else None, None, None
-                dy = dy.to(h.dtype).contiguous()  # a float32 y of bfloat16 rows: dy in their type, as torch's casts do
-                dx, dw = moe_rms_norm_grad(dy, h, weight, None if dh is None else dh.contiguous(), ctx.eps,
+                if dy.dtype != torch.float32:  # the gradient of a float32 y stays as it is
+                    dy = dy.to(h.dtype)
+                dx, dw = moe_rms_norm_grad(dy.contiguous(), h, weight, None if dh is None else dh.contiguous(), ctx.eps,
                                            need_dw=for_w)
                 return dx if for_x else None, dw, dx if for_r else None, None, None
 
@@ -864,14 +866,16 @@ def moe_rms_norm_workspace_size(rows: int, cols: int) -> int:
 
 def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dtype=None, workspace=None, out=None,
                       dw_out=None):
-    """Gradients of moe_rms_norm: (dx, dw) from dy (y's gradient), h (what the norm was taken of) and dh (what reaches h
-    past the norm, or None).  dx is the gradient of x and of the residual alike; dw has the weight's type, or dw_dtype,
-    and is None without a weight or with need_dw=False.  out (for dx) may be dy or dh."""
+    """Gradients of moe_rms_norm: (dx, dw) from dy (y's gradient, of h's type or float32), h (what the norm was taken
+    of) and dh (what reaches h past the norm, or None).  dx is the gradient of x and of the residual alike, in h's type;
+    dw has the weight's type, or dw_dtype, and is None without a weight or with need_dw=False.  out (for dx) may be dy (of
+    h's type) or dh."""
     import torch
 
     dt, wdt = _norm_args(h, weight, None, "h")
     rows, cols = h.shape
-    _want(dy, "dy", h.shape, h.dtype)
+    wide = dy.dtype == torch.float32 and dt == MOE_BF16  # the gradient of a float32 y of bfloat16 rows
+    _want(dy, "dy", h.shape, None if wide else h.dtype)
     if dh is not None:
         _want(dh, "dh", h.shape, h.dtype)
     dev = _one_device(dy, h, weight, dh, workspace, out, dw_out)
@@ -890,8 +894,9 @@ def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dt
         ws, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     elif dw_out is not None or dw_dtype is not None:
         raise ValueError("dw_out and dw_dtype are for the weight's gradient: none is asked for")
-    _launch(dev, load_library().moe_rms_norm_grad, dt, rows, cols, dy.data_ptr(), h.data_ptr(), _addr(weight), wdt, eps,
-            _addr(dh), out.data_ptr(), _addr(dw), dwt, ws, nb)
+    lib = load_library()
+    _launch(dev, lib.moe_rms_norm_grad_f32 if wide else lib.moe_rms_norm_grad, dt, rows, cols, dy.data_ptr(),
+            h.data_ptr(), _addr(weight), wdt, eps, _addr(dh), out.data_ptr(), _addr(dw), dwt, ws, nb)
     return out, dw
 
 

@@ -676,6 +676,42 @@ size_t norm_workspace(int64_t rows, int32_t cols) {
   return cv.used;
 }
 
+int run_norm_grad(const char* fn, int32_t dtype, int32_t dy_dtype, int64_t rows, int32_t cols, const void* dy,
+                  const void* h, const void* weight, int32_t w_dtype, float eps, const void* dh, void* dx, void* dw,
+                  int32_t dw_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  prof_reset();
+  int st;
+  if ((st = check_norm(fn, dtype, rows, cols, w_dtype, eps)) || (st = check_dtype(fn, "dw_dtype", dw_dtype))) return st;
+  if (rows == 0 && !dw) return ok();
+  if (rows > 0 && (!dy || !h || !dx)) return fail(MOE_ERR_INVALID_ARG, "%s: dy, h and dx are required", fn);
+  const size_t e = elem_bytes(dtype);
+  if ((st = check_aligned(fn, {{dy, elem_bytes(dy_dtype), "dy"}, {h, e, "h"}, {weight, elem_bytes(w_dtype), "weight"},
+                               {dh, e, "dh"}, {dx, e, "dx"}, {dw, elem_bytes(dw_dtype), "dw"}})))
+    return st;
+  if (dw && (st = check_ws(workspace, workspace_bytes, norm_workspace(rows, cols)))) return st;
+  moe::NormGradArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.w = weight;
+  a.dh = dh;
+  a.dx = dx;
+  a.part = dw ? static_cast<float*>(workspace) : nullptr;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.bf16 = dtype == MOE_BF16;
+  a.w_bf16 = w_dtype == MOE_BF16;
+  a.dy_f32 = a.bf16 && dy_dtype == MOE_F32;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t err = hipSuccess;
+  if (rows > 0) err = timed("rms_norm_grad", s, [&] { return moe::launch_norm_grad(a, s); });
+  if (err == hipSuccess && dw)
+    err = timed("rms_norm_grad_join", s, [&] {
+      return moe::launch_norm_grad_join(a.part, moe::norm_grad_parts(rows, cols), cols, dw, dw_dtype == MOE_BF16, s);
+    });
+  return device_status(err, fn);
+}
+
 // ----------------------------------------------------------------------------- no-allocation forward
 // Scratch of moe_forward_noalloc: a file-scope device array that every GPU the library runs on holds
 // (its own copy, at its own address) until the process ends.  In host code `scratch` names a host
@@ -1275,37 +1311,15 @@ size_t moe_rms_norm_workspace_size(int64_t rows, int32_t cols) {
 int moe_rms_norm_grad(int32_t dtype, int64_t rows, int32_t cols, const void* dy, const void* h, const void* weight,
                       int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype, void* workspace,
                       size_t workspace_bytes, void* stream) {
-  prof_reset();
-  const char* fn = "moe_rms_norm_grad";
-  int st;
-  if ((st = check_norm(fn, dtype, rows, cols, w_dtype, eps)) || (st = check_dtype(fn, "dw_dtype", dw_dtype))) return st;
-  if (rows == 0 && !dw) return ok();
-  if (rows > 0 && (!dy || !h || !dx)) return fail(MOE_ERR_INVALID_ARG, "%s: dy, h and dx are required", fn);
-  const size_t e = elem_bytes(dtype);
-  if ((st = check_aligned(fn, {{dy, e, "dy"}, {h, e, "h"}, {weight, elem_bytes(w_dtype), "weight"}, {dh, e, "dh"},
-                               {dx, e, "dx"}, {dw, elem_bytes(dw_dtype), "dw"}})))
-    return st;
-  if (dw && (st = check_ws(workspace, workspace_bytes, norm_workspace(rows, cols)))) return st;
-  moe::NormGradArgs a{};
-  a.dy = dy;
-  a.h = h;
-  a.w = weight;
-  a.dh = dh;
-  a.dx = dx;
-  a.part = dw ? static_cast<float*>(workspace) : nullptr;
-  a.rows = rows;
-  a.cols = cols;
-  a.eps = eps;
-  a.bf16 = dtype == MOE_BF16;
-  a.w_bf16 = w_dtype == MOE_BF16;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t err = hipSuccess;
-  if (rows > 0) err = timed("rms_norm_grad", s, [&] { return moe::launch_norm_grad(a, s); });
-  if (err == hipSuccess && dw)
-    err = timed("rms_norm_grad_join", s, [&] {
-      return moe::launch_norm_grad_join(a.part, moe::norm_grad_parts(rows, cols), cols, dw, dw_dtype == MOE_BF16, s);
-    });
-  return device_status(err, fn);
+  return run_norm_grad("moe_rms_norm_grad", dtype, dtype, rows, cols, dy, h, weight, w_dtype, eps, dh, dx, dw, dw_dtype,
+                       workspace, workspace_bytes, stream);
+}
+
+int moe_rms_norm_grad_f32(int32_t dtype, int64_t rows, int32_t cols, const float* dy, const void* h, const void* weight,
+                          int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  return run_norm_grad("moe_rms_norm_grad_f32", dtype, MOE_F32, rows, cols, dy, h, weight, w_dtype, eps, dh, dx, dw,
+                       dw_dtype, workspace, workspace_bytes, stream);
 }
 
 const char* moe_last_error(void) { return g_last_error.c_str(); }

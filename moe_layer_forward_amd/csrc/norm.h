@@ -33,7 +33,8 @@ struct NormGradArgs {
   int64_t rows;
   int32_t cols;
   float eps;
-  bool bf16, w_bf16;
+  bool bf16, w_bf16;   // h, dh and dx; w
+  bool dy_f32;         // dy in fp32 over bf16 rows
 };
 int norm_grad_parts(int64_t rows, int32_t cols);
 __host__ __device__ inline int64_t norm_grad_ld(int32_t cols) { return (cols + 31) / 32 * 32; }

@@ -176,7 +176,8 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
 // Rows r, r + gridDim.x * kRows, ... of a work-group's kRows sets of kLanes lanes; dw of its rows stays in
 // registers and leaves once, as row blockIdx.x of part.  kHold: so do the weights, and dh is read ahead; without, both are
 // read where they are used (the weights twice a row, from the cache), for rows that leave no registers for them.
-template <class T, int kLanes, int kChunks, bool kHold, bool kNt>
+// D: the type of dy.
+template <class T, class D, int kLanes, int kChunks, bool kHold, bool kNt>
 __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(NormGradArgs a) {
   constexpr int kRows = norm_threads(kLanes) / kLanes;
   struct Two {
@@ -211,16 +212,17 @@ __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(Norm
   int turn = 0;
   for (int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes; r < a.rows; r += (int64_t)gridDim.x * kRows) {
     const int64_t at = r * a.cols;
-    const T* pdy = static_cast<const T*>(a.dy) + at;
+    const D* pdy = static_cast<const D*>(a.dy) + at;
     const T* ph = static_cast<const T*>(a.h) + at;
     const T* pdh = static_cast<const T*>(a.dh) + at;
-    Raw8<T> dy[kChunks], h[kChunks];
+    Raw8<D> dy[kChunks];
+    Raw8<T> h[kChunks];
     [[maybe_unused]] Raw8<T> dh[kHold ? kChunks : 1];
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
       const int c = 8 * (j * kLanes + lane);
       if (c < whole) {
-        dy[j].template load<kNt>(pdy + c);
+        dy[j].template load<(kNt && sizeof(D) == 2)>(pdy + c);
         h[j].template load<kNt>(ph + c);
       }
     }
@@ -389,22 +391,22 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return launch_norm<T, Out, 0>(a, s);
 }
 
-template <class T, bool kNt>
+template <class T, class D, bool kNt>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
   const int lanes = grad_lanes(a.rows, a.cols), threads = norm_threads(lanes);
   const int grid = norm_grad_parts(a.rows, a.cols);
-  if (lanes == 16) norm_grad_kernel<T, 16, 4, true, kNt><<<grid, threads, 0, s>>>(a);
-  else if (lanes == 64) norm_grad_kernel<T, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
-  else if (lanes == 256) norm_grad_kernel<T, 256, 4, true, kNt><<<grid, threads, 0, s>>>(a);
-  else if (a.cols <= 1024 * 8 * 2) norm_grad_kernel<T, 1024, 2, true, kNt><<<grid, threads, 0, s>>>(a);
-  else norm_grad_kernel<T, 1024, 4, false, kNt><<<grid, threads, 0, s>>>(a);
+  if (lanes == 16) norm_grad_kernel<T, D, 16, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else if (lanes == 64) norm_grad_kernel<T, D, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else if (lanes == 256) norm_grad_kernel<T, D, 256, 4, true, kNt><<<grid, threads, 0, s>>>(a);
+  else if (a.cols <= 1024 * 8 * 2) norm_grad_kernel<T, D, 1024, 2, true, kNt><<<grid, threads, 0, s>>>(a);
+  else norm_grad_kernel<T, D, 1024, 4, false, kNt><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
 }
-template <class T>
+template <class T, class D>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (row_streams<T>(a.rows * a.cols)) return launch_grad<T, true>(a, s);
-  return launch_grad<T, false>(a, s);
+    if (row_streams<T>(a.rows * a.cols)) return launch_grad<T, D, true>(a, s);
+  return launch_grad<T, D, false>(a, s);
 }
 
 }  // namespace
@@ -428,7 +430,8 @@ int norm_grad_parts(int64_t rows, int32_t cols) {
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
-  return a.bf16 ? launch_grad<uint16_t>(a, s) : launch_grad<float>(a, s);
+  if (!a.bf16) return launch_grad<float, float>(a, s);
+  return a.dy_f32 ? launch_grad<uint16_t, float>(a, s) : launch_grad<uint16_t, uint16_t>(a, s);
 }
 
 hipError_t launch_norm_grad_join(const float* part, int parts, int32_t cols, void* dw, bool dw_bf16, hipStream_t s) {
