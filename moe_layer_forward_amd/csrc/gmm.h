@@ -47,10 +47,10 @@ GmmPlan gmm_plan(const GmmArgs& a, void* workspace);
 hipError_t launch_gmm(const GmmPlan& p, hipStream_t s);
 // The workspace bytes it needs (decided by type, form and sizes alone).
 size_t gmm_workspace(const GmmArgs& a);
-// A grid of n work-groups (n < 2^32): a launch takes fewer than 2^32 threads in each dimension, so those past
-// kGmmGridX go to further rows of the grid.  A multiple of 8, so that work-group n still runs on XCD n % 8.
+// A grid of n work-groups (n < 2^32) of up to 1024 threads: a launch takes fewer than 2^32 threads in each dimension, so
+// those past kGmmGridX go to further rows of the grid.  A multiple of 8, so that work-group n still runs on XCD n % 8.
 // The last row may have work-groups past n: kernels return for them.
-constexpr unsigned kGmmGridX = 1u << 22;
+constexpr unsigned kGmmGridX = 1u << 21;
 inline dim3 gmm_grid(int64_t n) {
   return n <= kGmmGridX ? dim3((unsigned)n) : dim3(kGmmGridX, (unsigned)((n + kGmmGridX - 1) / kGmmGridX));
 }

@@ -393,14 +393,14 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #endif
 }
 
-// The scales of tile or slab blockIdx.x (the row tiles' places first, then the slabs of every group), pairs
-// blockIdx.y * kPackPairs on, into the order of the tile kernel's reads.  A work-group of 32 W threads, a row each.
+// The scales of tile or slab gmm_block() (the row tiles' places first, then the slabs of every group), pairs
+// blockIdx.z * kPackPairs on, into the order of the tile kernel's reads.  A work-group of 32 W threads, a row each.
 constexpr int kPackPairs = 4;
 template <int W>
 __global__ __launch_bounds__(32 * W) void mx4_pack_kernel(Mx4Args a, int slabs, uint8_t* packed) {
   constexpr int kTile = 32 * W, kBytes = kMx4PairScales<W>;
   __shared__ __align__(16) uint16_t order[kPackPairs][kBytes / 2];
-  const int64_t places = gmm_max_tiles(a.max_rows, a.G, kTile), at = blockIdx.x;
+  const int64_t places = gmm_max_tiles(a.max_rows, a.G, kTile), at = gmm_block();
   const int lds = mx4_scale_cols(a.K), pairs = lds / 16, rl = threadIdx.x, r = rl & 15;
   const uint8_t* row;
   int place;  // of the lane that reads this row's first block (l / 16 = 0), in units of 2 bytes, and from block to block
@@ -420,12 +420,13 @@ __global__ __launch_bounds__(32 * W) void mx4_pack_kernel(Mx4Args a, int slabs, 
     place = ((rl >> 4 & 1) * 64 + r) * per + (rl >> 5);
   } else {
     const int64_t s = at - places, q0 = s % slabs * kTile;
+    if (s >= (int64_t)a.G * slabs) return;  // past the grid's last place
     const int64_t n = s / slabs * a.N + (q0 + rl < a.N ? q0 + rl : a.N - 1);
     row = a.ws + n * lds;
     per = 4;  // row 64 wc + 16 s + r: scale s of lane r of wave column wc
     place = ((rl >> 6) * 64 + r) * per + (rl >> 4 & 3);
   }
-  const int first = blockIdx.y * kPackPairs;
+  const int first = blockIdx.z * kPackPairs;
 #pragma unroll
   for (int j = 0; j < kPackPairs; ++j)
     if (first + j < pairs) {
@@ -462,7 +463,8 @@ size_t mx4_packed_bytes(const Mx4Args& a) {
 
 hipError_t launch_mx4_pack(const Mx4Args& a, hipStream_t s) {
   const int pairs = mx4_scale_cols(a.K) / 16;
-  const dim3 grid((unsigned)pack_places(a), (unsigned)((pairs + kPackPairs - 1) / kPackPairs));
+  dim3 grid = gmm_grid(pack_places(a));
+  grid.z = (unsigned)((pairs + kPackPairs - 1) / kPackPairs);
   mx4_pack_kernel<8><<<grid, 256, 0, s>>>(a, tile_slabs(a, 8), a.packed);
   return hipGetLastError();
 }
