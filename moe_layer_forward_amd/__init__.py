@@ -453,6 +453,16 @@ def _launch(dev, entry, *args):
             _check(entry(*args, _current[0](index)))
 
 
+def _written(*tensors):
+    """The caller's tensors that a call has written (None: a new one was): their versions rise, as under torch's own
+    operations in place, so that a backward pass that saved one of them raises an error."""
+    for t in tensors:
+        if t is not None:
+            import torch
+
+            torch.autograd.graph.increment_version(t)
+
+
 @functools.lru_cache(maxsize=1024)  # a function of the sizes alone, asked before every call of the same sizes
 def moe_matmul_workspace_size(op: int, dtype: int, n_groups: int, max_rows: int, N: int, K: int) -> int:
     n = load_library().moe_matmul_workspace_size(op, dtype, n_groups, max_rows, N, K)
@@ -539,6 +549,7 @@ def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, worksp
     ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_FORWARD, dt, G, rows, N, K, dev)
     _launch(dev, load_library().moe_grouped_matmul, dt, G, N, K, _addr(group_offsets), rows, x.data_ptr(), x_rows,
             _addr(row_index), w.data_ptr(), y.data_ptr(), ydt, wp, nb)
+    _written(out)
     return y
 
 
@@ -557,6 +568,7 @@ def moe_grouped_matmul_dx(dy, w, group_offsets, dx_dtype=None, workspace=None, o
     ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_DX, dt, G, rows, N, K, dev)
     _launch(dev, load_library().moe_grouped_matmul_dx, dt, G, N, K, _addr(group_offsets), rows, dy.data_ptr(),
             w.data_ptr(), dx.data_ptr(), odt, wp, nb)
+    _written(out)
     return dx
 
 
@@ -578,6 +590,7 @@ def moe_grouped_matmul_dw(dy, x, group_offsets, row_index=None, dw_dtype=None, w
     ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_DW, dt, G, rows, N, K, dev)
     _launch(dev, load_library().moe_grouped_matmul_dw, dt, G, N, K, _addr(group_offsets), rows, dy.data_ptr(),
             x.data_ptr(), x_rows, _addr(row_index), dw.data_ptr(), odt, wp, nb)
+    _written(out)
     return dw
 
 
@@ -591,6 +604,7 @@ def moe_quantize_rows(x, swiglu=False, codes=None, scales=None):
         raise ValueError("x must be [rows, cols] (swiglu: [rows, 2 cols])")
     rows, cols = x.shape[0], x.shape[1] // 2 if swiglu else x.shape[1]
     dev = _one_device(x, codes, scales)
+    given = codes, scales
     if codes is None:
         codes = torch.empty((rows, cols), dtype=torch.int8, device=dev)
     else:
@@ -601,6 +615,7 @@ def moe_quantize_rows(x, swiglu=False, codes=None, scales=None):
         _want(scales, "scales", (rows,), torch.float32)
     _launch(dev, load_library().moe_quantize_rows, dt, rows, cols, 1 if swiglu else 0, x.data_ptr(), codes.data_ptr(),
             scales.data_ptr())
+    _written(*given)
     return codes, scales
 
 
@@ -630,6 +645,7 @@ def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_
     _launch(dev, load_library().moe_matmul_i8, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
             x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
             nb)
+    _written(out)
     return y
 
 
@@ -667,6 +683,7 @@ def moe_quantize_mx4(x, swiglu=False, codes=None, scales=None):
     if cols % 32:
         raise ValueError(f"cols ({cols}) must be a multiple of 32")
     dev = _one_device(x, codes, scales)
+    given = codes, scales
     if codes is None:
         codes = x.new_empty((rows, cols // 2), dtype=torch.uint8)
     else:
@@ -677,6 +694,7 @@ def moe_quantize_mx4(x, swiglu=False, codes=None, scales=None):
         _want(scales, "scales", (rows, mx4_scale_cols(cols)), torch.uint8)
     _launch(dev, load_library().moe_quantize_mx4, dt, rows, cols, 1 if swiglu else 0, x.data_ptr(), codes.data_ptr(),
             scales.data_ptr())
+    _written(*given)
     return codes, scales
 
 
@@ -689,6 +707,7 @@ def moe_dequantize_mx4(codes, scales, y_dtype=None, out=None):
     dev = _one_device(codes, scales, out)
     y, ydt = _out(out, (rows, K), y_dtype, MOE_BF16, dev)
     _launch(dev, load_library().moe_dequantize_mx4, rows, K, codes.data_ptr(), scales.data_ptr(), y.data_ptr(), ydt)
+    _written(out)
     return y
 
 
@@ -716,6 +735,7 @@ def moe_matmul_mx4(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row
     _launch(dev, load_library().moe_matmul_mx4, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
             x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
             nb)
+    _written(out)
     return y
 
 
@@ -810,7 +830,7 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None
 
     x [rows, cols] and residual (or None: h = x) of one type (bfloat16 or float32), weight [cols] bfloat16 or float32
     (None: ones).  Returns y of x's type, or of y_dtype (MOE_BF16, MOE_F32), and with a residual (y, h), h in x's type.
-    h_out may be x or residual, out may be x.
+    h_out may be x or residual, out may be x; a backward pass that saved what they overwrite raises torch's error.
 
     Where an input requires a gradient, y and h have one (moe_rms_norm_grad); what is written to out or h_out has none,
     as have the results of the calls below.  A backward pass can be captured into a graph; torch ends the process where
@@ -831,6 +851,7 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None
         y, ydt = _out(out, (rows, cols), y_dtype, dt, dev)
     _launch(dev, load_library().moe_rms_norm, dt, rows, cols, x.data_ptr(), _addr(residual), _addr(weight), wdt, eps,
             _addr(h), y.data_ptr(), ydt)
+    _written(out, h_out)
     return y if h is None else (y, h)
 
 
@@ -842,6 +863,7 @@ def moe_rms_norm_i8(x, weight=None, residual=None, eps=1e-6, codes=None, scales=
     dt, wdt = _norm_args(x, weight, residual)
     rows, cols = x.shape
     dev = _one_device(x, weight, residual, codes, scales, h_out)
+    given = codes, scales, h_out
     h = _norm_h(x, residual, h_out)
     if codes is None:
         codes = torch.empty_like(x, dtype=torch.int8)
@@ -853,6 +875,7 @@ def moe_rms_norm_i8(x, weight=None, residual=None, eps=1e-6, codes=None, scales=
         _want(scales, "scales", (rows,), torch.float32)
     _launch(dev, load_library().moe_rms_norm_i8, dt, rows, cols, x.data_ptr(), _addr(residual), _addr(weight), wdt, eps,
             _addr(h), codes.data_ptr(), scales.data_ptr())
+    _written(*given)
     return (codes, scales) if h is None else (codes, scales, h)
 
 
@@ -879,6 +902,7 @@ def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dt
     if dh is not None:
         _want(dh, "dh", h.shape, h.dtype)
     dev = _one_device(dy, h, weight, dh, workspace, out, dw_out)
+    given = out, dw_out
     if out is None:
         out = torch.empty_like(h)
     else:
@@ -897,6 +921,7 @@ def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dt
     lib = load_library()
     _launch(dev, lib.moe_rms_norm_grad_f32 if wide else lib.moe_rms_norm_grad, dt, rows, cols, dy.data_ptr(),
             h.data_ptr(), _addr(weight), wdt, eps, _addr(dh), out.data_ptr(), _addr(dw), dwt, ws, nb)
+    _written(*given)
     return out, dw
 
 

@@ -74,3 +74,51 @@ def test_an_fp32_gradient_unaligned_in_place_and_refused():
                 lambda: moe.moe_rms_norm_grad(dy, h, dh=dy)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_outputs_over_a_saved_tensor_are_noticed():
+    """The first norm saved h1 for its backward pass, and the second writes its own h over it."""
+    torch = _torch()
+    x, w = _randn((5, 96), "float32", 1).requires_grad_(), _randn((96,), "float32", 2).requires_grad_()
+    y1, h1 = moe.moe_rms_norm(x, w, residual=_randn((5, 96), "float32", 3))
+    buffer = h1.detach()
+    moe.moe_rms_norm(_randn((5, 96), "float32", 4), residual=buffer, h_out=buffer)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y1.sum().backward()
+    y2 = moe.moe_rms_norm(x, w)
+    with torch.no_grad():
+        moe.moe_rms_norm(x, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y2.sum().backward()
+
+
+def test_every_given_output_is_a_new_version():
+    """Outputs of the norm, the conversions and the products; a new output is at version 0, what is only read stays."""
+    torch = _torch()
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    b = lambda *s: torch.zeros(s, device="cuda", dtype=torch.uint8)  # noqa: E731
+    i8 = lambda *s: torch.zeros(s, device="cuda", dtype=torch.int8)  # noqa: E731
+    x, w, r, off = f(4, 64), f(64), f(4, 64), torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    w3, c, s, wc, ws = f(1, 8, 64), b(4, 32), b(4, 16), b(1, 8, 32), b(1, 8, 16)
+    calls = [(lambda o: moe.moe_rms_norm(x, w, out=o), f(4, 64)),
+             (lambda o: moe.moe_rms_norm(x, w, residual=r, h_out=o), f(4, 64)),
+             (lambda o: moe.moe_rms_norm_i8(x, w, codes=o), i8(4, 64)), (lambda o: moe.moe_rms_norm_i8(x, w, scales=o), f(4)),
+             (lambda o: moe.moe_rms_norm_i8(x, w, residual=r, h_out=o), f(4, 64)),
+             (lambda o: moe.moe_rms_norm_grad(x, r, w, out=o), f(4, 64)),
+             (lambda o: moe.moe_rms_norm_grad(x, r, w, dw_out=o), f(64)),
+             (lambda o: moe.moe_quantize_rows(x, codes=o), i8(4, 64)), (lambda o: moe.moe_quantize_rows(x, scales=o), f(4)),
+             (lambda o: moe.moe_quantize_mx4(x, codes=o), b(4, 32)), (lambda o: moe.moe_quantize_mx4(x, scales=o), b(4, 16)),
+             (lambda o: moe.moe_dequantize_mx4(c, s, out=o), f(4, 64)),
+             (lambda o: moe.moe_matmul_mx4(c, s, wc, ws, out=o), f(4, 8)),
+             (lambda o: moe.moe_matmul_i8(i8(4, 64), f(4), i8(1, 8, 64), f(1, 8), out=o), f(4, 8)),
+             (lambda o: moe.moe_grouped_matmul(x, w3, off, out=o), f(4, 8)),
+             (lambda o: moe.moe_grouped_matmul_dx(f(4, 8), w3, off, out=o), f(4, 64)),
+             (lambda o: moe.moe_grouped_matmul_dw(f(4, 8), x, off, out=o), f(1, 8, 64))]
+    for i, (call, out) in enumerate(calls):
+        before = out._version
+        call(out)
+        assert out._version > before, i
+    assert all(t._version == 0 for t in (x, w, r, w3, c, s, wc, ws))
+    assert all(t._version == 0 for t in moe.moe_rms_norm(x, w, residual=r))
+    with torch.inference_mode():  # tensors without versions
+        moe.moe_rms_norm(f(4, 64), out=f(4, 64))
