@@ -453,6 +453,21 @@ def _launch(dev, entry, *args):
             _check(entry(*args, _current[0](index)))
 
 
+_forward_ad = None  # torch.autograd.forward_ad
+
+
+def _no_tangent(*tensors):
+    """Refuse forward-mode derivatives, which the differentiable calls do not have: a dual tensor asks for no gradient, and
+    its tangent would be lost without a word."""
+    global _forward_ad
+    if _forward_ad is None:
+        from torch.autograd import forward_ad as _forward_ad
+    if getattr(_forward_ad, "_current_level", 0) >= 0:  # inside a dual_level
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("moe: no forward-mode derivatives")
+
+
 def _written(*tensors):
     """The caller's tensors that a call has written (None: a new one was): their versions rise, as under torch's own
     operations in place, so that a backward pass that saved one of them raises an error."""
@@ -530,10 +545,11 @@ def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, worksp
     x's type, or of y_dtype (MOE_BF16, MOE_F32).  Rows past group_offsets[G] are not written.
 
     Where x or w requires a gradient, y has one: moe_grouped_matmul_dx (summed over the rows that gathered a row of
-    x) and moe_grouped_matmul_dw, each once.  A y written to out has none, as have the results of the calls
+    x) and moe_grouped_matmul_dw, each once (none in forward mode: dual tensors are refused).  A y written to out has none, as have the results of the calls
     below."""
     import torch
 
+    _no_tangent(x, w)
     if out is None and (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
         return _differentiable_product(x, w, group_offsets, row_index, y_dtype, workspace)
     dt = _matmul_dtype(x, "x")
@@ -832,11 +848,12 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None
     (None: ones).  Returns y of x's type, or of y_dtype (MOE_BF16, MOE_F32), and with a residual (y, h), h in x's type.
     h_out may be x or residual, out may be x; a backward pass that saved what they overwrite raises torch's error.
 
-    Where an input requires a gradient, y and h have one (moe_rms_norm_grad); what is written to out or h_out has none,
-    as have the results of the calls below.  A backward pass can be captured into a graph; torch ends the process where
+    Where an input requires a gradient, y and h have one (moe_rms_norm_grad; none in forward mode: dual tensors are
+    refused); what is written to out or h_out has none, as have the results of the calls below.  A backward pass can be captured into a graph; torch ends the process where
     results of eager calls on the same leaves are alive meanwhile, which is refused where they are this function's."""
     import torch
 
+    _no_tangent(x, weight, residual)
     if out is None and h_out is None and torch.is_grad_enabled() and (
             x.requires_grad or (weight is not None and weight.requires_grad)
             or (residual is not None and residual.requires_grad)):

@@ -18,3 +18,19 @@ def test_gradient_of_an_fp32_y(dtype, dy, h, ws, status):
                                                    None)
     assert got == (moe.MOE_ERR_UNSUPPORTED if status is None else status)
     assert "moe_rms_norm_grad_f32" in moe.moe_last_error() or status == WORKSPACE
+
+
+def test_dual_tensors_are_refused():
+    """Forward-mode derivatives: the tangent of a dual tensor, which asks for no gradient, would be lost."""
+    torch = pytest.importorskip("torch")
+    forward_ad = torch.autograd.forward_ad
+    x, w, w3 = torch.ones(4, 64), torch.ones(64), torch.ones(1, 8, 64)
+    with forward_ad.dual_level():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: moe.moe_rms_norm(dual(x), w), lambda: moe.moe_rms_norm(x, dual(w)),
+                     lambda: moe.moe_rms_norm(x, w, residual=dual(x)), lambda: moe.moe_rms_norm(dual(x), out=x),
+                     lambda: moe.moe_grouped_matmul(dual(x), w3, None), lambda: moe.moe_grouped_matmul(x, dual(w3), None)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        with pytest.raises(ValueError, match="GPU"):  # no tangent: the call goes on to its other checks
+            moe.moe_rms_norm(x, w)
