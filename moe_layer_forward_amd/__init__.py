@@ -830,14 +830,18 @@ def _graph_leaves(*tensors):
     process."""
     import torch
 
-    stream, nodes = torch.cuda.current_stream().cuda_stream, []
+    dev = _one_device(*tensors)  # the stream is that device's, whichever is the current one
+    stream, nodes = torch.cuda.current_stream(dev).cuda_stream, []
     for t in tensors:
         if t is not None and t.requires_grad and t.is_leaf:
             node = torch.autograd.graph.get_gradient_edge(t).node
             nodes.append(node)
-            if node.metadata.setdefault("moe_stream", stream) != stream and torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("moe: an eager graph of the same leaves is alive: drop its results before the capture, "
-                                   "or warm up on the capturing stream")
+            if node.metadata.setdefault("moe_stream", stream) != stream:
+                with torch.cuda.device(dev):
+                    capturing = torch.cuda.is_current_stream_capturing()
+                if capturing:
+                    raise RuntimeError("moe: an eager graph of the same leaves is alive: drop its results before the "
+                                       "capture, or warm up on the capturing stream")
     return nodes
 
 

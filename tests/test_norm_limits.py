@@ -34,3 +34,11 @@ def test_dual_tensors_are_refused():
                 call()
         with pytest.raises(ValueError, match="GPU"):  # no tangent: the call goes on to its other checks
             moe.moe_rms_norm(x, w)
+
+
+def test_leaves_outside_the_gpu_are_refused_like_every_tensor():
+    torch = pytest.importorskip("torch")
+    x, w = torch.ones(4, 64), torch.ones(64)
+    for args in ((x, w), (x.clone().requires_grad_(), w), (x, w.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="every tensor must live on the GPU"):
+            moe.moe_rms_norm(*args)
