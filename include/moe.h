@@ -389,7 +389,7 @@ int moe_matmul_mx4(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_
  *   dtype     MOE_BF16 or MOE_F32: x, residual and h, [rows, cols]
  *   weight    [cols] of w_dtype (MOE_BF16 or MOE_F32), or NULL: ones
  *   eps       finite, >= 0
- *   h         may be x or residual; y may be x, if it has its type
+ *   h         may be x or residual; y may be x, if it has its type and h is another
  *   y         [rows, cols] of y_dtype out
  * 1 <= cols <= 32768, rows <= 2^31-1.  Matrices need only start on a boundary of their element size.  No workspace. */
 int moe_rms_norm(int32_t dtype, int64_t rows, int32_t cols, const void* x, const void* residual, const void* weight,

@@ -850,11 +850,13 @@ def moe_rms_norm(x, weight=None, residual=None, eps=1e-6, y_dtype=None, out=None
 
     x [rows, cols] and residual (or None: h = x) of one type (bfloat16 or float32), weight [cols] bfloat16 or float32
     (None: ones).  Returns y of x's type, or of y_dtype (MOE_BF16, MOE_F32), and with a residual (y, h), h in x's type.
-    h_out may be x or residual, out may be x; a backward pass that saved what they overwrite raises torch's error.
+    h_out may be x or residual, out may be x (not both x); a backward pass that saved what they overwrite raises torch's
+    error.
 
     Where an input requires a gradient, y and h have one (moe_rms_norm_grad; none in forward mode: dual tensors are
-    refused); what is written to out or h_out has none, as have the results of the calls below.  A backward pass can be captured into a graph; torch ends the process where
-    results of eager calls on the same leaves are alive meanwhile, which is refused where they are this function's."""
+    refused); what is written to out or h_out has none, as have the results of the calls below.  A backward pass can be
+    captured into a graph; torch ends the process where results of eager calls on the same leaves are alive meanwhile,
+    which is refused where they are this function's."""
     import torch
 
     _no_tangent(x, weight, residual)

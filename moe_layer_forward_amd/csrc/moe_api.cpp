@@ -650,6 +650,7 @@ int run_norm(const char* fn, const char* kernel, int32_t dtype, int64_t rows, in
     return fail(MOE_ERR_INVALID_ARG, "%s: x and %s are required", fn, i8 ? "codes and scales" : "y");
   if ((residual == nullptr) != (h == nullptr))
     return fail(MOE_ERR_INVALID_ARG, "%s: residual and h must both be given or both be NULL", fn);
+  if (h == out) return fail(MOE_ERR_INVALID_ARG, "%s: h and %s must not be the same", fn, i8 ? "codes" : "y");
   const size_t e = elem_bytes(dtype);
   if ((st = check_aligned(fn, {{x, e, "x"}, {residual, e, "residual"}, {weight, elem_bytes(w_dtype), "weight"}, {h, e, "h"},
                                {out, i8 ? 1 : kind == moe::NormOut::kBf16 ? 2u : 4u, "y"}, {scales, 4, "scales"}})))

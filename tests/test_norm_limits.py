@@ -42,3 +42,12 @@ def test_leaves_outside_the_gpu_are_refused_like_every_tensor():
     for args in ((x, w), (x.clone().requires_grad_(), w), (x, w.clone().requires_grad_())):
         with pytest.raises(ValueError, match="every tensor must live on the GPU"):
             moe.moe_rms_norm(*args)
+
+
+def test_h_and_y_in_one_place_are_refused():
+    """Each may be x, but one would overwrite the other."""
+    lib, y = moe.load_library(), ctypes.c_void_p(0x2000)
+    assert lib.moe_rms_norm(1, 4, 64, FAKE, FAKE, FAKE, 1, 1e-6, FAKE, FAKE, 1, None) == INVALID
+    assert "same" in moe.moe_last_error()
+    assert lib.moe_rms_norm_i8(1, 4, 64, FAKE, FAKE, FAKE, 1, 1e-6, y, y, FAKE, None) == INVALID
+    assert "same" in moe.moe_last_error()
