@@ -385,7 +385,8 @@ int moe_matmul_mx4(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_
  * The root-mean-square norm that stands before the layer, with the residual's addition:
  *     h = x + residual, rounded to dtype (residual NULL: h = x and the argument h must be NULL)
  *     y = h * w / sqrt(mean(h^2) + eps)
- * Each row by itself, in fp32, y rounded once; mean(h^2) overflows (y = 0) where a row's squares do.
+ * Each row by itself, in fp32, y rounded once; mean(h^2) overflows (y = 0) where a row's squares do.  With eps = 0 they
+ * have to be normal numbers of fp32, too: where all of them vanish (values below 2^-75), y is infinite, or NaN where h is 0.
  *   dtype     MOE_BF16 or MOE_F32: x, residual and h, [rows, cols]
  *   weight    [cols] of w_dtype (MOE_BF16 or MOE_F32), or NULL: ones
  *   eps       finite, >= 0

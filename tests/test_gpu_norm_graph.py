@@ -122,3 +122,22 @@ def test_every_given_output_is_a_new_version():
     assert all(t._version == 0 for t in moe.moe_rms_norm(x, w, residual=r))
     with torch.inference_mode():  # tensors without versions
         moe.moe_rms_norm(f(4, 64), out=f(4, 64))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_squares_outside_fp32(dtype):
+    """Rows whose squares vanish or overflow, as include/moe.h states them; other rows keep their bits."""
+    torch = _torch()
+    x = _randn((5, 520), dtype, 1)
+    plain = {eps: moe.moe_rms_norm(x, eps=eps) for eps in (0.0, 1e-6)}
+    x[1], x[2], x[3] = 1e-23, 1e25, 0
+    x[1, 0] = 0
+    y = moe.moe_rms_norm(x, eps=0.0)
+    assert bool(y[1, 0].isnan()) and bool((y[1, 1:] == float("inf")).all())
+    assert not bool(y[2].any()) and bool(y[3].isnan().all())
+    z = moe.moe_rms_norm(x, eps=1e-6)
+    ref = x[1].double() * 1e3
+    assert bool(((z[1].double() - ref).abs() <= (torch.finfo(x.dtype).eps / 2 + 40 * U) * ref).all())
+    assert not bool(z[2].any()) and not bool(z[3].any())
+    for i in (0, 4):
+        assert torch.equal(y[i], plain[0.0][i]) and torch.equal(z[i], plain[1e-6][i])
