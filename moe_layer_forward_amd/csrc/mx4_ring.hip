@@ -98,7 +98,7 @@ struct RingLoads {
     typedef __attribute__((address_space(3))) void* Lds;
     const int lane = threadIdx.x & 63, quarter = lane >> 4;
     const uint32_t kb = (uint32_t)win * kRingRow, left = ld - kb;
-    const Mx4Rsrc rw = mx4_rsrc(w + kb, nw - kb), rx = mx4_rsrc(x + kb, nx - kb);
+    const Mx4Rsrc rw = mx4_rsrc(w + kb, nw > kb ? nw - kb : 0), rx = mx4_rsrc(x + kb, nx > kb ? nx - kb : 0);
     // chunks past the end of a row put zeros into LDS and read nothing
 #pragma unroll
     for (int i = 0; i < 4 * QB; ++i)
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
         tiles.find(a, 16 * NB, load_item / slabs, g, beg, end);
         loads.init(a, g, beg, end, load_item % slabs, wave);
       } else {
-        loads.nw = loads.nx = 0;  // past the last item: nothing is read, but the waits count the same
+        loads.nw = loads.nx = 0;  // past the last item: no codes are read (its scales are), and the waits count the same
       }
     }
   };
