@@ -16,12 +16,6 @@ __device__ __forceinline__ Mx4Rsrc mx4_rsrc(const uint8_t* base, uint32_t record
 __device__ __forceinline__ gmm_u32x4 mx4_load128(Mx4Rsrc r, uint32_t off) {
   return __builtin_bit_cast(gmm_u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
-__device__ __forceinline__ uint32_t mx4_load32(Mx4Rsrc r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
-}
-__device__ __forceinline__ uint32_t mx4_load8(Mx4Rsrc r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b8(r, (int)off, 0, 0);
-}
 
 // The row tiles of the groups, `tile` rows each: the full ones first, in the order of their groups, then every group's
 // last, partial one, by their blocks of 32 rows, the longest first, so that the chip's last round is a short one (48

@@ -23,13 +23,11 @@ constexpr int kRingWaves = 4;
 constexpr int kRingP = 1, kRingQ = 2, kRingPer = 2;  // NB, QB, work-groups to a CU
 constexpr int kRingRow = 256;  // bytes of a row and step
 
-// QB 16-column blocks to a wave; as many stages as let `per` work-groups run on a CU.
+// QB 16-column blocks to a wave; two stages, which let `per` work-groups run on a CU.
 template <int NB, int QB, int per>
 struct RingShape {
   static constexpr int kX = NB * 16 * kRingRow, kW = kRingWaves * QB * 16 * kRingRow, kS = kRingWaves * (QB + 1) * 256;
-  static constexpr int kFit = 160 * 1024 / per / (kX + kW + kS), kDepth = kFit < 6 ? kFit : 6;
-  static constexpr int kLoads = 4 * QB + NB + 1;  // of a wave and step
-  static_assert((kDepth - 2) * kLoads <= 63, "vmcnt");
+  static_assert(2 * per * (kX + kW + kS) <= 160 * 1024, "LDS");
 };
 
 struct RingStage {
@@ -127,24 +125,10 @@ struct RingShare {
 template <int NB, int QB, int per>
 __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args a, int slabs) {
   using S = RingShape<NB, QB, per>;
-  constexpr int D = S::kDepth;
-#define MOE_MX4_STAGE(i) \
-  __shared__ __align__(16) char x##i##_[i < D ? S::kX : 16], w##i##_[i < D ? S::kW : 16], s##i##_[i < D ? S::kS : 16]
-  MOE_MX4_STAGE(0);
-  MOE_MX4_STAGE(1);
-  MOE_MX4_STAGE(2);
-  MOE_MX4_STAGE(3);
-  MOE_MX4_STAGE(4);
-  MOE_MX4_STAGE(5);
-#undef MOE_MX4_STAGE
-  [[maybe_unused]] const auto stage = [&](auto dc) -> RingStage {
-    constexpr int d = decltype(dc)::value % D;
-    if constexpr (d == 0) return {x0_, w0_, s0_};
-    else if constexpr (d == 1) return {x1_, w1_, s1_};
-    else if constexpr (d == 2) return {x2_, w2_, s2_};
-    else if constexpr (d == 3) return {x3_, w3_, s3_};
-    else if constexpr (d == 4) return {x4_, w4_, s4_};
-    else return {x5_, w5_, s5_};
+  __shared__ __align__(16) char x0_[S::kX], w0_[S::kW], s0_[S::kS], x1_[S::kX], w1_[S::kW], s1_[S::kS];
+  [[maybe_unused]] const auto stage = [&](auto odd) -> RingStage {
+    if constexpr (decltype(odd)::value) return {x1_, w1_, s1_};
+    else return {x0_, w0_, s0_};
   };
 #if defined(__HIP_DEVICE_COMPILE__)
   Mx4Tiles tiles;
@@ -175,21 +159,20 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
   };
   tiles.find(a, 16 * NB, load_item / slabs, g, beg, end);
   loads.init(a, g, beg, end, load_item % slabs, wave);
-  static_for<D - 1>([&](auto dc) { next_load(stage(dc)); });
+  next_load(stage(std::false_type{}));
   f32x4 acc[NB][QB];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int j = 0; j < QB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t turns = ((int64_t)mine * windows + D - 1) / D;
+  const int64_t turns = ((int64_t)mine * windows + 1) / 2;
   for (int64_t turn = 0; turn < turns; ++turn)
-    static_for<D>([&](auto dc) {
-      constexpr int d = decltype(dc)::value;
-      wait_vmcnt<(D - 2) * S::kLoads>();
+    static_for<2>([&](auto odd) {
+      wait_vmcnt<0>();
       block_sync_lds();
-      next_load(stage(std::integral_constant<int, d + D - 1>{}));
+      next_load(stage(std::bool_constant<!decltype(odd)::value>{}));
       __builtin_amdgcn_sched_barrier(0);
-      const RingStage st = stage(dc);
+      const RingStage st = stage(odd);
       const uint32_t mask = mx4_scale_mask(a.K / 32 - 16 * win - 4 * part);  // no scales from the padding
       const char* const scales = st.s + r * 16 + part * 4;
       uint32_t sw[QB], sx[NB];
