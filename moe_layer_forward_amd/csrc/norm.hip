@@ -357,11 +357,16 @@ __global__ __launch_bounds__(kJoinThreads) void norm_grad_join_kernel(const floa
 // lanes, 3.3 with 256; of 7168: 4.5 with 256, 3.9 with 1024; 1024 rows of 7168: 10.8 and 14.3).
 int lanes_of(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
 // Short rows (those of heads, say): 16 lanes, four rows to a wave, where there are many of them (bf16, 262144 rows of 128,
-// 16 and 64 lanes: 23.6 us and 64.8, with 8-bit output 27 and 92, gradients 46 and 148; of 512: 85 and 111, 66 and 110, 134
-// and 192; fp32 of 512: 183 and 183, 118 and 150, 305 and 292; 600 rows of 512: 3.5 and 3.1; 4096 of 512 with a residual: 5.6
-// and 4.8, of 256 4.2 and 4.2).
+// 16 and 64 lanes: 23.6 us and 64.8, with 8-bit output 27 and 92; of 512: 85 and 111, 66 and 110; fp32 of 512: 183 and 183,
+// 118 and 150; 600 rows of 512: 3.5 and 3.1; 4096 of 512 with a residual: 5.6 and 4.8, of 256 4.2 and 4.2).
 bool short_rows(int64_t rows, int32_t cols) { return cols <= 512 && rows > (cols <= 256 ? 512 : 8192); }
-int grad_lanes(int64_t rows, int32_t cols) { return cols <= 512 && rows > 512 ? 16 : lanes_of(cols); }
+// Gradients, both launches, 16 and 64 lanes, bf16: 262144 rows of 128 45 us and 146, of 512 135 and 193; 8192 of 512 13.2
+// and 14.4; 520 of 512 6.6 and 6.8.  fp32: 262144 rows of 256 147 and 184; 4096 of 512 11.3 and 13.0; 64 where both are
+// many: 8192 of 512 18.2 and 17.4, 262144 308 and 293, of 400 250 and 234; of 384 and less either by up to 5%.
+int grad_lanes(int64_t rows, int32_t cols, bool bf16) {
+  const bool narrow = cols <= 512 && rows > 512;
+  return narrow && (bf16 || cols <= 384 || rows < 8192) ? 16 : lanes_of(cols);
+}
 int norm_lanes(int64_t rows, int32_t cols) {
   const int lanes = lanes_of(cols);
   if (short_rows(rows, cols)) return 16;
@@ -393,7 +398,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 
 template <class T, class D, bool kNt>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t s) {
-  const int lanes = grad_lanes(a.rows, a.cols), threads = norm_threads(lanes);
+  const int lanes = grad_lanes(a.rows, a.cols, a.bf16), threads = norm_threads(lanes);
   const int grid = norm_grad_parts(a.rows, a.cols);
   if (lanes == 16) norm_grad_kernel<T, D, 16, 4, true, kNt><<<grid, threads, 0, s>>>(a);
   else if (lanes == 64) norm_grad_kernel<T, D, 64, 4, true, kNt><<<grid, threads, 0, s>>>(a);
@@ -422,9 +427,10 @@ hipError_t launch_rms_norm(const NormArgs& a, NormOut out, hipStream_t s) {
 }
 
 // As many work-groups as run at once, two on a CU or one of 1024 lanes: more write more sums and gain nothing (32768 rows of
-// 1024: 49 us with 512, 59 with 1024; 2048 of 16384: 79 with 256, 89 with 512).
+// 1024: 49 us with 512, 59 with 1024; 2048 of 16384: 79 with 256, 89 with 512).  The same for either type: from 8192 rows on
+// 16 lanes to a row make as many of them as 64.
 int norm_grad_parts(int64_t rows, int32_t cols) {
-  const int lanes = grad_lanes(rows, cols), per = norm_threads(lanes) / lanes;
+  const int lanes = grad_lanes(rows, cols, true), per = norm_threads(lanes) / lanes;
   const int64_t most = lanes == 1024 ? 256 : 512, groups = (rows + per - 1) / per;
   return (int)(groups < most ? groups : most);
 }

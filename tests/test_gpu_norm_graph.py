@@ -141,3 +141,15 @@ def test_squares_outside_fp32(dtype):
     assert not bool(z[2].any()) and not bool(z[3].any())
     for i in (0, 4):
         assert torch.equal(y[i], plain[0.0][i]) and torch.equal(z[i], plain[1e-6][i])
+
+
+@pytest.mark.parametrize("rows,cols", [(8191, 512), (8192, 512), (9003, 511), (8200, 385), (8200, 384), (8193, 383), (20000, 500)])
+def test_gradients_of_many_narrow_fp32_rows(rows, cols):
+    """On both sides of where 64 lanes take a row instead of 16; the same bits every time."""
+    torch = _torch()
+    dy, h, dh = (_randn((rows, cols), "float32", i, 0.5) for i in range(3))
+    w = _randn((cols,), "bfloat16", 4) + 1
+    dx, dw = moe.moe_rms_norm_grad(dy, h, w, dh=dh, dw_dtype=moe.MOE_F32)
+    _check(dx, dw, dy, h, w, dh)
+    again = moe.moe_rms_norm_grad(dy, h, w, dh=dh, dw_dtype=moe.MOE_F32)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
