@@ -352,14 +352,14 @@ int moe_matmul_i8(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_o
  *   codes   K / 2 bytes: value k in bits 4 (k % 2) .. + 3 of byte k / 2; bit 3 the sign, bits 2..0 the magnitude
  *           {0, 1/2, 1, 3/2, 2, 3, 4, 6}
  *   scales  S = 16 ceil(K / 512) bytes: byte b is the power s of block b, values 32 b .. 32 b + 31:
- *           value = magnitude * 2^(s - 127); s = 255: NaN.  Bytes from K / 32 on are padding (moe_quantize_mx4 writes 0;
- *           the product reads no value from them).
+ *           value = magnitude * 2^(s - 127); s = 255: NaN.  Bytes from K / 32 on are padding (moe_quantize_mx4 writes
+ *           0; the product reads no value from them).
  * Codes and scales start on 16 bytes.
  *
  * Rows to this format: a = max |v| over a block, s = max(floor(log2 a) - 2, -127) + 127 (a = 0: 0), each code the
  * nearest to v 2^(127 - s), ties to the even code, beyond 6 to 6.  A block with an infinity or NaN: s = 255, codes 0.
- * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up, and v = SiLU(gate) * up in fp32, the same
- * value as in moe_quantize_rows and in the layer's experts.
+ * swiglu = 0: v = x [rows, cols].  swiglu = 1: x is [rows, 2 cols], gate | up, and v = SiLU(gate) * up in fp32, the
+ * same value as in moe_quantize_rows and in the layer's experts.
  *   x of x_dtype (MOE_BF16 or MOE_F32; any alignment); codes [rows, cols / 2], scales [rows, S] out
  * cols a multiple of 32, at most 2^20, rows <= 2^31-1.  No workspace. */
 int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu, const void* x, uint8_t* codes,
@@ -367,8 +367,8 @@ int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu
 
 /* The values that codes stand for: y [rows, cols] of y_dtype out (exact but where bf16 or fp32 overflows or rounds a
  * subnormal; a block of scale 255: NaN).  Sizes as above; y of any alignment.  No workspace. */
-int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* codes, const uint8_t* scales, void* y, int32_t y_dtype,
-                       void* stream);
+int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* codes, const uint8_t* scales, void* y,
+                       int32_t y_dtype, void* stream);
 
 /* The grouped product: y[r, n] = sum_k x[i, k] * W[g(r), n, k], i = row_index ? row_index[r] : r, both in this format,
  * with groups, gathers, sizes and limits as in moe_grouped_matmul above (K a multiple of 32).  Sums in fp32, each
@@ -385,8 +385,9 @@ int moe_matmul_mx4(int32_t n_groups, int32_t N, int32_t K, const int32_t* group_
  * The root-mean-square norm that stands before the layer, with the residual's addition:
  *     h = x + residual, rounded to dtype (residual NULL: h = x and the argument h must be NULL)
  *     y = h * w / sqrt(mean(h^2) + eps)
- * Each row by itself, in fp32, y rounded once; mean(h^2) overflows (y = 0) where a row's squares do.  With eps = 0 they
- * have to be normal numbers of fp32, too: where all of them vanish (values below 2^-75), y is infinite, or NaN where h is 0.
+ * Each row by itself, in fp32, y rounded once; mean(h^2) overflows (y = 0) where a row's squares do.  With eps = 0
+ * they have to be normal numbers of fp32, too: where all of them vanish (values below 2^-75), y is infinite, or NaN
+ * where h is 0.
  *   dtype     MOE_BF16 or MOE_F32: x, residual and h, [rows, cols]
  *   weight    [cols] of w_dtype (MOE_BF16 or MOE_F32), or NULL: ones
  *   eps       finite, >= 0
@@ -414,8 +415,8 @@ int moe_rms_norm_grad(int32_t dtype, int64_t rows, int32_t cols, const void* dy,
                       int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype, void* workspace,
                       size_t workspace_bytes, void* stream);
 
-/* The same with dy in fp32 whatever dtype is: the gradient of a y that left in fp32, unrounded.  dx may be dy where dtype
- * is MOE_F32, and dh. */
+/* The same with dy in fp32 whatever dtype is: the gradient of a y that left in fp32, unrounded.  dx may be dy where
+ * dtype is MOE_F32, and dh. */
 int moe_rms_norm_grad_f32(int32_t dtype, int64_t rows, int32_t cols, const float* dy, const void* h, const void* weight,
                           int32_t w_dtype, float eps, const void* dh, void* dx, void* dw, int32_t dw_dtype,
                           void* workspace, size_t workspace_bytes, void* stream);

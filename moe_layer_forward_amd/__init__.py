@@ -457,8 +457,8 @@ _forward_ad = None  # torch.autograd.forward_ad
 
 
 def _no_tangent(*tensors):
-    """Refuse forward-mode derivatives, which the differentiable calls do not have: a dual tensor asks for no gradient, and
-    its tangent would be lost without a word."""
+    """Refuse forward-mode derivatives, which the differentiable calls do not have: a dual tensor asks for no gradient,
+    and its tangent would be lost without a word."""
     global _forward_ad
     if _forward_ad is None:
         from torch.autograd import forward_ad as _forward_ad
@@ -545,8 +545,8 @@ def moe_grouped_matmul(x, w, group_offsets, row_index=None, y_dtype=None, worksp
     x's type, or of y_dtype (MOE_BF16, MOE_F32).  Rows past group_offsets[G] are not written.
 
     Where x or w requires a gradient, y has one: moe_grouped_matmul_dx (summed over the rows that gathered a row of
-    x) and moe_grouped_matmul_dw, each once (none in forward mode: dual tensors are refused).  A y written to out has none, as have the results of the calls
-    below."""
+    x) and moe_grouped_matmul_dw, each once (none in forward mode: dual tensors are refused).  A y written to out has
+    none, as have the results of the calls below."""
     import torch
 
     _no_tangent(x, w)
@@ -659,8 +659,8 @@ def moe_matmul_i8(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row_
     y, ydt = _out(out, (rows, N), y_dtype, MOE_BF16, dev)
     ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_I8, MOE_F32, G, rows, N, K, dev)
     _launch(dev, load_library().moe_matmul_i8, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
-            x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
-            nb)
+            x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt,
+            wp, nb)
     _written(out)
     return y
 
@@ -749,8 +749,8 @@ def moe_matmul_mx4(x_codes, x_scales, w_codes, w_scales, group_offsets=None, row
     y, ydt = _out(out, (rows, N), y_dtype, MOE_BF16, dev)
     ws, wp, nb = _matmul_ws(workspace, MOE_MATMUL_MX4, MOE_F32, G, rows, N, K, dev)
     _launch(dev, load_library().moe_matmul_mx4, G, N, K, _addr(group_offsets), rows, x_codes.data_ptr(),
-            x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt, wp,
-            nb)
+            x_scales.data_ptr(), x_rows, _addr(row_index), w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), ydt,
+            wp, nb)
     _written(out)
     return y
 
@@ -914,8 +914,8 @@ def moe_rms_norm_grad(dy, h, weight=None, dh=None, eps=1e-6, need_dw=True, dw_dt
                       dw_out=None):
     """Gradients of moe_rms_norm: (dx, dw) from dy (y's gradient, of h's type or float32), h (what the norm was taken
     of) and dh (what reaches h past the norm, or None).  dx is the gradient of x and of the residual alike, in h's type;
-    dw has the weight's type, or dw_dtype, and is None without a weight or with need_dw=False.  out (for dx) may be dy (of
-    h's type) or dh."""
+    dw has the weight's type, or dw_dtype, and is None without a weight or with need_dw=False.  out (for dx) may be dy
+    (of h's type) or dh."""
     import torch
 
     dt, wdt = _norm_args(h, weight, None, "h")

@@ -592,12 +592,14 @@ int check_mx4(const char* fn, const moe::Mx4Args& a, int32_t out_dtype) {
   if (a.N < 1 || a.K < 1) return fail(MOE_ERR_INVALID_ARG, "%s: N and K must be positive (N=%d K=%d)", fn, a.N, a.K);
   if (a.K % kMx4Block) return fail(MOE_ERR_INVALID_ARG, "%s: K (%d) must be a multiple of %d", fn, a.K, kMx4Block);
   if (a.max_rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: negative max_rows", fn);
-  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: output dtype %d", fn, out_dtype);
+  if (out_dtype != MOE_F32 && out_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: output dtype %d", fn, out_dtype);
   if (a.max_rows > 0x7fffffffLL) return fail(MOE_ERR_UNSUPPORTED, "%s: max_rows exceeds 2^31-1", fn);
   if (a.N > kMaxMatmulSide || a.K > kMaxMatmulSide)
     return fail(MOE_ERR_UNSUPPORTED, "%s: N and K must be at most %d", fn, kMaxMatmulSide);
   constexpr int64_t kSpan = int64_t(1) << 32;  // 32-bit byte offsets
-  if ((int64_t)a.N * a.K / 2 >= kSpan) return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weight must stay below 4 GiB", fn);
+  if ((int64_t)a.N * a.K / 2 >= kSpan)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: one group's weight must stay below 4 GiB", fn);
   if (!a.group_offsets && a.G != 1)
     return fail(MOE_ERR_INVALID_ARG, "%s: group_offsets may be NULL for one group only", fn);
   if (a.x_rows < 0 || (a.row_index ? a.x_rows == 0 && a.max_rows > 0 : a.x_rows < a.max_rows))
@@ -652,8 +654,8 @@ int run_norm(const char* fn, const char* kernel, int32_t dtype, int64_t rows, in
     return fail(MOE_ERR_INVALID_ARG, "%s: residual and h must both be given or both be NULL", fn);
   if (h == out) return fail(MOE_ERR_INVALID_ARG, "%s: h and %s must not be the same", fn, i8 ? "codes" : "y");
   const size_t e = elem_bytes(dtype);
-  if ((st = check_aligned(fn, {{x, e, "x"}, {residual, e, "residual"}, {weight, elem_bytes(w_dtype), "weight"}, {h, e, "h"},
-                               {out, i8 ? 1 : kind == moe::NormOut::kBf16 ? 2u : 4u, "y"}, {scales, 4, "scales"}})))
+  if ((st = check_aligned(fn, {{x, e, "x"}, {residual, e, "residual"}, {weight, elem_bytes(w_dtype), "weight"},
+                               {h, e, "h"}, {out, i8 ? 1 : kind == moe::NormOut::kBf16 ? 2u : 4u, "y"}, {scales, 4, "scales"}})))
     return st;
   moe::NormArgs a{};
   a.x = x;
@@ -1226,7 +1228,8 @@ int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu
   if (swiglu != 0 && swiglu != 1) return fail(MOE_ERR_INVALID_ARG, "%s: swiglu must be 0 or 1", fn);
   if (rows == 0) return ok();
   if (!x || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "%s: x, codes and scales are required", fn);
-  if ((st = check_aligned(fn, {{x, elem_bytes(x_dtype), "x"}, {codes, 16, "codes"}, {scales, 16, "scales"}}))) return st;
+  if ((st = check_aligned(fn, {{x, elem_bytes(x_dtype), "x"}, {codes, 16, "codes"}, {scales, 16, "scales"}})))
+    return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return device_status(timed("quantize_mx4", s, [&] {
                          return moe::launch_quantize_mx4(x, x_dtype == MOE_BF16, rows, cols, swiglu == 1, codes, scales,
@@ -1235,15 +1238,16 @@ int moe_quantize_mx4(int32_t x_dtype, int64_t rows, int32_t cols, int32_t swiglu
                        fn);
 }
 
-int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* codes, const uint8_t* scales, void* y, int32_t y_dtype,
-                       void* stream) {
+int moe_dequantize_mx4(int64_t rows, int32_t cols, const uint8_t* codes, const uint8_t* scales, void* y,
+                       int32_t y_dtype, void* stream) {
   prof_reset();
   const char* fn = "moe_dequantize_mx4";
   int st;
   if ((st = check_dtype(fn, "dtype", y_dtype)) || (st = check_mx4_rows(fn, rows, cols))) return st;
   if (rows == 0) return ok();
   if (!codes || !scales || !y) return fail(MOE_ERR_INVALID_ARG, "%s: codes, scales and y are required", fn);
-  if ((st = check_aligned(fn, {{codes, 16, "codes"}, {scales, 16, "scales"}, {y, elem_bytes(y_dtype), "y"}}))) return st;
+  if ((st = check_aligned(fn, {{codes, 16, "codes"}, {scales, 16, "scales"}, {y, elem_bytes(y_dtype), "y"}})))
+    return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return device_status(timed("dequantize_mx4", s, [&] {
                          return moe::launch_dequantize_mx4(codes, scales, rows, cols, y, y_dtype == MOE_BF16, s);

@@ -1,8 +1,8 @@
 // Launchers of the microscaled 4-bit operators.
 //
-// A row of K values (K a multiple of 32) is K / 2 bytes of codes, two to a byte with the earlier value in the low half,
-// and one scale byte s for every 32 of them: value = e2m1(code) 2^(s - 127), s = 255: NaN.  Rows of scales are padded to
-// whole 16 bytes (512 values): what a work-group reads at a time.
+// A row of K values (K a multiple of 32) is K / 2 bytes of codes, two to a byte with the earlier value in the low
+// half, and one scale byte s for every 32 of them: value = e2m1(code) 2^(s - 127), s = 255: NaN.  Rows of scales are
+// padded to whole 16 bytes (512 values): what a work-group reads at a time.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stddef.h>

@@ -10,24 +10,25 @@ typedef __amdgpu_buffer_rsrc_t Mx4Rsrc;
 constexpr uint32_t kMx4Outside = 0xfffffff0u;  // an offset past every record count: reads zeros
 
 __device__ __forceinline__ Mx4Rsrc mx4_rsrc(const uint8_t* base, uint32_t records) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(gmm_uniform(reinterpret_cast<const char*>(base))), (short)0,
-                                           gmm_uniform((int)records), 0x00020000);
+  const char* const at = gmm_uniform(reinterpret_cast<const char*>(base));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), (short)0, gmm_uniform((int)records), 0x00020000);
 }
 __device__ __forceinline__ gmm_u32x4 mx4_load128(Mx4Rsrc r, uint32_t off) {
   return __builtin_bit_cast(gmm_u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
 
-// The row tiles of the groups, `tile` rows each: the full ones first, in the order of their groups, then every group's
-// last, partial one, by their blocks of 32 rows, the longest first, so that the chip's last round is a short one (48
-// groups of 21 to 2118 rows, 2048 x 7168: 137 -> 133 us).  GmmTiles walks a lane's groups one by one; here the lanes' loads
-// go out together and a tile is found in the registers, since with few rows the search is a good part of an item.  More
-// than 512 groups go through GmmTiles, in the order of the groups.
+// The row tiles of the groups, `tile` rows each: the full ones first, in the order of their groups, then every
+// group's last, partial one, by their blocks of 32 rows, the longest first, so that the chip's last round is a short
+// one (48 groups of 21 to 2118 rows, 2048 x 7168: 137 -> 133 us).  GmmTiles walks a lane's groups one by one; here
+// the lanes' loads go out together and a tile is found in the registers, since with few rows the search is a good
+// part of an item.  More than 512 groups go through GmmTiles, in the order of the groups.
 struct Mx4Tiles {
   static constexpr int kHeld = 8;  // groups of a lane whose rows stay in registers: 512 in all
   static constexpr int kClasses = 8;  // blocks of 32 rows of a tile
   GmmTiles t;
   int n_full;  // of this lane's groups
-  uint32_t n_part[3], part_to[3];  // partial tiles of class c (8 - blocks), 10 bits each: this lane's, and up to its end
+  // partial tiles of class c (8 - blocks), 10 bits each: this lane's, and up to its end
+  uint32_t n_part[3], part_to[3];
   int off[kHeld + 1];
 
   __device__ __forceinline__ static int scan(int v) {  // inclusive sum over the lanes
@@ -140,7 +141,8 @@ struct Mx4Tiles {
 template <int TQ, int TP>
 __device__ __forceinline__ f32x4 mx4_mfma(gmm_u32x4 q, uint32_t sq, gmm_u32x4 p, uint32_t sp, f32x4 c) {
   typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-  const i32x8 qv{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0}, pv{(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
+  const i32x8 qv{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
+  const i32x8 pv{(int)p[0], (int)p[1], (int)p[2], (int)p[3], 0, 0, 0, 0};
   constexpr int kE2M1 = 4;
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(qv, pv, c, kE2M1, kE2M1, TQ, (int)sq, TP, (int)sp);
 }

@@ -3,11 +3,11 @@
 // +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} to v 2^-X, ties to the even code, beyond 6 to 6 (v_cvt_scalef32_pk_fp4_f32: exact,
 // since the scale is a power of two).  A block with an infinity or a NaN gets the scale 255 (NaN) and codes 0.
 //
-// Bound: HBM (with SwiGLU of bf16 rows the vector unit as well: 8192 x 7168 in 55 us, 4.8 TB/s).  A wave takes windows of
-// 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales leave as 256 and 16 consecutive
-// bytes.  Large matrices: four windows to a wave, all loaded before the first is used (one at a time: 32 KB in flight on a
-// CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3 at 18432 x 7168, 53 us; back 22.8 and
-// 48.7).
+// Bound: HBM (with SwiGLU of bf16 rows the vector unit as well: 8192 x 7168 in 55 us, 4.8 TB/s).  A wave takes
+// windows of 512 values of a row, 8 a lane: four lanes share a block, and its codes and scales leave as 256 and 16
+// consecutive bytes.  Large matrices: four windows to a wave, all loaded before the first is used (one at a time: 32
+// KB in flight on a CU, 4.1 TB/s of reads and writes; four: 5.8 at 8192 x 7168 bf16, 25.4 us, and 6.3 at 18432 x
+// 7168, 53 us; back 22.8 and 48.7).
 #include "mx4.h"
 #include "row_core.h"
 #include "tile_core.h"
@@ -41,10 +41,10 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
   return o > m ? o : m;
 }
 
-// v = swiglu_f32(gate, up) bit for bit, with a reciprocal in place of its division: the hardware's is off by a unit at
-// most, and a step of Newton's method in fused multiply-adds rounds it correctly (compared with the division for every
-// fp32 number of [1, 2^126)).  From 2^126 on (gates below -87.3), where it is subnormal, the division itself.  bf16, 8192 x
-// 7168: 55 us, with the division everywhere 66; 8192 x 2048: 16.8 and 20.5.
+// v = swiglu_f32(gate, up) bit for bit, with a reciprocal in place of its division: the hardware's is off by a unit
+// at most, and a step of Newton's method in fused multiply-adds rounds it correctly (compared with the division for
+// every fp32 number of [1, 2^126)).  From 2^126 on (gates below -87.3), where it is subnormal, the division itself.
+// bf16, 8192 x 7168: 55 us, with the division everywhere 66; 8192 x 2048: 16.8 and 20.5.
 template <class In>
 __device__ __forceinline__ void swiglu8(const Raw8<In>& gate, const Raw8<In>& up, float (&v)[8]) {
   float d[8];
@@ -247,8 +247,8 @@ struct Mx4Grid {
   }
 };
 
-// Rows of up to 256 values: several to a wave (bf16, 65536 rows of 64: 12.4 -> 3.6 us, back 11.8 -> 3.9; of 256: 12.4 -> 9.1,
-// 13.0 -> 8.4; 262144 of 128: 37.6 -> 15.4; with SwiGLU 65536 of 64: 31.5 -> 5.0).
+// Rows of up to 256 values: several to a wave (bf16, 65536 rows of 64: 12.4 -> 3.6 us, back 11.8 -> 3.9; of 256: 12.4
+// -> 9.1, 13.0 -> 8.4; 262144 of 128: 37.6 -> 15.4; with SwiGLU 65536 of 64: 5.6).
 constexpr int kMx4Short = 256;
 int short_lanes(int32_t cols) { return cols <= 64 ? 8 : cols <= 128 ? 16 : 32; }
 dim3 short_grid(int64_t rows, int lanes) {
@@ -257,7 +257,8 @@ dim3 short_grid(int64_t rows, int lanes) {
 }
 
 template <class In, bool kSwiglu>
-void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+void launch_q(const Mx4Grid& g, const void* x, int64_t rows, int32_t cols, uint8_t* codes, uint8_t* scales,
+              hipStream_t s) {
   if (cols <= kMx4Short) {
     const int lanes = short_lanes(cols);
     const auto go = [&](auto kernel) {

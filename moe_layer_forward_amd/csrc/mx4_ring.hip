@@ -1,19 +1,19 @@
 // Microscaled 4-bit products for groups of few rows: a stream of weights.
 //
 // Work item = up to 16 NB rows of one group x 64 QB columns, 16 QB to each of four waves.  A step is a window of 512
-// values: 256 bytes of every row, whole lines, which go straight to LDS, four rows an instruction: the wave's own rows of
-// weights, its quarter of the token rows, and in one more instruction the 16 bytes of scales of its weight rows and of one
-// block of token rows.  In v_mfma_scale_f32_16x16x128 number t of a step lane l multiplies block 4 (l / 16) + t of row
-// l % 16, so that one dword holds its scales, byte t for number t.  Row r keeps that block's 16 bytes at position
-// (4 t + l / 16) ^ r: the rows of one fragment read fall in different banks.
+// values: 256 bytes of every row, whole lines, which go straight to LDS, four rows an instruction: the wave's own
+// rows of weights, its quarter of the token rows, and in one more instruction the 16 bytes of scales of its weight
+// rows and of one block of token rows.  In v_mfma_scale_f32_16x16x128 number t of a step lane l multiplies block 4 (l
+// / 16) + t of row l % 16, so that one dword holds its scales, byte t for number t.  Row r keeps that block's 16
+// bytes at position (4 t + l / 16) ^ r: the rows of one fragment read fall in different banks.
 //
-// Work-groups stay, two to a CU: each takes every 64th item of its XCD's share (neighbours read neighbouring weights), and
-// the loads run ahead of the products, across the ends of items, so that the stream never stops.  One barrier a step: a
-// stage is loaded again when every wave has passed the barrier of the step after it.
+// Work-groups stay, two to a CU: each takes every 64th item of its XCD's share (neighbours read neighbouring
+// weights), and the loads run ahead of the products, across the ends of items, so that the stream never stops.  One
+// barrier a step: a stage is loaded again when every wave has passed the barrier of the step after it.
 //
-// Bound: HBM.  384 groups, 512 rows, 7168 x 2048: 328 us, 6.8 TB/s of weights (16-row x 64-byte loads into
-// registers: 480, stopping at every item).  Two work-groups of 64 columns, three stages: 346; one of 128, four: 382; 32 or
-// more rows to an item: slower than tiles wherever there are so many.
+// Bound: HBM.  384 groups, 512 rows, 7168 x 2048: 328 us, 6.8 TB/s of weights (16-row x 64-byte loads into registers:
+// 480, stopping at every item).  Two work-groups of 64 columns, three stages: 346; one of 128, four: 382; 32 or more
+// rows to an item: slower than tiles wherever there are so many.
 #include "mx4_core.h"
 
 namespace moe {
@@ -51,7 +51,8 @@ struct RingLoads {
   uint32_t nw, nx;
   uint32_t wo[4 * QB], xo[NB];
 
-  __device__ __forceinline__ static uint32_t chunk(int r) {  // which 16 bytes of a window of row r go where the lane's go
+  // which 16 bytes of a window of row r go where the lane's go
+  __device__ __forceinline__ static uint32_t chunk(int r) {
     const int c = (threadIdx.x ^ r) & 15;
     return (uint32_t)(4 * (c & 3) + (c >> 2)) * 16;
   }
@@ -106,7 +107,8 @@ struct RingLoads {
     for (int i = 0; i < NB; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (Lds)(st.x + (i * 4 + wave) * 1024), 16,
                                                chunk(4 * wave + quarter) < left ? xo[i] : kMx4Outside, 0, 0, 0);
-    if (lane < 16 * QB + 16) __builtin_amdgcn_global_load_lds(s + kb / 16, (Lds)(st.s + wave * (QB + 1) * 256), 16, 0, 0);
+    if (lane < 16 * QB + 16)
+      __builtin_amdgcn_global_load_lds(s + kb / 16, (Lds)(st.s + wave * (QB + 1) * 256), 16, 0, 0);
   }
 };
 
@@ -153,7 +155,7 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
         tiles.find(a, 16 * NB, load_item / slabs, g, beg, end);
         loads.init(a, g, beg, end, load_item % slabs, wave);
       } else {
-        loads.nw = loads.nx = 0;  // past the last item: no codes are read (its scales are), and the waits count the same
+        loads.nw = loads.nx = 0;  // past the last item no codes are read (its scales are); the waits stay the same
       }
     }
   };
@@ -220,16 +222,16 @@ __global__ __launch_bounds__(64 * kRingWaves, per) void mx4_ring_kernel(Mx4Args 
 #endif
 }
 
+int ring_slabs(const Mx4Args& a) { return (a.N + 64 * kRingQ - 1) / (64 * kRingQ); }
+
 }  // namespace
 
-int64_t mx4_ring_items(const Mx4Args& a) {
-  return gmm_max_tiles(a.max_rows, a.G, 16 * kRingP) * ((a.N + 64 * kRingQ - 1) / (64 * kRingQ));
-}
+int64_t mx4_ring_items(const Mx4Args& a) { return gmm_max_tiles(a.max_rows, a.G, 16 * kRingP) * ring_slabs(a); }
 
 hipError_t launch_mx4_ring(const Mx4Args& a, hipStream_t s) {
   const int64_t items = (mx4_ring_items(a) + kXcds - 1) / kXcds * kXcds, most = 256 * kRingPer;
   const dim3 grid((unsigned)(items < most ? items : most));
-  mx4_ring_kernel<kRingP, kRingQ, kRingPer><<<grid, 64 * kRingWaves, 0, s>>>(a, (a.N + 64 * kRingQ - 1) / (64 * kRingQ));
+  mx4_ring_kernel<kRingP, kRingQ, kRingPer><<<grid, 64 * kRingWaves, 0, s>>>(a, ring_slabs(a));
   return hipGetLastError();
 }
 

@@ -1,17 +1,17 @@
 // Grouped product of microscaled 4-bit rows and weights, operands straight from memory to registers:
 //   y[r, n] = sum over blocks b of 32: 2^(sx[i, b] + sw[g, n, b] - 254) sum_{k in b} qx[i, k] qw[g, n, k]
-// with v_mfma_scale_f32_16x16x128: lane l holds 32 values of row l % 16 of each operand, 16 bytes, which is one
-// block and its scale.  A window of 512 values is four products: lane l takes block 4 t + l / 16 in the t-th, so that
-// every load instruction reads 64 consecutive bytes of each of 16 rows, and its scale is byte l / 16 of the t-th dword of
+// with v_mfma_scale_f32_16x16x128: lane l holds 32 values of row l % 16 of each operand, 16 bytes, which is one block
+// and its scale.  A window of 512 values is four products: lane l takes block 4 t + l / 16 in the t-th, so that every
+// load instruction reads 64 consecutive bytes of each of 16 rows, and its scale is byte l / 16 of the t-th dword of
 // the window's 16 bytes.
 //
 // Work item = up to 16 PB rows of one group x 16 QB columns; the W waves of a work-group take every W-th window each
 // and join their sums in LDS, in a fixed order.  (4 or 16 waves: within 2%, and up to 30% slower.)
 //
 // Bound: the way of weights through registers: a wave holds one window of both operands and asks for the next when it
-// has multiplied this one, and many waves on a CU cover that (asking earlier takes registers from other waves: 17.3 us
-// against 13.7 with one row).  18432 x 7168 (70 MB with scales), one row: 13.7 us where the weights come from the last-level
-// cache, 16.3 from HBM; 32 rows, 7168 x 18432: 21.4 and 23.7.
+// has multiplied this one, and many waves on a CU cover that (asking earlier takes registers from other waves: 17.3
+// us against 13.7 with one row).  18432 x 7168 (70 MB with scales), one row: 13.7 us where the weights come from the
+// last-level cache, 16.3 from HBM; 32 rows, 7168 x 18432: 21.4 and 23.7.
 #include "mx4_core.h"
 
 namespace moe {
@@ -35,8 +35,10 @@ __global__ __launch_bounds__(64 * W, PB * QB >= 4 ? 2 : 4) void mx4_stream_kerne
   const uint32_t ld = (uint32_t)(a.K / 2), lds = (uint32_t)mx4_scale_cols(a.K);
   const int windows = (int)(lds / 16);
   const int64_t w0 = (int64_t)g * a.N + q0, x0 = a.row_index ? 0 : beg, xn = a.row_index ? a.x_rows : rows;
-  const Mx4Rsrc rw = mx4_rsrc(a.w + w0 * ld, (uint32_t)cols * ld), rws = mx4_rsrc(a.ws + w0 * lds, (uint32_t)cols * lds);
-  const Mx4Rsrc rx = mx4_rsrc(a.x + x0 * ld, (uint32_t)(xn * ld)), rxs = mx4_rsrc(a.xs + x0 * lds, (uint32_t)(xn * lds));
+  const Mx4Rsrc rw = mx4_rsrc(a.w + w0 * ld, (uint32_t)cols * ld);
+  const Mx4Rsrc rws = mx4_rsrc(a.ws + w0 * lds, (uint32_t)cols * lds);
+  const Mx4Rsrc rx = mx4_rsrc(a.x + x0 * ld, (uint32_t)(xn * ld));
+  const Mx4Rsrc rxs = mx4_rsrc(a.xs + x0 * lds, (uint32_t)(xn * lds));
   uint32_t wrow[QB], xrow[PB];  // rows past the end read the last one
 #pragma unroll
   for (int j = 0; j < QB; ++j) wrow[j] = (uint32_t)(16 * j + r < cols ? 16 * j + r : cols - 1);
@@ -56,13 +58,15 @@ __global__ __launch_bounds__(64 * W, PB * QB >= 4 ? 2 : 4) void mx4_stream_kerne
 #pragma unroll
     for (int j = 0; j < QB; ++j) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) w[j][t] = mx4_load128(rw, kb + 64 * t < ld ? wrow[j] * ld + kb + 64 * t : kMx4Outside);
+      for (int t = 0; t < 4; ++t)
+        w[j][t] = mx4_load128(rw, kb + 64 * t < ld ? wrow[j] * ld + kb + 64 * t : kMx4Outside);
       sw[j] = mx4_load128(rws, wrow[j] * lds + ks);
     }
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) x[i][t] = mx4_load128(rx, kb + 64 * t < ld ? xrow[i] * ld + kb + 64 * t : kMx4Outside);
+      for (int t = 0; t < 4; ++t)
+        x[i][t] = mx4_load128(rx, kb + 64 * t < ld ? xrow[i] * ld + kb + 64 * t : kMx4Outside);
       sx[i] = mx4_load128(rxs, xrow[i] * lds + ks);
     }
     __builtin_amdgcn_sched_barrier(0);  // every load of a window is in flight before the first product waits

@@ -1,20 +1,20 @@
-// Tile kernel of the microscaled 4-bit products, for groups of many rows: 256 x 256 outputs of one group and 8 waves, or
-// 128 x 128 and 4.  Operands, stages and stores as in gmm_tile.h; what differs:
-//   * A step is 128 bytes of a row, 256 values, 8 blocks; one 16-byte fragment of a lane is one block, and its scale goes
-//     to the matrix instruction (v_mfma_scale_f32_16x16x128) as a byte of a register.  Lane l multiplies blocks 2 (l / 16)
-//     and 2 (l / 16) + 1 of a step, so that one 2-byte read brings both scales; in LDS they sit where the
+// Tile kernel of the microscaled 4-bit products, for groups of many rows: 256 x 256 outputs of one group and 8 waves,
+// or 128 x 128 and 4.  Operands, stages and stores as in gmm_tile.h; what differs:
+//   * A step is 128 bytes of a row, 256 values, 8 blocks; one 16-byte fragment of a lane is one block, and its scale
+//     goes to the matrix instruction (v_mfma_scale_f32_16x16x128) as a byte of a register.  Lane l multiplies blocks
+//     2 (l / 16) and 2 (l / 16) + 1 of a step, so that one 2-byte read brings both scales; in LDS they sit where the
 //     fragment reads of gmm_core.h expect the step's chunks l / 16 and 4 + l / 16.
-//   * Scales go to LDS too, a window of four steps (32 bytes of every row) at a time, two load instructions per wave, and
-//     every lane's 2-byte reads pick its blocks.  Those bytes cost the memory path whole lines, a quarter of what the
-//     codes cost (a half with windows of two steps: 64 groups of 256 rows, 2048 x 7168: 161 -> 157 us; 48 of 21 to 2118:
-//     133 -> 128).  Large products therefore have their scales packed first (mx4_pack_kernel): for every tile and pair
-//     of steps in the order of the reads, so that a load is 1 KiB of consecutive bytes and one 16-byte and one 8-byte
-//     read bring a lane all scales of a step.
+//   * Scales go to LDS too, a window of four steps (32 bytes of every row) at a time, two load instructions per wave,
+//     and every lane's 2-byte reads pick its blocks.  Those bytes cost the memory path whole lines, a quarter of what
+//     the codes cost (a half with windows of two steps: 64 groups of 256 rows, 2048 x 7168: 161 -> 157 us; 48 of 21
+//     to 2118: 133 -> 128).  Large products therefore have their scales packed first (mx4_pack_kernel): for every
+//     tile and pair of steps in the order of the reads, so that a load is 1 KiB of consecutive bytes and one 16-byte
+//     and one 8-byte read bring a lane all scales of a step.
 //   * LDS holds two steps of both operands and two windows of scales: 160 KiB (80 KiB, two work-groups to a CU).
-// What bounds it: 8192 x 18432 x 7168 takes 470 to 490 us, 1.6 a step of a work-group: the matrix instructions 1.3 (6.4 POP/s, what
-// they reach from registers on random data, by power; 0.85 by their clocks), LDS about 1.4 (64 KiB written at 64 bytes a
-// clock, 192 read at 128), the loads alone 0.7.  The same step with weights of its own for every work-group, 64 groups of
-// 256 rows: 2.6.
+// What bounds it: 8192 x 18432 x 7168 takes 470 to 490 us, 1.6 a step of a work-group: the matrix instructions 1.3
+// (6.4 POP/s, what they reach from registers on random data, by power; 0.85 by their clocks), LDS about 1.4 (64 KiB
+// written at 64 bytes a clock, 192 read at 128), the loads alone 0.7.  The same step with weights of its own for
+// every work-group, 64 groups of 256 rows: 2.6.
 #include "gmm_tile.h"
 #include "mx4_core.h"
 
@@ -65,9 +65,9 @@ template <int W>
 constexpr int kMx4WindowScales = 4 * kMx4PairScales<W>;
 constexpr int kMx4ScaleLoads = 2;  // instructions of a window
 
-// The scales of a window, P's rows and then Q's, 64 rows a wave.  Not packed: 32 rows an instruction, the two chunks of a
-// row in lanes side by side (in the other order in every second 8 rows, for the banks of the reads).  Packed: one pair of
-// steps an instruction.
+// The scales of a window, P's rows and then Q's, 64 rows a wave.  Not packed: 32 rows an instruction, the two chunks
+// of a row in lanes side by side (in the other order in every second 8 rows, for the banks of the reads).  Packed:
+// one pair of steps an instruction.
 template <int W, bool kPacked>
 struct Mx4LoadScales {
   const char* base;  // of the wave's operand, uniform
@@ -180,13 +180,13 @@ __device__ __forceinline__ void mx4_read_first(char* const (&p)[2], const char* 
 //   at its end: P1(kt + 2), and in a window's last step, when the next one's first scales have been read (the compiler
 //     lets no read of the scales' array pass while a load into it is in flight), the scales of window (kt + 5) / 4,
 //     whose slot the step's own scales have left
-// The middle waits for P1(kt), behind which P0(kt + 1), Q(kt + 1) and P1(kt + 1) may be in flight; the end for P0(kt + 1)
-// and Q(kt + 1), behind which P1(kt + 1), P0(kt + 2) and Q(kt + 2) may be; in a window's first step the scales, too.
-// `next`: the window of step kt + 1.
+// The middle waits for P1(kt), behind which P0(kt + 1), Q(kt + 1) and P1(kt + 1) may be in flight; the end for P0(kt
+// + 1) and Q(kt + 1), behind which P1(kt + 1), P0(kt + 2) and Q(kt + 2) may be; in a window's first step the scales,
+// too. `next`: the window of step kt + 1.
 template <int W, int NB, int D, class LoadP, class LoadQ, class LoadS, class FP, class FQ, class Scales>
 __device__ __forceinline__ void mx4_step(const LoadP (&lp)[2], const LoadQ& lq, const LoadS& ls, int kt,
-                                         const Mx4Rings& r, char* next, const FP& fp, const FQ& fq, const Scales& sc, int wave,
-                                         Mx4Carry<NB>& c, f32x4 (&acc)[NB][4]) {
+                                         const Mx4Rings& r, char* next, const FP& fp, const FQ& fq, const Scales& sc,
+                                         int wave, Mx4Carry<NB>& c, f32x4 (&acc)[NB][4]) {
   using O = GmmOrder<W, NB>;
   constexpr int n0 = O::kLoads0, n1 = O::kLoads1;
   constexpr int NF = 2 * NB, kMid = 2 * O::kH0 - 2;
@@ -302,7 +302,8 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& a, const Mx4Rings& 
   Mx4Load<W, kGmmPLoads> lp[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    lp[h].init(a.x + x0 * ld, (uint32_t)(xn * ld), ld, wave, [&](int rl) { return x_row(rl + h * 32 * GmmOrder<W, NB>::kH0); });
+    lp[h].init(a.x + x0 * ld, (uint32_t)(xn * ld), ld, wave,
+               [&](int rl) { return x_row(rl + h * 32 * GmmOrder<W, NB>::kH0); });
   Mx4Load<W, kGmmQLoads, kNt> lq;
   lq.init(a.w + w0 * ld, (uint32_t)cols * ld, ld, wave, w_row);
   Mx4LoadScales<W, kPacked> ls;
@@ -336,7 +337,8 @@ __device__ __forceinline__ void mx4_tile_body(const Mx4Args& a, const Mx4Rings& 
   o.ld = a.N;
   o.rows = rows;
   o.cols = cols;
-  const GmmRings stage{{{rings.p[0][0], rings.p[0][1]}, {rings.p[1][0], rings.p[1][1]}}, {rings.q[0], rings.q[1], nullptr}};
+  const GmmRings stage{{{rings.p[0][0], rings.p[0][1]}, {rings.p[1][0], rings.p[1][1]}},
+                       {rings.q[0], rings.q[1], nullptr}};
   gmm_store<W, NB>(o, stage, wr, wc, [&](int i, int s, int j, int, int) { return acc[i][s][j]; });
 }
 
@@ -360,7 +362,8 @@ __device__ __forceinline__ bool mx4_row_item(int64_t b, const GmmTiles& t, int s
 }
 
 template <int W, bool kPacked, bool kNt>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void mx4_tile_kernel(Mx4Args a, int slabs) {
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void mx4_tile_kernel(Mx4Args a, int slabs) {
   using S = GmmShape<W>;
   __shared__ __align__(16) char p00_[S::kPStage], p01_[S::kPStage], p10_[S::kPStage], p11_[S::kPStage], q0_[S::kQStage],
       q1_[S::kQStage], s_[2 * kMx4WindowScales<W>];
@@ -371,11 +374,12 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   Mx4Tiles tiles;
   tiles.count(a, S::kTile);
   if (!mx4_row_item(gmm_block(), tiles.t, slabs, t, slab)) return;
-  if (kPacked && t >= gmm_max_tiles(a.max_rows, a.G, S::kTile)) return;  // offsets that overlap: no place among the packed
+  // offsets that overlap: no place among the packed
+  if (kPacked && t >= gmm_max_tiles(a.max_rows, a.G, S::kTile)) return;
   tiles.find(a, S::kTile, t, g, beg, end);
   if (beg >= end) return;  // the same: more tiles than were counted
-  // P blocks per wave.  Two at least: with one the loop has one meeting a step, which waits for all that is in flight (32
-  // rows, 18432 x 7168: 17.9 us, with two 15.3).
+  // P blocks per wave.  Two at least: with one the loop has one meeting a step, which waits for all that is in flight
+  // (32 rows, 18432 x 7168: 17.9 us, with two 15.3).
   const int nb = end - beg > 32 ? (int)(end - beg + 31) / 32 : 2;
 #define MOE_MX4_CASE(N) \
   if constexpr (N <= W) \
@@ -403,8 +407,8 @@ __global__ __launch_bounds__(32 * W) void mx4_pack_kernel(Mx4Args a, int slabs, 
   const int64_t places = gmm_max_tiles(a.max_rows, a.G, kTile), at = gmm_block();
   const int lds = mx4_scale_cols(a.K), pairs = lds / 16, rl = threadIdx.x, r = rl & 15;
   const uint8_t* row;
-  int place;  // of the lane that reads this row's first block (l / 16 = 0), in units of 2 bytes, and from block to block
-  constexpr int kPart = 16;
+  int place;                 // of the lane that reads this row's first block (l / 16 = 0), in units of 2 bytes,
+  constexpr int kPart = 16;  // and from block to block
   int per;    // 2-byte scales of a lane
   if (at < places) {
     Mx4Tiles tiles;

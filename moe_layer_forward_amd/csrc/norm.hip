@@ -5,10 +5,10 @@
 // moe_quantize_rows (row_core.h).
 //
 // Bound: HBM, each value moved once.  A row stays in the registers of the lanes that share it (64, 256 or 1024 of
-// them, chunks of 8 values a lane; 16 where rows are short), from its one load to its last use; every load of a row is issued before the first is
-// waited for.  bf16, 7168 columns, with a residual: 8192 rows 77 us (470 MB, 6.1 TB/s; a copy reaches 5.2, reads alone
-// 7.0), in 8 bits 72 (5.7), the gradients of 16384 rows 155 and the join 7 (940 MB, 6.1).  Few rows: the latency of a
-// load, two joins over the lanes and a store, 2.8 us for one row, 3.9 for 64.
+// them, chunks of 8 values a lane; 16 where rows are short), from its one load to its last use; every load of a row
+// is issued before the first is waited for.  bf16, 7168 columns, with a residual: 8192 rows 77 us (470 MB, 6.1 TB/s;
+// a copy reaches 5.2, reads alone 7.0), in 8 bits 72 (5.7), the gradients of 16384 rows 155 and the join 7 (940 MB,
+// 6.1).  Few rows: the latency of a load, two joins over the lanes and a store, 2.8 us for one row, 3.9 for 64.
 #include "norm.h"
 #include "row_core.h"
 
@@ -173,10 +173,10 @@ __global__ __launch_bounds__(norm_threads(kLanes)) void rms_norm_kernel(NormArgs
   }
 }
 
-// Rows r, r + gridDim.x * kRows, ... of a work-group's kRows sets of kLanes lanes; dw of its rows stays in
-// registers and leaves once, as row blockIdx.x of part.  kHold: so do the weights, and dh is read ahead; without, both are
-// read where they are used (the weights twice a row, from the cache), for rows that leave no registers for them.
-// D: the type of dy.
+// Rows r, r + gridDim.x * kRows, ... of a work-group's kRows sets of kLanes lanes; dw of its rows stays in registers
+// and leaves once, as row blockIdx.x of part.  kHold: so do the weights, and dh is read ahead; without, both are read
+// where they are used (the weights twice a row, from the cache), for rows that leave no registers for them.  D: the
+// type of dy.
 template <class T, class D, int kLanes, int kChunks, bool kHold, bool kNt>
 __global__ __launch_bounds__(norm_threads(kLanes), 2) void norm_grad_kernel(NormGradArgs a) {
   constexpr int kRows = norm_threads(kLanes) / kLanes;
@@ -356,13 +356,15 @@ __global__ __launch_bounds__(kJoinThreads) void norm_grad_join_kernel(const floa
 // its share.  The norm of few rows: more lanes, for a shorter way through each (64 rows of 2048: 4.3 us with 64
 // lanes, 3.3 with 256; of 7168: 4.5 with 256, 3.9 with 1024; 1024 rows of 7168: 10.8 and 14.3).
 int lanes_of(int32_t cols) { return cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024; }
-// Short rows (those of heads, say): 16 lanes, four rows to a wave, where there are many of them (bf16, 262144 rows of 128,
-// 16 and 64 lanes: 23.6 us and 64.8, with 8-bit output 27 and 92; of 512: 85 and 111, 66 and 110; fp32 of 512: 183 and 183,
-// 118 and 150; 600 rows of 512: 3.5 and 3.1; 4096 of 512 with a residual: 5.6 and 4.8, of 256 4.2 and 4.2).
+// Short rows (those of heads, say): 16 lanes, four rows to a wave, where there are many of them (bf16, 262144 rows of
+// 128, 16 and 64 lanes: 23.6 us and 64.8, with 8-bit output 27 and 92; of 512: 85 and 111, 66 and 110; fp32 of 512:
+// 183 and 183, 118 and 150; 600 rows of 512: 3.5 and 3.1; 4096 of 512 with a residual: 5.6 and 4.8, of 256 4.2 and
+// 4.2).
 bool short_rows(int64_t rows, int32_t cols) { return cols <= 512 && rows > (cols <= 256 ? 512 : 8192); }
-// Gradients, both launches, 16 and 64 lanes, bf16: 262144 rows of 128 45 us and 146, of 512 135 and 193; 8192 of 512 13.2
-// and 14.4; 520 of 512 6.6 and 6.8.  fp32: 262144 rows of 256 147 and 184; 4096 of 512 11.3 and 13.0; 64 where both are
-// many: 8192 of 512 18.2 and 17.4, 262144 308 and 293, of 400 250 and 234; of 384 and less either by up to 5%.
+// Gradients, both launches, 16 and 64 lanes, bf16: 262144 rows of 128 45 us and 146, of 512 135 and 193; 8192 of 512
+// 13.2 and 14.4; 520 of 512 6.6 and 6.8.  fp32: 262144 rows of 256 147 and 184; 4096 of 512 11.3 and 13.0; 64 where
+// both are many: 8192 of 512 18.2 and 17.4, 262144 308 and 293, of 400 250 and 234; of 384 and less either by up to
+// 5%.
 int grad_lanes(int64_t rows, int32_t cols, bool bf16) {
   const bool narrow = cols <= 512 && rows > 512;
   return narrow && (bf16 || cols <= 384 || rows < 8192) ? 16 : lanes_of(cols);
@@ -426,9 +428,9 @@ hipError_t launch_rms_norm(const NormArgs& a, NormOut out, hipStream_t s) {
                                  : launch_norm<float, float>(a, s);
 }
 
-// As many work-groups as run at once, two on a CU or one of 1024 lanes: more write more sums and gain nothing (32768 rows of
-// 1024: 49 us with 512, 59 with 1024; 2048 of 16384: 79 with 256, 89 with 512).  The same for either type: from 8192 rows on
-// 16 lanes to a row make as many of them as 64.
+// As many work-groups as run at once, two on a CU or one of 1024 lanes: more write more sums and gain nothing (32768
+// rows of 1024: 49 us with 512, 59 with 1024; 2048 of 16384: 79 with 256, 89 with 512).  The same for either type:
+// from 8192 rows on 16 lanes to a row make as many of them as 64.
 int norm_grad_parts(int64_t rows, int32_t cols) {
   const int lanes = grad_lanes(rows, cols, true), per = norm_threads(lanes) / lanes;
   const int64_t most = lanes == 1024 ? 256 : 512, groups = (rows + per - 1) / per;

@@ -12,10 +12,11 @@
 
 namespace moe {
 
-// bf16 matrices from this size on are read, and written where nothing reads them next, with the non-temporal policy: they
-// leave the last-level cache (256 MB) to others, and the stores do not wait for lines.  Norm, gradients: 56 MB 43.8 ->
-// 42.7 us, 48.7 -> 52.8; 82 MB 66.7 -> 59.7, 76.2 -> 70.1; 224 MB 167 -> 160, 185 -> 168; 8192 x 7168 to 4-bit codes 28 ->
-// 26, back 31 -> 24.  Not fp32, where a lane's 32 bytes are two halves of other lanes' lines: 128 MB 99 -> 108.
+// bf16 matrices from this size on are read, and written where nothing reads them next, with the non-temporal policy:
+// they leave the last-level cache (256 MB) to others, and the stores do not wait for lines.  Norm, gradients: 56 MB
+// 43.8 -> 42.7 us, 48.7 -> 52.8; 82 MB 66.7 -> 59.7, 76.2 -> 70.1; 224 MB 167 -> 160, 185 -> 168; 8192 x 7168 to
+// 4-bit codes 28 -> 26, back 31 -> 24.  Not fp32, where a lane's 32 bytes are two halves of other lanes' lines: 128
+// MB 99 -> 108.
 constexpr int64_t kStreamBytes = 72 << 20;
 template <class T>
 inline bool row_streams(int64_t values) {
